@@ -10,7 +10,9 @@ Entry points (same names as the C ABI): ``moe_align``,
 ``moe_grouped_gate_up_silu``, ``moe_grouped_down``, ``moe_blend``,
 ``moe_layer_forward`` (via :class:`MoeLayer`), ``moe_layer_workspace_bytes``,
 ``moe_align_max_total``, ``moe_active_cap``, ``moe_tile_weights``,
-``moe_tiled_weight_bytes``, ``moe_align_gate_up_silu``.
+``moe_tiled_weight_bytes``, ``moe_align_gate_up_silu``.  The operators around
+the layer (norm, rows by expert, expert products, gradients) are in
+:mod:`.ops` and importable from here under their C names.
 
 Weights are passed as ``(w, scale)`` pairs: ``w`` is ``[E, N, K]``
 ``torch.uint8`` e4m3fn codes with ``scale`` float32 ``[E, N/128, K/128]`` (one
@@ -513,3 +515,16 @@ def moe_layer_workspace_bytes(layer: MoeLayer, M: int, idt: int = MOE_IDX_I64) -
 
 def moe_layer_forward(layer: MoeLayer, x, topk_ids, topk_weights, out=None, workspace=None, stream=None):
     return layer.forward(x, topk_ids, topk_weights, out, workspace, stream)
+
+
+from .ops import (  # noqa: E402,F401
+    moe_add_rms_norm,
+    moe_add_rms_norm_backward,
+    moe_grouped_act_backward,
+    moe_grouped_linear,
+    moe_grouped_linear_backward_w,
+    moe_grouped_linear_backward_x,
+    moe_permute,
+    moe_unpermute,
+    moe_unpermute_backward,
+)

@@ -1,4 +1,5 @@
-"""ctypes declarations of libmoe_mi355x.so (include/moe_mi355x.h)."""
+"""ctypes declarations of libmoe_mi355x.so (include/moe_mi355x.h and
+include/moe_mi355x_ops.h)."""
 
 from __future__ import annotations
 
@@ -105,6 +106,51 @@ SIGNATURES = {
     "moe_layer_forward_noalloc": (c_int, [P(MoeLayerDesc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
 }
 
+# ---- include/moe_mi355x_ops.h: the operators around the layer
+MOE_DT_BF16 = 0
+MOE_DT_F32 = 1
+MOE_DT_E4M3 = 2
+MOE_ACT_NONE = 0
+MOE_ACT_SILU = 1
+MOE_ACT_GELU = 2
+MOE_ACT_SWIGLU = 3
+MOE_NORM_MAX_H = 32768
+
+c_float = ctypes.c_float
+
+
+class MoeLinearDesc(ctypes.Structure):
+    _fields_ = [
+        ("rows", c_int64), ("E", c_int32), ("N", c_int32), ("K", c_int32), ("wdt", c_int), ("act", c_int),
+        ("ydt", c_int), ("expert_offsets", c_void_p), ("expert_counts", c_void_p), ("x", c_void_p),
+        ("x_scale", c_void_p), ("w", MoeWeight), ("up", MoeWeight), ("bias", c_void_p), ("up_bias", c_void_p),
+        ("residual", c_void_p), ("y", c_void_p), ("y_scale", c_void_p), ("preact", c_void_p),
+    ]
+
+
+OPS_SIGNATURES = {
+    "moe_ops_abi_version": (c_int32, []),
+    "moe_add_rms_norm": (c_int, [c_void_p, c_int64, c_void_p, c_int, c_void_p, c_void_p, c_float, c_void_p, c_int,
+                                 c_void_p, c_void_p, c_int64, c_int32, c_void_p]),
+    "moe_add_rms_norm_backward_workspace_bytes": (c_size_t, [c_int64, c_int32]),
+    "moe_add_rms_norm_backward": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                          c_int64, c_int32, c_void_p, c_size_t, c_void_p]),
+    "moe_permute": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_int64, c_int32, c_int32, c_void_p, c_void_p,
+                            c_int64, c_void_p]),
+    "moe_unpermute": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int32, c_int32, c_void_p, c_int64, c_void_p]),
+    "moe_unpermute_backward": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int32, c_int32, c_void_p,
+                                       c_void_p, c_int64, c_void_p]),
+    "moe_grouped_linear": (c_int, [P(MoeLinearDesc), c_void_p]),
+    "moe_grouped_act_backward": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int64, c_int32, c_int32,
+                                         c_void_p, c_void_p]),
+    "moe_grouped_linear_backward_x": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int32,
+                                              c_int32, c_int32, c_void_p, c_void_p]),
+    "moe_grouped_linear_backward_w_workspace_bytes": (c_size_t, [c_int64, c_int32, c_int32, c_int32, c_int32, c_int32]),
+    "moe_grouped_linear_backward_w": (c_int, [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int32,
+                                              c_int32, c_int32, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                                              c_void_p, c_size_t, c_void_p]),
+}
+
 _LIB = None
 
 
@@ -117,7 +163,7 @@ def load() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing: build it first "
                 "(python -m mixture_experts_routing_align_amd.build, or __graft_entry__.build())")
         lib = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **OPS_SIGNATURES}.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args

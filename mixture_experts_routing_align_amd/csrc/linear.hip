@@ -1,0 +1,597 @@
+// The experts' matrix products over sorted rows for gfx950: forward with bias,
+// activation, residual and 8-bit rows in the epilogue, and both gradients.
+//
+//   forward      z[p] = W[e] x[p] + b[e], y[p] = act(z[p]) + residual[p]
+//   backward x   dx[p] = sum_n dz[p, n] W[e][n, :]
+//   backward w   dW[e][n, :] = sum_p dz[p, n] x[p, :], db[e][n] = sum_p dz[p, n]
+//
+// All three are one tiled product on the matrix cores that differs in how its
+// operands lie in memory (linear_tile.h).
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "linear_tile.h"
+#include "moe_internal.h"
+#include "moe_mi355x_ops.h"
+#include "row_common.h"
+
+namespace moe {
+namespace {
+
+using namespace tile;
+using row::pack_bf16;
+
+extern __shared__ __attribute__((aligned(1024))) char smem[];
+
+__device__ __forceinline__ float silu(float z) { return z / (1.0f + expf(-z)); }
+__device__ __forceinline__ float gelu_tanh_arg(float z) { return 0.7978845608028654f * fmaf(0.044715f * z * z, z, z); }
+__device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.0f + tanhf(gelu_tanh_arg(z))); }
+
+__device__ __forceinline__ void unpack4(uint2 v, float (&f)[4]) {
+  f[0] = row::bf16_lo(v.x);
+  f[1] = row::bf16_hi(v.x);
+  f[2] = row::bf16_lo(v.y);
+  f[3] = row::bf16_hi(v.y);
+}
+__device__ __forceinline__ uint2 pack4(const float (&f)[4]) { return make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])); }
+
+// ---------------------------------------------------------------- forward --
+
+// A workgroup's tile: BQ rows by BP weight rows (SwiGLU: BP / 2 of the gate and
+// the same BP / 2 of the up weight, so that a lane holds z and u of its elements),
+// WQ x WP waves, DB bytes of depth per stage, STAGES stages in LDS.
+template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int STAGES>
+struct Forward {
+  static constexpr int kWaves = WQ * WP, kThreads = kWaves * 64;
+  static constexpr int kParts = GATED ? 2 : 1;
+  static constexpr int kCols = BP / kParts;      // output columns of a tile
+  static constexpr int kQ = BQ / WQ / 16;        // 16-row subtiles per wave
+  static constexpr int kP = BP / WP / 16;        // 16-column subtiles per wave, all parts
+  static constexpr int kC = kP / kParts;         // of them per part
+  using QTile = RowTile<BQ, DB, kWaves>;
+  using PTile = RowTile<kCols, DB, kWaves>;
+  static constexpr int kStage = QTile::kBytes + kParts * PTile::kBytes;
+  static constexpr int kLoads = QTile::kLoads + kParts * PTile::kLoads;
+  static constexpr int kLds = kStage * STAGES;
+};
+
+template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int STAGES>
+__global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
+  using T = Forward<FP8, GATED, BQ, BP, WQ, WP, DB, STAGES>;
+  constexpr int kQ = T::kQ, kP = T::kP, kC = T::kC, kParts = T::kParts, kCols = T::kCols;
+  static_assert(!FP8 || DB == row::kScaleBlock, "a stage of 8-bit depth is one scale block");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wq = wave / WP, wp = wave % WP;
+  const Item it = find_item(a, blockIdx.x, BQ, (a.N + kCols - 1) / kCols);
+  if (it.e < 0) return;
+  const int ld = FP8 ? a.K : a.K * 2;
+  const int q0 = it.tq * BQ, p0 = it.tp * kCols;
+  const int64_t first = (int64_t)it.row0 + q0;
+  const __amdgpu_buffer_rsrc_t rx = resource(static_cast<const char*>(a.x) + first * ld);
+  const int64_t expert = (int64_t)it.e * a.N * ld;
+  __amdgpu_buffer_rsrc_t rw[kParts];
+#pragma unroll
+  for (int h = 0; h < kParts; ++h) rw[h] = resource(static_cast<const char*>(a.w[h]) + expert);
+
+  typename T::QTile qt;
+  typename T::PTile pt;
+  qt.init(wave, lane, [&](int r) { return q0 + r < it.count ? (uint32_t)(r * ld) : kNoFetch; });
+  pt.init(wave, lane, [&](int r) { return p0 + r < a.N ? (uint32_t)((p0 + r) * ld) : kNoFetch; });
+  const int steps = (ld + DB - 1) / DB;
+  auto issue = [&](int s, int stage) {
+    char* b = smem + stage * T::kStage;
+    const int left = ld - s * DB;  // not positive past the last step: zeros
+    qt.load(rx, b, wave, s * DB, left);
+#pragma unroll
+    for (int h = 0; h < kParts; ++h) pt.load(rw[h], b + T::QTile::kBytes + h * T::PTile::kBytes, wave, s * DB, left);
+  };
+
+  f32x4 acc[kQ][kP];
+#pragma unroll
+  for (int i = 0; i < kQ; ++i)
+#pragma unroll
+    for (int j = 0; j < kP; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // 8-bit: this lane's row scales of the step at hand and of the next one
+  const int blocks = a.K / row::kScaleBlock;
+  const float* sx[kQ];
+  float sc[kQ], sn[kQ];
+  const float* sw[kParts];
+  if constexpr (FP8) {
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) {
+      const int m = min(q0 + wq * (BQ / WQ) + i * 16 + (lane & 15), it.count - 1);
+      sx[i] = a.x_scale + ((int64_t)it.row0 + m) * blocks;
+      sn[i] = sx[i][0];
+    }
+    static_assert(kCols / WP <= row::kScaleBlock && row::kScaleBlock % (kCols / WP) == 0, "a wave's columns share a scale");
+    const int nb = a.N / row::kScaleBlock;
+    const int cb = min((p0 + wp * (kCols / WP)) / row::kScaleBlock, nb - 1);
+#pragma unroll
+    for (int h = 0; h < kParts; ++h) sw[h] = a.ws[h] + ((int64_t)it.e * nb + cb) * blocks;
+  }
+
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
+  int stage = 0;
+  for (int s = 0; s < steps; ++s) {
+    wait_and_meet<(STAGES - 2) * T::kLoads>();
+    float swc[kParts];
+    if constexpr (FP8) {
+      const int nx = min(s + 1, steps - 1);
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) {
+        sc[i] = sn[i];
+        sn[i] = sx[i][nx];
+      }
+#pragma unroll
+      for (int h = 0; h < kParts; ++h) swc[h] = sw[h][s];
+    }
+    issue(s + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+    const char* b = smem + stage * T::kStage;
+    const char* pb = b + T::QTile::kBytes;
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
+    auto p_row = [&](int j) { return wp * (kCols / WP) + (j % kC) * 16; };
+    if constexpr (FP8) {
+      i32x8 q[kQ];
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) q[i] = T::QTile::frag8(b, wq * (BQ / WQ) + i * 16, lane);
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        const i32x8 p = T::PTile::frag8(pb + j / kC * T::PTile::kBytes, p_row(j), lane);
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) {
+          // one scale block of depth in one instruction, scaled as it is added
+          const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q[i], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
+          const float f = sc[i] * swc[j / kC];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(t[c], f, acc[i][j][c]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < DB / 64; ++kk) {
+        bf16x8 q[kQ], p[kP];
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) q[i] = T::QTile::frag(b, wq * (BQ / WQ) + i * 16, kk, lane);
+#pragma unroll
+        for (int j = 0; j < kP; ++j) p[j] = T::PTile::frag(pb + j / kC * T::PTile::kBytes, p_row(j), kk, lane);
+#pragma unroll
+        for (int j = 0; j < kP; ++j)
+#pragma unroll
+          for (int i = 0; i < kQ; ++i) acc[i][j] = mma::mfma(p[j], q[i], acc[i][j]);
+      }
+    }
+  }
+  wait_and_meet<0>();  // the loads past the last step have landed: LDS is free
+
+  // Epilogue: lane l holds row l % 16 and 4 consecutive columns of each subtile.
+  const int quad = lane >> 4;
+  const int colw = p0 + wp * (kCols / WP) + quad * 4;
+  float* red = reinterpret_cast<float*>(smem);  // [WP][BQ] absolute maxima
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) {
+    const int m = wq * (BQ / WQ) + i * 16 + (lane & 15);
+    const bool live = q0 + m < it.count;
+    const int64_t r = first + m;
+    uint32_t mx = 0;
+#pragma unroll
+    for (int j = 0; j < kC; ++j) {
+      const int n = colw + j * 16;
+      const bool in = live && n < a.N;
+      float z[4], y[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) z[c] = acc[i][j][c];
+      if (a.bias[0] != nullptr && in) {
+        float f[4];
+        unpack4(*reinterpret_cast<const uint2*>(a.bias[0] + (int64_t)it.e * a.N + n), f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) z[c] += f[c];
+      }
+      if constexpr (GATED) {
+        float u[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) u[c] = acc[i][kC + j][c];
+        if (a.bias[1] != nullptr && in) {
+          float f[4];
+          unpack4(*reinterpret_cast<const uint2*>(a.bias[1] + (int64_t)it.e * a.N + n), f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) u[c] += f[c];
+        }
+        if (a.preact != nullptr && in) {
+          *reinterpret_cast<uint2*>(a.preact + r * 2 * a.N + n) = pack4(z);
+          *reinterpret_cast<uint2*>(a.preact + r * 2 * a.N + a.N + n) = pack4(u);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = silu(z[c]) * u[c];
+      } else {
+        if (a.preact != nullptr && in) *reinterpret_cast<uint2*>(a.preact + r * a.N + n) = pack4(z);
+        if (a.act == MOE_ACT_SILU) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) y[c] = silu(z[c]);
+        } else if (a.act == MOE_ACT_GELU) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) y[c] = gelu(z[c]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) y[c] = z[c];
+        }
+      }
+      if (a.residual != nullptr && in) {
+        float f[4];
+        unpack4(*reinterpret_cast<const uint2*>(a.residual + r * a.N + n), f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] += f[c];
+      }
+      if (a.y_scale == nullptr) {
+        if (in) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + r * a.N + n) = pack4(y);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          acc[i][j][c] = y[c];
+          mx = max(mx, row::abs_bits(y[c]));
+        }
+      }
+    }
+    if (a.y_scale != nullptr) {
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
+      if (lane < 16) red[wp * BQ + m] = __uint_as_float(mx);
+    }
+  }
+  if (a.y_scale == nullptr) return;
+  // 8-bit rows: the tile's columns come in whole scale blocks, each spread over
+  // the waves that hold its columns
+  constexpr int kShare = row::kScaleBlock * WP / kCols;  // waves per block
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) {
+    const int m = wq * (BQ / WQ) + i * 16 + (lane & 15);
+    const bool live = q0 + m < it.count;
+    const int64_t r = first + m;
+    uint32_t mx = 0;
+#pragma unroll
+    for (int w = 0; w < kShare; ++w) mx = max(mx, __float_as_uint(red[(wp / kShare * kShare + w) * BQ + m]));
+    const float scale = row::block_scale(mx);
+    if (!live) continue;
+#pragma unroll
+    for (int j = 0; j < kC; ++j) {
+      const int n = colw + j * 16;
+      if (n >= a.N) continue;
+      uint32_t code = __builtin_amdgcn_cvt_pk_fp8_f32(acc[i][j][0] / scale, acc[i][j][1] / scale, 0, false);
+      code = __builtin_amdgcn_cvt_pk_fp8_f32(acc[i][j][2] / scale, acc[i][j][3] / scale, code, true);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + r * a.N + n) = code;
+      if (n % row::kScaleBlock == 0) a.y_scale[r * (a.N / row::kScaleBlock) + n / row::kScaleBlock] = scale;
+    }
+  }
+}
+
+// ------------------------------------------------------------- backward x --
+
+template <int BQ, int BP, int WQ, int WP, int STAGES>
+__global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_x_kernel(LinearArgs a) {
+  constexpr int kWaves = WQ * WP, kQ = BQ / WQ / 16, kP = BP / WP / 16, kD = 64;
+  using QTile = RowTile<BQ, kD * 2, kWaves>;
+  using PTile = DepthTile<BP, kD, kWaves>;
+  constexpr int kStage = QTile::kBytes + PTile::kBytes, kLoads = QTile::kLoads + PTile::kLoads;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wq = wave / WP, wp = wave % WP;
+  const Item it = find_item(a, blockIdx.x, BQ, (a.K + BP - 1) / BP);
+  if (it.e < 0) return;
+  const int q0 = it.tq * BQ, p0 = it.tp * BP;
+  const int64_t first = (int64_t)it.row0 + q0;
+  const int ldq = a.parts * a.N * 2, ldp = a.K * 2;
+  const char* dz = static_cast<const char*>(a.dz) + first * ldq;
+  const int64_t expert = (int64_t)it.e * a.N * ldp + p0 * 2;
+  QTile qt;
+  PTile pt;
+  qt.init(wave, lane, [&](int r) { return q0 + r < it.count ? (uint32_t)(r * ldq) : kNoFetch; });
+  pt.init(wave, lane, ldp, [&](int g) { return p0 + g * 8 < a.K ? (uint32_t)(g * 16) : kNoFetch; });
+  // the depth runs over the N columns of dz's first part, then of its second
+  const int per = (a.N + kD - 1) / kD, steps = per * a.parts;
+  const __amdgpu_buffer_rsrc_t rq = resource(dz);
+  auto issue = [&](int s, int stage) {
+    char* b = smem + stage * kStage;
+    const int h = s >= per ? 1 : 0, k = s - h * per;
+    const int left = s < steps ? a.N - k * kD : 0;
+    qt.load(rq, b, wave, (h * a.N + k * kD) * 2, left * 2);
+    pt.load(resource(static_cast<const char*>(a.w[s < steps ? h : 0]) + expert + (int64_t)k * kD * ldp), b + QTile::kBytes,
+            wave, 0, left);
+  };
+  f32x4 acc[kQ][kP];
+#pragma unroll
+  for (int i = 0; i < kQ; ++i)
+#pragma unroll
+    for (int j = 0; j < kP; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
+  int stage = 0;
+  for (int s = 0; s < steps; ++s) {
+    wait_and_meet<(STAGES - 2) * kLoads>();
+    issue(s + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+    const char* b = smem + stage * kStage;
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
+#pragma unroll
+    for (int kk = 0; kk < kD / 32; ++kk) {
+      bf16x8 q[kQ], p[kP];
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) q[i] = QTile::frag(b, wq * (BQ / WQ) + i * 16, kk, lane);
+#pragma unroll
+      for (int j = 0; j < kP; ++j) p[j] = PTile::frag(b + QTile::kBytes, wp * (BP / WP) + j * 16, kk, lane);
+#pragma unroll
+      for (int j = 0; j < kP; ++j)
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) acc[i][j] = mma::mfma(p[j], q[i], acc[i][j]);
+    }
+  }
+  wait_and_meet<0>();
+  uint16_t* dx = static_cast<uint16_t*>(a.y);
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) {
+    const int m = wq * (BQ / WQ) + i * 16 + (lane & 15);
+    if (q0 + m >= it.count) continue;
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      const int n = p0 + wp * (BP / WP) + j * 16 + (lane >> 4) * 4;
+      const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      if (n < a.K) *reinterpret_cast<uint2*>(dx + (first + m) * a.K + n) = pack4(v);
+    }
+  }
+}
+
+// ------------------------------------------------------------- backward w --
+
+// One workgroup: BQ weight rows by BP columns of one expert's gradient, over one of
+// `splits` equal parts of its rows.
+template <int BQ, int BP, int WQ, int WP, int STAGES>
+__global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_w_kernel(LinearArgs a) {
+  constexpr int kWaves = WQ * WP, kQ = BQ / WQ / 16, kP = BP / WP / 16, kD = 64;
+  using QTile = DepthTile<BQ, kD, kWaves>;
+  using PTile = DepthTile<BP, kD, kWaves>;
+  constexpr int kStage = QTile::kBytes + PTile::kBytes, kLoads = QTile::kLoads + PTile::kLoads;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wq = wave / WP, wp = wave % WP;
+  // experts dealt to XCDs in 8 equal runs of workgroups, as find_item does
+  const int tn = (a.N + BQ - 1) / BQ, tk = (a.K + BP - 1) / BP;
+  const int total = a.E * a.parts * tn * tk * a.splits, chunk = (total + 7) / 8;
+  int i = (blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= chunk || i >= total) return;
+  const int split = i % a.splits;
+  i /= a.splits;
+  const int tp = i % tk;
+  i /= tk;
+  const int tq = i % tn;
+  i /= tn;
+  const int h = i % a.parts, e = i / a.parts;
+  const int row0 = a.offsets != nullptr ? a.offsets[e] : 0;
+  const int count = a.offsets != nullptr ? run_length(row0, a.counts[e], a.rows) : a.rows;
+  const int share = ((count + a.splits - 1) / a.splits + kD - 1) / kD * kD;
+  const int begin = min(count, split * share), rows = min(count, begin + share) - begin;
+  const int q0 = tq * BQ, p0 = tp * BP;
+  const int ldq = a.parts * a.N * 2, ldp = a.K * 2;
+  const int64_t first = count > 0 ? (int64_t)row0 + begin : 0;
+  const char* dz = static_cast<const char*>(a.dz) + first * ldq + ((int64_t)h * a.N + q0) * 2;
+  const char* x = static_cast<const char*>(a.x) + first * ldp + p0 * 2;
+  QTile qt;
+  PTile pt;
+  qt.init(wave, lane, ldq, [&](int g) { return q0 + g * 8 < a.N ? (uint32_t)(g * 16) : kNoFetch; });
+  pt.init(wave, lane, ldp, [&](int g) { return p0 + g * 8 < a.K ? (uint32_t)(g * 16) : kNoFetch; });
+  const int steps = (rows + kD - 1) / kD;
+  auto issue = [&](int s, int stage) {
+    char* b = smem + stage * kStage;
+    const int left = rows - s * kD;
+    qt.load(resource(dz + (int64_t)s * kD * ldq), b, wave, 0, left);
+    pt.load(resource(x + (int64_t)s * kD * ldp), b + QTile::kBytes, wave, 0, left);
+  };
+  f32x4 acc[kQ][kP], ones_acc[kQ];
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    ones_acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int p = 0; p < kP; ++p) acc[q][p] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  // the bias gradient is the product with a column of ones: by the workgroups of
+  // the first column tile, in their first column of waves
+  const bool sums = a.db[0] != nullptr && tp == 0 && wp == 0;
+  const __bf16 one = (__bf16)1.0f;
+  const bf16x8 ones{one, one, one, one, one, one, one, one};
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
+  int stage = 0;
+  for (int s = 0; s < steps; ++s) {
+    wait_and_meet<(STAGES - 2) * kLoads>();
+    issue(s + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+    const char* b = smem + stage * kStage;
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
+#pragma unroll
+    for (int kk = 0; kk < kD / 32; ++kk) {
+      bf16x8 q[kQ], p[kP];
+#pragma unroll
+      for (int r = 0; r < kQ; ++r) q[r] = QTile::frag(b, wq * (BQ / WQ) + r * 16, kk, lane);
+#pragma unroll
+      for (int c = 0; c < kP; ++c) p[c] = PTile::frag(b + QTile::kBytes, wp * (BP / WP) + c * 16, kk, lane);
+      if (sums) {
+#pragma unroll
+        for (int r = 0; r < kQ; ++r) ones_acc[r] = mma::mfma(ones, q[r], ones_acc[r]);
+      }
+#pragma unroll
+      for (int c = 0; c < kP; ++c)
+#pragma unroll
+        for (int r = 0; r < kQ; ++r) acc[r][c] = mma::mfma(p[c], q[r], acc[r][c]);
+    }
+  }
+  wait_and_meet<0>();
+  // with splits the sums go to the workspace: per split dw (all parts), then db
+  const int64_t weight = (int64_t)a.E * a.N * a.K;
+  const bool whole = a.splits == 1;
+  float* part = whole ? nullptr : a.part + split * (a.parts * (weight + (a.db[0] != nullptr ? (int64_t)a.E * a.N : 0)));
+#pragma unroll
+  for (int r = 0; r < kQ; ++r) {
+    const int n = q0 + wq * (BQ / WQ) + r * 16 + (lane & 15);
+    if (n >= a.N) continue;
+    const int64_t line = (int64_t)e * a.N + n;
+    if (sums && lane < 16) {
+      float* db = whole ? a.db[h] : part + a.parts * weight + (int64_t)h * a.E * a.N;
+      db[line] = ones_acc[r][0];
+    }
+#pragma unroll
+    for (int c = 0; c < kP; ++c) {
+      const int k = p0 + wp * (BP / WP) + c * 16 + (lane >> 4) * 4;
+      if (k >= a.K) continue;
+      const int64_t at = line * a.K + k;
+      const float v[4] = {acc[r][c][0], acc[r][c][1], acc[r][c][2], acc[r][c][3]};
+      if (!whole)
+        *reinterpret_cast<f32x4*>(part + h * weight + at) = acc[r][c];
+      else if (a.dw_f32)
+        *reinterpret_cast<f32x4*>(static_cast<float*>(a.dw[h]) + at) = acc[r][c];
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dw[h]) + at) = pack4(v);
+    }
+  }
+}
+
+// Joins the splits' sums in order, 4 elements a thread (every part is a multiple
+// of 8 elements long).
+__global__ __launch_bounds__(256) void join_splits_kernel(LinearArgs a) {
+  const int64_t weight = (int64_t)a.E * a.N * a.K, bias = a.db[0] != nullptr ? (int64_t)a.E * a.N : 0;
+  const int64_t total = a.parts * (weight + bias);
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= total) return;
+  f32x4 v = *reinterpret_cast<const f32x4*>(a.part + i);
+  for (int s = 1; s < a.splits; ++s) v += *reinterpret_cast<const f32x4*>(a.part + s * total + i);
+  if (i < a.parts * weight) {
+    const int h = i >= weight ? 1 : 0;
+    const int64_t at = i - h * weight;
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    if (a.dw_f32)
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.dw[h]) + at) = v;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dw[h]) + at) = pack4(f);
+  } else {
+    const int64_t b = i - a.parts * weight;
+    const int h = b >= bias ? 1 : 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) a.db[h][b - h * bias + c] = v[c];
+  }
+}
+
+// ---------------------------------------------------- activation gradient --
+
+constexpr int kActRows = 16;  // rows a workgroup takes
+
+__global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs a, const uint16_t* __restrict__ dy,
+                                                           const uint16_t* pre, uint16_t* dz) {
+  const Item it = find_item(a, blockIdx.x, kActRows, 1);
+  if (it.e < 0) return;
+  const int per = a.N / 8, rows = min(kActRows, it.count - it.tq * kActRows);
+  const int64_t first = (int64_t)it.row0 + it.tq * kActRows;
+  for (int i = threadIdx.x; i < rows * per; i += 256) {
+    const int rr = i / per, c = (i - rr * per) * 8;
+    const int64_t r = first + rr;
+    float g[8], z[8], o[8];
+    row::load8(dy + r * a.N, c, a.N, g);
+    row::load8(pre + r * a.parts * a.N, c, a.N, z);
+    if (a.act == MOE_ACT_GELU) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float t = tanhf(gelu_tanh_arg(z[j]));
+        const float d = 0.7978845608028654f * fmaf(3.0f * 0.044715f * z[j], z[j], 1.0f);
+        // where tanh has reached 1 its slope is 0, also where d overflows
+        const float bend = 1.0f - t * t;
+        o[j] = g[j] * (0.5f * (1.0f + t) + (bend > 0.f ? 0.5f * z[j] * bend * d : 0.f));
+      }
+    } else {
+      float u[8];
+      if (a.act == MOE_ACT_SWIGLU) row::load8(pre + r * 2 * a.N + a.N, c, a.N, u);
+      float o2[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = 1.0f / (1.0f + expf(-z[j]));
+        const float d = s * fmaf(z[j], 1.0f - s, 1.0f);
+        if (a.act == MOE_ACT_SWIGLU) {
+          o[j] = g[j] * u[j] * d;
+          o2[j] = g[j] * (z[j] * s);
+        } else {
+          o[j] = g[j] * d;
+        }
+      }
+      if (a.act == MOE_ACT_SWIGLU) row::store8(dz + r * 2 * a.N + a.N, c, a.N, o2);
+    }
+    row::store8(dz + r * a.parts * a.N, c, a.N, o);
+  }
+}
+
+// ---------------------------------------------------------------- launch --
+
+// Instantiated by name: the host pass of this compiler otherwise leaves out the
+// launch stubs of some kernel templates that are only reached through pointers.
+template __global__ void linear_kernel<true, true, 128, 256, 2, 4, 128, 2>(LinearArgs);
+template __global__ void linear_kernel<true, false, 128, 128, 2, 2, 128, 2>(LinearArgs);
+template __global__ void linear_kernel<false, true, 128, 256, 2, 4, 64, 3>(LinearArgs);
+template __global__ void linear_kernel<false, false, 128, 128, 2, 2, 128, 2>(LinearArgs);
+template __global__ void linear_backward_x_kernel<128, 128, 2, 2, 2>(LinearArgs);
+template __global__ void linear_backward_w_kernel<128, 128, 2, 2, 2>(LinearArgs);
+
+template <typename K>
+hipError_t launch(K kern, int64_t items, int threads, int lds, const LinearArgs& a, hipStream_t s,
+                  std::atomic<size_t> (&allowed)[kMaxCachedDevices]) {
+  const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kern), lds, allowed);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)((items + 7) / 8 * 8)), dim3(threads), lds, s, a);
+  return hipGetLastError();
+}
+
+template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int STAGES>
+hipError_t run_forward(const LinearArgs& a, hipStream_t s) {
+  using T = Forward<FP8, GATED, BQ, BP, WQ, WP, DB, STAGES>;
+  static std::atomic<size_t> allowed[kMaxCachedDevices];
+  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, BQ) * ((a.N + T::kCols - 1) / T::kCols);
+  void (*const kern)(LinearArgs) = &linear_kernel<FP8, GATED, BQ, BP, WQ, WP, DB, STAGES>;
+  return launch(kern, items, T::kThreads, T::kLds, a, s, allowed);
+}
+
+constexpr int kBQ = 128, kBP = 128, kStages = 2;
+
+
+}  // namespace
+
+hipError_t launch_linear(const LinearArgs& a, bool fp8, hipStream_t s) {
+  if (fp8) return a.parts == 2 ? run_forward<true, true, 128, 256, 2, 4, 128, 2>(a, s) : run_forward<true, false, 128, 128, 2, 2, 128, 2>(a, s);
+  return a.parts == 2 ? run_forward<false, true, 128, 256, 2, 4, 64, 3>(a, s) : run_forward<false, false, 128, 128, 2, 2, 128, 2>(a, s);
+}
+
+hipError_t launch_linear_backward_x(const LinearArgs& a, hipStream_t s) {
+  static std::atomic<size_t> allowed[kMaxCachedDevices];
+  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, kBQ) * ((a.K + kBP - 1) / kBP);
+  return launch(linear_backward_x_kernel<kBQ, kBP, 2, 2, kStages>, items, 256, kStages * (kBQ + kBP) * 128, a, s, allowed);
+}
+
+int backward_w_splits(int64_t rows, int E, int N, int K, int parts) {
+  const int64_t tiles = (int64_t)E * parts * ((N + kBQ - 1) / kBQ) * ((K + kBP - 1) / kBP);
+  if (tiles >= 256) return 1;
+  // workgroups for two rounds of the GPU, as long as a split keeps 256 rows on average
+  return (int)std::max<int64_t>(1, std::min<int64_t>((512 + tiles - 1) / tiles, rows / E / 256));
+}
+
+hipError_t launch_linear_backward_w(const LinearArgs& a, hipStream_t s) {
+  static std::atomic<size_t> allowed[kMaxCachedDevices];
+  const int64_t items = (int64_t)a.E * a.parts * ((a.N + kBQ - 1) / kBQ) * ((a.K + kBP - 1) / kBP) * a.splits;
+  const hipError_t e =
+      launch(linear_backward_w_kernel<kBQ, kBP, 2, 2, kStages>, items, 256, kStages * (kBQ + kBP) * 128, a, s, allowed);
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t total = (int64_t)a.parts * a.E * a.N * (a.K + (a.db[0] != nullptr ? 1 : 0));
+  hipLaunchKernelGGL(join_splits_kernel, dim3((unsigned)((total / 4 + 255) / 256)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_act_backward(const LinearArgs& a, const uint16_t* dy, const uint16_t* pre, uint16_t* dz, hipStream_t s) {
+  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, kActRows);
+  hipLaunchKernelGGL(act_backward_kernel, dim3((unsigned)((items + 7) / 8 * 8)), dim3(256), 0, s, a, dy, pre, dz);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,357 @@
+// RMS norm with the residual's addition, bf16 or 8-bit rows out, and its
+// gradient, for gfx950.
+//
+//   z = x + r (rounded to r's type), rstd = (mean z^2 + eps)^(-1/2), y = z rstd w
+//   t = dy w, n = z rstd, dx = dz + rstd (t - n mean(t n)), dw = sum_rows dy n
+//
+// Both are bound by HBM: a row is read once and stays in registers between the
+// sum and its use, so each element moves once.  A row belongs to one wave (up to
+// 2048 columns, 8 per lane and piece, at most 4 pieces) or to a workgroup of 4 or
+// 16 waves; with one wave per row the sum needs no LDS and no barrier.  A few
+// rows take the wider form, which has fewer dependent loads per lane.
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "moe_internal.h"
+#include "ops_internal.h"
+#include "row_common.h"
+
+namespace moe {
+namespace {
+
+using namespace row;
+
+// The sum of v over the TPR threads of a row; `red` holds one float per wave of
+// the workgroup, and a barrier separates two uses of it.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = wave_sum(v);
+  if constexpr (TPR == 64) {
+    return v;
+  } else {
+    constexpr int W = TPR / 64;
+    const int wave = threadIdx.x >> 6, base = wave / W * W;
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    float s = red[base];
+#pragma unroll
+    for (int i = 1; i < W; ++i) s += red[base + i];
+    return s;
+  }
+}
+
+constexpr float kLargeMean = 0x1p100f, kSmallMean = 0x1p-100f, kSmallEps = 0x1p-80f;
+
+template <typename RT, bool HAS_R>
+__device__ __forceinline__ void load_z(const uint16_t* x, const RT* r, int c, int H, float (&z)[8]) {
+  load8(x, c, H, z);
+  if constexpr (HAS_R) {
+    float a[8];
+    load8(r, c, H, a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      z[i] += a[i];
+      // the stored row is the one that is normalised: round to its type here
+      if constexpr (sizeof(RT) == 2) z[i] = (float)(__bf16)z[i];
+    }
+  }
+}
+
+// TPR threads per row, NV pieces of 8 columns per thread, THREADS / TPR rows per workgroup.
+template <int TPR, int NV, int THREADS, typename RT, bool HAS_R, bool FP8>
+__global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
+  __shared__ float red[THREADS / 64];
+  const int sub = threadIdx.x / TPR, j = threadIdx.x % TPR;
+  const int64_t m = (int64_t)blockIdx.x * (THREADS / TPR) + sub;
+  const bool live = m < a.M;
+  const int64_t mm = live ? m : a.M - 1;  // a row past the last repeats it and stores nothing
+  const int H = a.H;
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + mm * a.ldx;
+  const RT* r = static_cast<const RT*>(a.res) + mm * H;
+  float z[NV][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) load_z<RT, HAS_R>(x, r, (v * TPR + j) * 8, H, z[v]);
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(z[v][i], z[v][i], ss);
+  float w[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) load8(static_cast<const uint16_t*>(a.w), (v * TPR + j) * 8, H, w[v]);
+  if constexpr (HAS_R) {
+    if (live && a.zout != nullptr) {
+      RT* zo = static_cast<RT*>(a.zout) + m * H;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) store8(zo, (v * TPR + j) * 8, H, z[v]);
+    }
+  }
+  float mean = row_sum<TPR>(ss, red) / (float)H, eps = a.eps, unit = 1.f;
+  // Squares that leave float32's range (values past 2^63, or below 2^-50 with
+  // next to no eps) are summed once more in a unit that keeps them inside it;
+  // the whole row takes the same way.
+  const bool large = mean > kLargeMean, small = mean < kSmallMean && eps < kSmallEps;
+  if (large || small) {
+    unit = large ? 0x1p-64f : 0x1p64f;
+    ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = z[v][i] * unit;
+        ss = fmaf(t, t, ss);
+      }
+    if constexpr (TPR > 64) __syncthreads();  // red is read
+    mean = row_sum<TPR>(ss, red) / (float)H;
+    eps = eps * unit * unit;
+  }
+  const float rstd = unit / sqrtf(mean + eps);
+  if (!live) return;
+  if (a.rstd != nullptr && j == 0) a.rstd[m] = rstd;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * TPR + j) * 8;
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = z[v][i] * rstd * w[v][i];
+    if constexpr (FP8) {
+      // 16 neighbouring lanes hold one scale block (H is a multiple of 128, so a
+      // block is wholly inside the row or wholly past it)
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = max(mx, abs_bits(y[i]));
+      const float scale = block_scale(row16_umax(mx));
+      if (c < H) {
+        uint32_t lo, hi;
+        e4m3x8(y, scale, lo, hi);
+        *reinterpret_cast<u32x2_e1*>(static_cast<uint8_t*>(a.out) + m * H + c) = u32x2_e1{lo, hi};
+        if ((j & 15) == 0) a.scale[m * (H / kScaleBlock) + c / kScaleBlock] = scale;
+      }
+    } else {
+      store8(static_cast<uint16_t*>(a.out) + m * H, c, H, y);
+    }
+  }
+}
+
+// Each row group of the workgroup walks rows g, g + groups, ...; the columns' sums
+// of dy n stay in registers, the workgroup's groups add theirs in order through
+// LDS, and each workgroup leaves one partial row (or, when it is the only one,
+// the result).
+template <int TPR, int NV, int THREADS, typename ZT, bool DW>
+__global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackwardArgs a) {
+  constexpr int R = THREADS / TPR;
+  __shared__ float red[THREADS / 64];
+  __shared__ float cols[DW && R > 1 ? TPR * NV * 8 : 1];
+  const int sub = threadIdx.x / TPR, j = threadIdx.x % TPR;
+  const int H = a.H;
+  uint32_t w[NV][4];
+  float acc[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    float t[8];
+    load8(static_cast<const uint16_t*>(a.w), (v * TPR + j) * 8, H, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[v][i] = pack_bf16(t[2 * i], t[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[v][i] = 0.f;
+  }
+  const int64_t step = (int64_t)gridDim.x * R;
+  for (int64_t m0 = (int64_t)blockIdx.x * R; m0 < a.M; m0 += step) {
+    const int64_t m = m0 + sub;
+    const bool live = m < a.M;
+    const int64_t mm = live ? m : a.M - 1;
+    const ZT* zp = static_cast<const ZT*>(a.z) + mm * H;
+    const ZT* dzp = static_cast<const ZT*>(a.dz) + mm * H;
+    float n[NV][8], dy[NV][8], dz[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + j) * 8;
+      load8(zp, c, H, n[v]);
+      load8(static_cast<const uint16_t*>(a.dy) + mm * H, c, H, dy[v]);
+      if (a.dz != nullptr) load8(dzp, c, H, dz[v]);
+    }
+    const float rstd = a.rstd[mm];
+    float dot = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        n[v][i] *= rstd;
+        const float g = dy[v][i] * n[v][i];
+        if (DW && live) acc[v][i] += g;
+        const float wv = i & 1 ? bf16_hi(w[v][i / 2]) : bf16_lo(w[v][i / 2]);
+        dy[v][i] *= wv;
+        dot = fmaf(dy[v][i], n[v][i], dot);
+      }
+    if constexpr (TPR > 64) __syncthreads();  // red is read to the end of the last row
+    dot = row_sum<TPR>(dot, red) / (float)H;
+    if (live) {
+      ZT* dx = static_cast<ZT*>(a.dx) + m * H;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o[i] = rstd * fmaf(-n[v][i], dot, dy[v][i]);
+          if (a.dz != nullptr) o[i] += dz[v][i];
+        }
+        store8(dx, (v * TPR + j) * 8, H, o);
+      }
+    }
+  }
+  if constexpr (DW) {
+    if constexpr (R > 1) {
+      // groups 0, 1, ... add their columns in turn
+#pragma unroll 1
+      for (int g = 0; g < R; ++g) {
+        if (sub == g) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float* p = &cols[(v * 8 + i) * TPR + j];
+              *p = g == 0 ? acc[v][i] : *p + acc[v][i];
+            }
+        }
+        __syncthreads();
+      }
+    }
+    if (sub == 0) {
+      float* out = a.part + (int64_t)blockIdx.x * H;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if constexpr (R > 1) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[v][i] = cols[(v * 8 + i) * TPR + j];
+        }
+        store8(out, (v * TPR + j) * 8, H, acc[v]);
+      }
+    }
+  }
+}
+
+// dw[c] = the partial rows' sum: 16 columns a workgroup, 16 threads a column, each
+// every 16th partial row in order, the 16 sums joined in a fixed tree.
+__global__ __launch_bounds__(256) void norm_dw_kernel(const float* __restrict__ part, int G, int H, float* __restrict__ dw) {
+  __shared__ float red[16][17];
+  const int cc = threadIdx.x & 15, s = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + cc;
+  float v = 0.f;
+  if (c < H) {
+#pragma unroll 8
+    for (int g = s; g < G; g += 16) v += part[(int64_t)g * H + c];
+  }
+  red[s][cc] = v;
+  __syncthreads();
+  for (int d = 8; d > 0; d >>= 1) {
+    if (s < d) red[s][cc] += red[s + d][cc];
+    __syncthreads();
+  }
+  if (s == 0 && c < H) dw[c] = red[0][cc];
+}
+
+__global__ __launch_bounds__(256) void zero_kernel(float* p, int n) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = 0.f;
+}
+
+template <int TPR, int NV, int THREADS, typename RT, bool HAS_R>
+hipError_t run_norm(const NormArgs& a, hipStream_t s) {
+  const unsigned blocks = (unsigned)((a.M + THREADS / TPR - 1) / (THREADS / TPR));
+  if (a.scale != nullptr)
+    hipLaunchKernelGGL((norm_kernel<TPR, NV, THREADS, RT, HAS_R, true>), dim3(blocks), dim3(THREADS), 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_kernel<TPR, NV, THREADS, RT, HAS_R, false>), dim3(blocks), dim3(THREADS), 0, s, a);
+  return hipGetLastError();
+}
+
+// A row's threads: one wave up to 2048 columns when there are rows enough to fill
+// the GPU with such waves, else 256 threads (up to 8192 columns), else 1024.
+constexpr int64_t kWaveRows = 2048;
+
+template <typename RT, bool HAS_R>
+hipError_t norm_by_width(const NormArgs& a, hipStream_t s) {
+  const int p = (a.H + 7) / 8;
+  if (p <= 64) return run_norm<64, 1, 256, RT, HAS_R>(a, s);
+  if (p <= 256 && a.M >= kWaveRows)
+    return p <= 128 ? run_norm<64, 2, 256, RT, HAS_R>(a, s) : run_norm<64, 4, 256, RT, HAS_R>(a, s);
+  if (p <= 256) return run_norm<256, 1, 256, RT, HAS_R>(a, s);
+  if (p <= 512) return run_norm<256, 2, 256, RT, HAS_R>(a, s);
+  if (p <= 1024) return run_norm<256, 4, 256, RT, HAS_R>(a, s);
+  if (p <= 2048) return run_norm<1024, 2, 1024, RT, HAS_R>(a, s);
+  return run_norm<1024, 4, 1024, RT, HAS_R>(a, s);
+}
+
+struct BackwardShape {
+  int tpr, nv, threads, groups;
+};
+
+BackwardShape backward_shape(int64_t M, int H) {
+  const int p = (H + 7) / 8;
+  BackwardShape b;
+  b.tpr = p <= 256 ? 64 : (p <= 1024 ? 256 : 1024);
+  b.nv = p <= 64 ? 1 : p <= 128 ? 2 : p <= 256 ? 4 : p <= 512 ? 2 : p <= 1024 ? 4 : p <= 2048 ? 2 : 4;
+  b.threads = b.tpr == 1024 ? 1024 : 512;
+  const int64_t per = b.threads / b.tpr;
+  b.groups = (int)std::min<int64_t>((M + per - 1) / per, 512);
+  return b;
+}
+
+template <int TPR, int NV, int THREADS, typename ZT>
+void run_backward(const NormBackwardArgs& a, int groups, bool dw, hipStream_t s) {
+  if (dw)
+    hipLaunchKernelGGL((norm_backward_kernel<TPR, NV, THREADS, ZT, true>), dim3(groups), dim3(THREADS), 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_backward_kernel<TPR, NV, THREADS, ZT, false>), dim3(groups), dim3(THREADS), 0, s, a);
+}
+
+template <typename ZT>
+void backward_by_width(const NormBackwardArgs& a, const BackwardShape& b, bool dw, hipStream_t s) {
+  if (b.tpr == 64) {
+    if (b.nv == 1) return run_backward<64, 1, 512, ZT>(a, b.groups, dw, s);
+    if (b.nv == 2) return run_backward<64, 2, 512, ZT>(a, b.groups, dw, s);
+    return run_backward<64, 4, 512, ZT>(a, b.groups, dw, s);
+  }
+  if (b.tpr == 256) {
+    if (b.nv == 2) return run_backward<256, 2, 512, ZT>(a, b.groups, dw, s);
+    return run_backward<256, 4, 512, ZT>(a, b.groups, dw, s);
+  }
+  if (b.nv == 2) return run_backward<1024, 2, 1024, ZT>(a, b.groups, dw, s);
+  return run_backward<1024, 4, 1024, ZT>(a, b.groups, dw, s);
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, bool res_f32, hipStream_t s) {
+  if (a.res == nullptr) return norm_by_width<uint16_t, false>(a, s);
+  return res_f32 ? norm_by_width<float, true>(a, s) : norm_by_width<uint16_t, true>(a, s);
+}
+
+size_t norm_backward_workspace(int64_t M, int H) {
+  const int g = backward_shape(M, H).groups;
+  return g > 1 ? (size_t)g * H * 4 : 0;
+}
+
+hipError_t launch_norm_backward(const NormBackwardArgs& args, bool z_f32, float* dw, float* ws, hipStream_t s) {
+  NormBackwardArgs a = args;
+  if (a.M == 0) {
+    if (dw != nullptr) hipLaunchKernelGGL(zero_kernel, dim3((a.H + 255) / 256), dim3(256), 0, s, dw, a.H);
+    return hipGetLastError();
+  }
+  const BackwardShape b = backward_shape(a.M, a.H);
+  a.part = b.groups > 1 ? ws : dw;
+  if (z_f32)
+    backward_by_width<float>(a, b, dw != nullptr, s);
+  else
+    backward_by_width<uint16_t>(a, b, dw != nullptr, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || dw == nullptr || b.groups == 1) return e;
+  hipLaunchKernelGGL(norm_dw_kernel, dim3((a.H + 15) / 16), dim3(256), 0, s, ws, b.groups, a.H, dw);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,146 @@
+// Row building blocks shared by the gfx950 kernels that stream token rows
+// (norm, permutation, epilogues): 8-element pieces of bf16 or float32 rows at any
+// element alignment, wave sums on the DPP crossbar, e4m3 rounding.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mma_common.h"
+
+namespace moe {
+namespace row {
+
+constexpr int kScaleBlock = 128;             // columns that share one scale of an 8-bit row
+constexpr float kE4m3Max = 448.0f;           // largest e4m3fn value
+constexpr float kMinScale = 0x1p-126f;       // smallest normal float: a scale never underflows
+
+// Vectors the compiler may only assume element-aligned: gfx950 serves them with
+// full-width loads and stores at any element alignment, so rows of odd length
+// need no other path; a 16-byte aligned address costs nothing extra.
+typedef uint32_t u32x4_e2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_e4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2_e1 __attribute__((ext_vector_type(2), aligned(1)));
+
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// float32 pair -> packed bf16, round to nearest even (the hardware conversion; NaN stays NaN)
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  const bf2 v{(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// 8 consecutive elements from column c of a row of H, zero past its end.
+__device__ __forceinline__ void load8(const uint16_t* __restrict__ p, int c, int H, float (&v)[8]) {
+  if (c + 8 <= H) {
+    const u32x4_e2 d = *reinterpret_cast<const u32x4_e2*>(p + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(d[i]);
+      v[2 * i + 1] = bf16_hi(d[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < H ? mma::bf16_bits_to_f32(p[c + i]) : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(const float* __restrict__ p, int c, int H, float (&v)[8]) {
+  if (c + 8 <= H) {
+    const u32x4_e4 a = *reinterpret_cast<const u32x4_e4*>(p + c);
+    const u32x4_e4 b = *reinterpret_cast<const u32x4_e4*>(p + c + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(a[i]);
+      v[4 + i] = __uint_as_float(b[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < H ? p[c + i] : 0.f;
+  }
+}
+
+__device__ __forceinline__ void store8(uint16_t* __restrict__ p, int c, int H, const float (&v)[8]) {
+  uint32_t d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  if (c + 8 <= H) {
+    *reinterpret_cast<u32x4_e2*>(p + c) = u32x4_e2{d[0], d[1], d[2], d[3]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < H) p[c + i] = (uint16_t)(d[i / 2] >> (16 * (i & 1)));
+  }
+}
+__device__ __forceinline__ void store8(float* __restrict__ p, int c, int H, const float (&v)[8]) {
+  if (c + 8 <= H) {
+    u32x4_e4 a, b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = __float_as_uint(v[i]);
+      b[i] = __float_as_uint(v[4 + i]);
+    }
+    *reinterpret_cast<u32x4_e4*>(p + c) = a;
+    *reinterpret_cast<u32x4_e4*>(p + c + 4) = b;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < H) p[c + i] = v[i];
+  }
+}
+
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float dpp0(float v) {  // lanes without a source read 0
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROW_MASK, 0xF, false));
+}
+
+// Sum over each 16-lane row, in every lane of it (butterflies on the DPP crossbar).
+__device__ __forceinline__ float row16_sum(float v) {
+  v += dpp0<0xB1, 0xF>(v);   // quad_perm [1,0,3,2]
+  v += dpp0<0x4E, 0xF>(v);   // quad_perm [2,3,0,1]
+  v += dpp0<0x141, 0xF>(v);  // row_half_mirror
+  v += dpp0<0x140, 0xF>(v);  // row_mirror
+  return v;
+}
+// The wave's sum, the same bits in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row16_sum(v);
+  v += dpp0<0x142, 0xA>(v);  // row_bcast15 into rows 1 and 3
+  v += dpp0<0x143, 0xC>(v);  // row_bcast31 into rows 2 and 3
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Maximum of |v|'s bits over each 16-lane row: as integers NaN > inf > finite, so
+// a NaN or an infinity wins.
+__device__ __forceinline__ uint32_t row16_umax(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
+  return v;
+}
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Scale of a block from the bits of its absolute maximum.
+__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+  if (amax_bits == 0) return 1.f;
+  return fmaxf(__uint_as_float(amax_bits) / kE4m3Max, kMinScale);
+}
+
+// 8 values over the block's scale as e4m3fn codes, round to nearest even.  The
+// quotient is at most 448 (1 + 2^-23), which rounds to 448; with a NaN scale
+// every code is NaN.
+__device__ __forceinline__ void e4m3x8(const float (&v)[8], float scale, uint32_t& lo, uint32_t& hi) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = v[i] / scale;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
+}
+
+}  // namespace row
+}  // namespace moe
