@@ -41,6 +41,72 @@ __device__ __forceinline__ uint2 pack4(const float (&f)[4]) { return make_uint2(
 
 // ---------------------------------------------------------------- forward --
 
+// 4 consecutive columns n ... n + 3 of row r of expert e: bias, activation and
+// residual on float32 sums (z and u are rounded only into preact), `in`: stored.
+template <bool GATED>
+__device__ __forceinline__ void epilogue4(const LinearArgs& a, int e, int64_t r, int n, bool in, float (&z)[4], float (&u)[4],
+                                          float (&y)[4]) {
+  float f[4];
+  if (a.bias[0] != nullptr && in) {
+    unpack4(*reinterpret_cast<const uint2*>(a.bias[0] + (int64_t)e * a.N + n), f);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) z[c] += f[c];
+  }
+  if constexpr (GATED) {
+    if (a.bias[1] != nullptr && in) {
+      unpack4(*reinterpret_cast<const uint2*>(a.bias[1] + (int64_t)e * a.N + n), f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) u[c] += f[c];
+    }
+    if (a.preact != nullptr && in) {
+      *reinterpret_cast<uint2*>(a.preact + r * 2 * a.N + n) = pack4(z);
+      *reinterpret_cast<uint2*>(a.preact + r * 2 * a.N + a.N + n) = pack4(u);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = silu(z[c]) * u[c];
+  } else {
+    if (a.preact != nullptr && in) *reinterpret_cast<uint2*>(a.preact + r * a.N + n) = pack4(z);
+    if (a.act == MOE_ACT_SILU) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c] = silu(z[c]);
+    } else if (a.act == MOE_ACT_GELU) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c] = gelu(z[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c] = z[c];
+    }
+  }
+  if (a.residual != nullptr && in) {
+    unpack4(*reinterpret_cast<const uint2*>(a.residual + r * a.N + n), f);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] += f[c];
+  }
+}
+
+// 4 columns of an 8-bit row (n a multiple of 4), and the block's scale with its first.
+__device__ __forceinline__ void store_codes(const LinearArgs& a, int64_t r, int n, const float (&y)[4], float scale) {
+  uint32_t code = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] / scale, y[1] / scale, 0, false);
+  code = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] / scale, y[3] / scale, code, true);
+  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + r * a.N + n) = code;
+  if (n % row::kScaleBlock == 0) a.y_scale[r * (a.N / row::kScaleBlock) + n / row::kScaleBlock] = scale;
+}
+
+// Calls f with the smallest of kQ / 4, kQ / 2, 3 kQ / 4 and kQ subtiles that covers `live`.
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
+template <int kQ, typename F>
+__device__ __forceinline__ void by_live_subtiles(int live, F f) {
+  if constexpr (kQ >= 4) {
+    if (live <= kQ / 4) return f(Count<kQ / 4>{});
+    if (live <= kQ / 2) return f(Count<kQ / 2>{});
+    if (live <= kQ * 3 / 4) return f(Count<kQ * 3 / 4>{});
+  }
+  f(Count<kQ>{});
+}
+
 // A workgroup's tile: BQ rows by BP weight rows (SwiGLU: BP / 2 of the gate and
 // the same BP / 2 of the up weight, so that a lane holds z and u of its elements),
 // WQ x WP waves, DB bytes of depth per stage, STAGES stages in LDS.
@@ -59,6 +125,12 @@ struct Forward {
   static constexpr int kLds = kStage * STAGES;
 };
 
+// Rows of a tile are dealt to the WQ rows of waves in subtiles of 16 in turn, so a
+// partly filled tile leaves every wave the same share (at most one subtile apart);
+// a wave multiplies only its LIVE first subtiles.
+template <int WQ>
+__device__ __forceinline__ int q_row(int wq, int i) { return (i * WQ + wq) * 16; }
+
 template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int STAGES>
 __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
   using T = Forward<FP8, GATED, BQ, BP, WQ, WP, DB, STAGES>;
@@ -70,6 +142,7 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
   if (it.e < 0) return;
   const int ld = FP8 ? a.K : a.K * 2;
   const int q0 = it.tq * BQ, p0 = it.tp * kCols;
+  const int live = min(BQ, it.count - q0);  // rows of this tile
   const int64_t first = (int64_t)it.row0 + q0;
   const __amdgpu_buffer_rsrc_t rx = resource(static_cast<const char*>(a.x) + first * ld);
   const int64_t expert = (int64_t)it.e * a.N * ld;
@@ -79,13 +152,13 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
 
   typename T::QTile qt;
   typename T::PTile pt;
-  qt.init(wave, lane, [&](int r) { return q0 + r < it.count ? (uint32_t)(r * ld) : kNoFetch; });
+  qt.init(wave, lane, [&](int r) { return r < live ? (uint32_t)(r * ld) : kNoFetch; });
   pt.init(wave, lane, [&](int r) { return p0 + r < a.N ? (uint32_t)((p0 + r) * ld) : kNoFetch; });
   const int steps = (ld + DB - 1) / DB;
   auto issue = [&](int s, int stage) {
     char* b = smem + stage * T::kStage;
     const int left = ld - s * DB;  // not positive past the last step: zeros
-    qt.load(rx, b, wave, s * DB, left);
+    qt.load(rx, b, wave, s * DB, left, STAGES == 2 ? live : BQ);
 #pragma unroll
     for (int h = 0; h < kParts; ++h) pt.load(rw[h], b + T::QTile::kBytes + h * T::PTile::kBytes, wave, s * DB, left);
   };
@@ -96,18 +169,14 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
 #pragma unroll
     for (int j = 0; j < kP; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // 8-bit: this lane's row scales of the step at hand and of the next one
+  // 8-bit: where this lane's row scales and its columns' scales are
   const int blocks = a.K / row::kScaleBlock;
   const float* sx[kQ];
-  float sc[kQ], sn[kQ];
   const float* sw[kParts];
   if constexpr (FP8) {
 #pragma unroll
-    for (int i = 0; i < kQ; ++i) {
-      const int m = min(q0 + wq * (BQ / WQ) + i * 16 + (lane & 15), it.count - 1);
-      sx[i] = a.x_scale + ((int64_t)it.row0 + m) * blocks;
-      sn[i] = sx[i][0];
-    }
+    for (int i = 0; i < kQ; ++i)
+      sx[i] = a.x_scale + (first + min(q_row<WQ>(wq, i) + (lane & 15), live - 1)) * blocks;
     static_assert(kCols / WP <= row::kScaleBlock && row::kScaleBlock % (kCols / WP) == 0, "a wave's columns share a scale");
     const int nb = a.N / row::kScaleBlock;
     const int cb = min((p0 + wp * (kCols / WP)) / row::kScaleBlock, nb - 1);
@@ -117,117 +186,100 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
 
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
-  int stage = 0;
-  for (int s = 0; s < steps; ++s) {
-    wait_and_meet<(STAGES - 2) * T::kLoads>();
-    float swc[kParts];
+
+  auto p_row = [&](int j) { return wp * (kCols / WP) + (j % kC) * 16; };
+  auto multiply = [&](auto live_subtiles) {
+    constexpr int L = decltype(live_subtiles)::value;
+    float sc[L], sn[L];  // row scales of this step and of the next
     if constexpr (FP8) {
-      const int nx = min(s + 1, steps - 1);
 #pragma unroll
-      for (int i = 0; i < kQ; ++i) {
-        sc[i] = sn[i];
-        sn[i] = sx[i][nx];
-      }
-#pragma unroll
-      for (int h = 0; h < kParts; ++h) swc[h] = sw[h][s];
+      for (int i = 0; i < L; ++i) sn[i] = sx[i][0];
     }
-    issue(s + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-    const char* b = smem + stage * T::kStage;
-    const char* pb = b + T::QTile::kBytes;
-    stage = stage == STAGES - 1 ? 0 : stage + 1;
-    auto p_row = [&](int j) { return wp * (kCols / WP) + (j % kC) * 16; };
-    if constexpr (FP8) {
-      i32x8 q[kQ];
+    int stage = 0;
+    for (int s = 0; s < steps; ++s) {
+      wait_and_meet<(STAGES - 2) * T::kLoads>();
+      float swc[kParts];
+      if constexpr (FP8) {
+        const int nx = min(s + 1, steps - 1);
 #pragma unroll
-      for (int i = 0; i < kQ; ++i) q[i] = T::QTile::frag8(b, wq * (BQ / WQ) + i * 16, lane);
+        for (int i = 0; i < L; ++i) {
+          sc[i] = sn[i];
+          sn[i] = sx[i][nx];
+        }
 #pragma unroll
-      for (int j = 0; j < kP; ++j) {
-        const i32x8 p = T::PTile::frag8(pb + j / kC * T::PTile::kBytes, p_row(j), lane);
+        for (int h = 0; h < kParts; ++h) swc[h] = sw[h][s];
+      }
+      issue(s + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+      const char* b = smem + stage * T::kStage;
+      const char* pb = b + T::QTile::kBytes;
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
+      if constexpr (FP8) {
+        // The matrix cores' own 8-bit products lose the low bits of their sums
+        // (measured 1.5e-5 of the result on 128 terms), so the codes are widened to
+        // bf16, which is exact, and each scale block is scaled as it is added.
+        bf16x8 q[L][4];
 #pragma unroll
-        for (int i = 0; i < kQ; ++i) {
-          // one scale block of depth in one instruction, scaled as it is added
-          const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q[i], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
-          const float f = sc[i] * swc[j / kC];
+        for (int i = 0; i < L; ++i) T::QTile::frag8(b, q_row<WQ>(wq, i), lane, q[i]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(t[c], f, acc[i][j][c]);
+        for (int j = 0; j < kP; ++j) {
+          bf16x8 p[4];
+          T::PTile::frag8(pb + j / kC * T::PTile::kBytes, p_row(j), lane, p);
+          f32x4 t[L];
+#pragma unroll
+          for (int i = 0; i < L; ++i) t[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int i = 0; i < L; ++i) t[i] = mma::mfma(p[kk], q[i][kk], t[i]);
+#pragma unroll
+          for (int i = 0; i < L; ++i) {
+            const float f = sc[i] * swc[j / kC];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(t[i][c], f, acc[i][j][c]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < DB / 64; ++kk) {
+          bf16x8 q[L], p[kP];
+#pragma unroll
+          for (int i = 0; i < L; ++i) q[i] = T::QTile::frag(b, q_row<WQ>(wq, i), kk, lane);
+#pragma unroll
+          for (int j = 0; j < kP; ++j) p[j] = T::PTile::frag(pb + j / kC * T::PTile::kBytes, p_row(j), kk, lane);
+#pragma unroll
+          for (int j = 0; j < kP; ++j)
+#pragma unroll
+            for (int i = 0; i < L; ++i) acc[i][j] = mma::mfma(p[j], q[i], acc[i][j]);
         }
       }
-    } else {
-#pragma unroll
-      for (int kk = 0; kk < DB / 64; ++kk) {
-        bf16x8 q[kQ], p[kP];
-#pragma unroll
-        for (int i = 0; i < kQ; ++i) q[i] = T::QTile::frag(b, wq * (BQ / WQ) + i * 16, kk, lane);
-#pragma unroll
-        for (int j = 0; j < kP; ++j) p[j] = T::PTile::frag(pb + j / kC * T::PTile::kBytes, p_row(j), kk, lane);
-#pragma unroll
-        for (int j = 0; j < kP; ++j)
-#pragma unroll
-          for (int i = 0; i < kQ; ++i) acc[i][j] = mma::mfma(p[j], q[i], acc[i][j]);
-      }
     }
-  }
+  };
+  by_live_subtiles<kQ>((live - wq * 16 + 16 * WQ - 1) / (16 * WQ), multiply);
   wait_and_meet<0>();  // the loads past the last step have landed: LDS is free
 
+  // a tile can write 8-bit rows if it holds whole scale blocks of columns
+  constexpr bool kCodes = kCols % row::kScaleBlock == 0;
   // Epilogue: lane l holds row l % 16 and 4 consecutive columns of each subtile.
   const int quad = lane >> 4;
   const int colw = p0 + wp * (kCols / WP) + quad * 4;
   float* red = reinterpret_cast<float*>(smem);  // [WP][BQ] absolute maxima
 #pragma unroll
   for (int i = 0; i < kQ; ++i) {
-    const int m = wq * (BQ / WQ) + i * 16 + (lane & 15);
-    const bool live = q0 + m < it.count;
+    const int m = q_row<WQ>(wq, i) + (lane & 15);
     const int64_t r = first + m;
     uint32_t mx = 0;
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
       const int n = colw + j * 16;
-      const bool in = live && n < a.N;
-      float z[4], y[4];
+      const bool in = m < live && n < a.N;
+      float z[4], u[4], y[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) z[c] = acc[i][j][c];
-      if (a.bias[0] != nullptr && in) {
-        float f[4];
-        unpack4(*reinterpret_cast<const uint2*>(a.bias[0] + (int64_t)it.e * a.N + n), f);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) z[c] += f[c];
+      for (int c = 0; c < 4; ++c) {
+        z[c] = acc[i][j][c];
+        u[c] = acc[i][(GATED ? kC : 0) + j][c];
       }
-      if constexpr (GATED) {
-        float u[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) u[c] = acc[i][kC + j][c];
-        if (a.bias[1] != nullptr && in) {
-          float f[4];
-          unpack4(*reinterpret_cast<const uint2*>(a.bias[1] + (int64_t)it.e * a.N + n), f);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) u[c] += f[c];
-        }
-        if (a.preact != nullptr && in) {
-          *reinterpret_cast<uint2*>(a.preact + r * 2 * a.N + n) = pack4(z);
-          *reinterpret_cast<uint2*>(a.preact + r * 2 * a.N + a.N + n) = pack4(u);
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] = silu(z[c]) * u[c];
-      } else {
-        if (a.preact != nullptr && in) *reinterpret_cast<uint2*>(a.preact + r * a.N + n) = pack4(z);
-        if (a.act == MOE_ACT_SILU) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) y[c] = silu(z[c]);
-        } else if (a.act == MOE_ACT_GELU) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) y[c] = gelu(z[c]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) y[c] = z[c];
-        }
-      }
-      if (a.residual != nullptr && in) {
-        float f[4];
-        unpack4(*reinterpret_cast<const uint2*>(a.residual + r * a.N + n), f);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] += f[c];
-      }
-      if (a.y_scale == nullptr) {
+      epilogue4<GATED>(a, it.e, r, n, in, z, u, y);
+      if (!kCodes || a.y_scale == nullptr) {
         if (in) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + r * a.N + n) = pack4(y);
       } else {
 #pragma unroll
@@ -237,35 +289,154 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
         }
       }
     }
-    if (a.y_scale != nullptr) {
+    if (kCodes && a.y_scale != nullptr) {
       mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16));
       mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
       if (lane < 16) red[wp * BQ + m] = __uint_as_float(mx);
     }
   }
-  if (a.y_scale == nullptr) return;
-  // 8-bit rows: the tile's columns come in whole scale blocks, each spread over
-  // the waves that hold its columns
-  constexpr int kShare = row::kScaleBlock * WP / kCols;  // waves per block
+  if constexpr (kCodes) {
+    if (a.y_scale == nullptr) return;
+    // 8-bit rows: the tile's columns come in whole scale blocks, each spread over
+    // the waves that hold its columns
+    constexpr int kShare = row::kScaleBlock * WP / kCols;  // waves per block
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) {
+      const int m = q_row<WQ>(wq, i) + (lane & 15);
+      uint32_t mx = 0;
+#pragma unroll
+      for (int w = 0; w < kShare; ++w) mx = max(mx, __float_as_uint(red[(wp / kShare * kShare + w) * BQ + m]));
+      const float scale = row::block_scale(mx);
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        const int n = colw + j * 16;
+        const float y[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        if (m < live && n < a.N) store_codes(a, first + m, n, y, scale);
+      }
+    }
+  }
+}
+
+// --------------------------------------------------- forward, few rows --
+
+// Few rows per expert: the weights are read once and nothing is reused enough to
+// stage it, so a workgroup takes 16 rows by 16 WC columns, and WK waves split the
+// depth of each 16 columns in interleaved 128-deep chunks, both operands loaded
+// straight into the matrix cores' registers (16 lanes x 256 contiguous bytes a
+// chunk).  All loads of a chunk are in flight at once; the WK sums meet in LDS in
+// wave order.  8-bit rows out need all 128 columns of a scale block: WC = 8.
+template <bool FP8, bool GATED, int WC, int WK>
+__global__ __launch_bounds__(WC* WK * 64) void linear_few_kernel(LinearArgs a) {
+  constexpr int kParts = GATED ? 2 : 1, kCols = 16 * WC, kChunk = 128;
+  __shared__ f32x4 part[WC][WK][kParts][64];
+  __shared__ uint32_t red[WC][16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wc = wave % WC, wk = wave / WC, quad = lane >> 4;
+  const Item it = find_item(a, blockIdx.x, 16, (a.N + kCols - 1) / kCols);
+  if (it.e < 0) return;
+  const int live = min(16, it.count - it.tq * 16);
+  const int64_t first = (int64_t)it.row0 + it.tq * 16;
+  const int col0 = it.tp * kCols + wc * 16;
+  // rows and columns past the end repeat the last one and are not stored
+  const int64_t xr = first + min(lane & 15, live - 1);
+  const int64_t wr = (int64_t)it.e * a.N + min(col0 + (lane & 15), a.N - 1);
+  constexpr int kItem = FP8 ? 1 : 2;
+  const uint8_t* x = static_cast<const uint8_t*>(a.x) + xr * a.K * kItem;
+  const uint8_t* w[kParts];
+#pragma unroll
+  for (int h = 0; h < kParts; ++h) w[h] = static_cast<const uint8_t*>(a.w[h]) + wr * a.K * kItem;
+  f32x4 acc[kParts];
+#pragma unroll
+  for (int h = 0; h < kParts; ++h) acc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int chunks = (a.K + kChunk - 1) / kChunk;
+  constexpr int kLoads = FP8 ? 2 : 4;  // 16-byte pieces of a lane's 32 depth elements
+  if constexpr (FP8) {
+    const int nb = a.N / row::kScaleBlock;
+    const float* sx = a.x_scale + xr * chunks;
+    const float* sw[kParts];
+#pragma unroll
+    for (int h = 0; h < kParts; ++h) sw[h] = a.ws[h] + ((int64_t)it.e * nb + min(col0, a.N - 1) / row::kScaleBlock) * chunks;
+    for (int c = wk; c < chunks; c += WK) {
+      uint4 xv[kLoads], wv[kParts][kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = c * kChunk + quad * 32 + i * 16;
+        xv[i] = *reinterpret_cast<const uint4*>(x + at);
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) wv[h][i] = *reinterpret_cast<const uint4*>(w[h] + at);
+      }
+      const float f = sx[c];
+#pragma unroll
+      for (int h = 0; h < kParts; ++h) {
+        f32x4 t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          t = mma::mfma(mma::fp8x8_to_bf16(wv[h][i].x, wv[h][i].y), mma::fp8x8_to_bf16(xv[i].x, xv[i].y), t);
+          t = mma::mfma(mma::fp8x8_to_bf16(wv[h][i].z, wv[h][i].w), mma::fp8x8_to_bf16(xv[i].z, xv[i].w), t);
+        }
+        const float g = f * sw[h][c];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[h][k] = fmaf(t[k], g, acc[h][k]);
+      }
+    }
+  } else {
+    for (int c = wk; c < chunks; c += WK) {
+      uint4 xv[kLoads], wv[kParts][kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int d = c * kChunk + quad * 32 + i * 8;
+        const bool in = d < a.K;  // K is a multiple of 8
+        const int at = in ? d * 2 : 0;
+        xv[i] = *reinterpret_cast<const uint4*>(x + at);
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+          wv[h][i] = *reinterpret_cast<const uint4*>(w[h] + at);
+          if (!in) wv[h][i] = make_uint4(0, 0, 0, 0);
+        }
+        if (!in) xv[i] = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) acc[h] = mma::mfma(mma::as_bf16x8(wv[h][i]), mma::as_bf16x8(xv[i]), acc[h]);
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < kParts; ++h) part[wc][wk][h][lane] = acc[h];
   __syncthreads();
+  const int m = lane & 15, n = col0 + quad * 4;
+  const bool in = m < live && n < a.N;
+  float y[4] = {0.f, 0.f, 0.f, 0.f};
+  if (wk == 0) {
+    float z[4], u[4];
 #pragma unroll
-  for (int i = 0; i < kQ; ++i) {
-    const int m = wq * (BQ / WQ) + i * 16 + (lane & 15);
-    const bool live = q0 + m < it.count;
-    const int64_t r = first + m;
-    uint32_t mx = 0;
+    for (int h = 0; h < kParts; ++h) {
+      f32x4 s = part[wc][0][h][lane];
 #pragma unroll
-    for (int w = 0; w < kShare; ++w) mx = max(mx, __float_as_uint(red[(wp / kShare * kShare + w) * BQ + m]));
-    const float scale = row::block_scale(mx);
-    if (!live) continue;
+      for (int k = 1; k < WK; ++k) s += part[wc][k][h][lane];
 #pragma unroll
-    for (int j = 0; j < kC; ++j) {
-      const int n = colw + j * 16;
-      if (n >= a.N) continue;
-      uint32_t code = __builtin_amdgcn_cvt_pk_fp8_f32(acc[i][j][0] / scale, acc[i][j][1] / scale, 0, false);
-      code = __builtin_amdgcn_cvt_pk_fp8_f32(acc[i][j][2] / scale, acc[i][j][3] / scale, code, true);
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + r * a.N + n) = code;
-      if (n % row::kScaleBlock == 0) a.y_scale[r * (a.N / row::kScaleBlock) + n / row::kScaleBlock] = scale;
+      for (int c = 0; c < 4; ++c) (h == 0 ? z[c] : u[c]) = s[c];
+    }
+    epilogue4<GATED>(a, it.e, first + m, n, in, z, u, y);
+    if (a.y_scale == nullptr && in) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + (first + m) * a.N + n) = pack4(y);
+  }
+  if constexpr (WC == 8) {
+    if (a.y_scale == nullptr) return;
+    if (wk == 0) {
+      uint32_t mx = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mx = max(mx, row::abs_bits(y[c]));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
+      if (lane < 16) red[wc][lane] = mx;
+    }
+    __syncthreads();
+    if (wk == 0 && in) {
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < WC; ++i) mx = max(mx, red[i][m]);
+      store_codes(a, first + m, n, y, row::block_scale(mx));
     }
   }
 }
@@ -283,13 +454,14 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_x_kernel(Linea
   const Item it = find_item(a, blockIdx.x, BQ, (a.K + BP - 1) / BP);
   if (it.e < 0) return;
   const int q0 = it.tq * BQ, p0 = it.tp * BP;
+  const int live = min(BQ, it.count - q0);
   const int64_t first = (int64_t)it.row0 + q0;
   const int ldq = a.parts * a.N * 2, ldp = a.K * 2;
   const char* dz = static_cast<const char*>(a.dz) + first * ldq;
   const int64_t expert = (int64_t)it.e * a.N * ldp + p0 * 2;
   QTile qt;
   PTile pt;
-  qt.init(wave, lane, [&](int r) { return q0 + r < it.count ? (uint32_t)(r * ldq) : kNoFetch; });
+  qt.init(wave, lane, [&](int r) { return r < live ? (uint32_t)(r * ldq) : kNoFetch; });
   pt.init(wave, lane, ldp, [&](int g) { return p0 + g * 8 < a.K ? (uint32_t)(g * 16) : kNoFetch; });
   // the depth runs over the N columns of dz's first part, then of its second
   const int per = (a.N + kD - 1) / kD, steps = per * a.parts;
@@ -298,7 +470,7 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_x_kernel(Linea
     char* b = smem + stage * kStage;
     const int h = s >= per ? 1 : 0, k = s - h * per;
     const int left = s < steps ? a.N - k * kD : 0;
-    qt.load(rq, b, wave, (h * a.N + k * kD) * 2, left * 2);
+    qt.load(rq, b, wave, (h * a.N + k * kD) * 2, left * 2, STAGES == 2 ? live : BQ);
     pt.load(resource(static_cast<const char*>(a.w[s < steps ? h : 0]) + expert + (int64_t)k * kD * ldp), b + QTile::kBytes,
             wave, 0, left);
   };
@@ -309,31 +481,35 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_x_kernel(Linea
     for (int j = 0; j < kP; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
-  int stage = 0;
-  for (int s = 0; s < steps; ++s) {
-    wait_and_meet<(STAGES - 2) * kLoads>();
-    issue(s + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-    const char* b = smem + stage * kStage;
-    stage = stage == STAGES - 1 ? 0 : stage + 1;
+  auto multiply = [&](auto live_subtiles) {
+    constexpr int L = decltype(live_subtiles)::value;
+    int stage = 0;
+    for (int s = 0; s < steps; ++s) {
+      wait_and_meet<(STAGES - 2) * kLoads>();
+      issue(s + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+      const char* b = smem + stage * kStage;
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
 #pragma unroll
-    for (int kk = 0; kk < kD / 32; ++kk) {
-      bf16x8 q[kQ], p[kP];
+      for (int kk = 0; kk < kD / 32; ++kk) {
+        bf16x8 q[L], p[kP];
 #pragma unroll
-      for (int i = 0; i < kQ; ++i) q[i] = QTile::frag(b, wq * (BQ / WQ) + i * 16, kk, lane);
+        for (int i = 0; i < L; ++i) q[i] = QTile::frag(b, q_row<WQ>(wq, i), kk, lane);
 #pragma unroll
-      for (int j = 0; j < kP; ++j) p[j] = PTile::frag(b + QTile::kBytes, wp * (BP / WP) + j * 16, kk, lane);
+        for (int j = 0; j < kP; ++j) p[j] = PTile::frag(b + QTile::kBytes, wp * (BP / WP) + j * 16, kk, lane);
 #pragma unroll
-      for (int j = 0; j < kP; ++j)
+        for (int j = 0; j < kP; ++j)
 #pragma unroll
-        for (int i = 0; i < kQ; ++i) acc[i][j] = mma::mfma(p[j], q[i], acc[i][j]);
+          for (int i = 0; i < L; ++i) acc[i][j] = mma::mfma(p[j], q[i], acc[i][j]);
+      }
     }
-  }
+  };
+  by_live_subtiles<kQ>((live - wq * 16 + 16 * WQ - 1) / (16 * WQ), multiply);
   wait_and_meet<0>();
   uint16_t* dx = static_cast<uint16_t*>(a.y);
 #pragma unroll
   for (int i = 0; i < kQ; ++i) {
-    const int m = wq * (BQ / WQ) + i * 16 + (lane & 15);
-    if (q0 + m >= it.count) continue;
+    const int m = q_row<WQ>(wq, i) + (lane & 15);
+    if (m >= live) continue;
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
       const int n = p0 + wp * (BP / WP) + j * 16 + (lane >> 4) * 4;
@@ -529,12 +705,21 @@ __global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs a, const u
 
 // Instantiated by name: the host pass of this compiler otherwise leaves out the
 // launch stubs of some kernel templates that are only reached through pointers.
+#define MOE_TILES(F, G)                                                     \
+  template __global__ void linear_kernel<F, G, 128, 128, 2, 2, 128, 2>(LinearArgs); \
+  template __global__ void linear_few_kernel<F, G, 1, 16>(LinearArgs);      \
+  template __global__ void linear_few_kernel<F, G, 8, 2>(LinearArgs);
+MOE_TILES(false, false)
+MOE_TILES(false, true)
+MOE_TILES(true, false)
+MOE_TILES(true, true)
+#undef MOE_TILES
+template __global__ void linear_kernel<false, false, 256, 256, 2, 4, 128, 2>(LinearArgs);
+template __global__ void linear_kernel<false, true, 256, 256, 2, 4, 128, 2>(LinearArgs);
 template __global__ void linear_kernel<true, true, 128, 256, 2, 4, 128, 2>(LinearArgs);
-template __global__ void linear_kernel<true, false, 128, 128, 2, 2, 128, 2>(LinearArgs);
-template __global__ void linear_kernel<false, true, 128, 256, 2, 4, 64, 3>(LinearArgs);
-template __global__ void linear_kernel<false, false, 128, 128, 2, 2, 128, 2>(LinearArgs);
 template __global__ void linear_backward_x_kernel<128, 128, 2, 2, 2>(LinearArgs);
 template __global__ void linear_backward_w_kernel<128, 128, 2, 2, 2>(LinearArgs);
+template __global__ void linear_backward_w_kernel<256, 256, 2, 4, 2>(LinearArgs);
 
 template <typename K>
 hipError_t launch(K kern, int64_t items, int threads, int lds, const LinearArgs& a, hipStream_t s,
@@ -554,34 +739,70 @@ hipError_t run_forward(const LinearArgs& a, hipStream_t s) {
   return launch(kern, items, T::kThreads, T::kLds, a, s, allowed);
 }
 
-constexpr int kBQ = 128, kBP = 128, kStages = 2;
+template <bool FP8, bool GATED, int WC, int WK>
+hipError_t run_few(const LinearArgs& a, hipStream_t s) {
+  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, 16) * ((a.N + 16 * WC - 1) / (16 * WC));
+  hipLaunchKernelGGL((linear_few_kernel<FP8, GATED, WC, WK>), dim3((unsigned)((items + 7) / 8 * 8)), dim3(WC * WK * 64), 0, s, a);
+  return hipGetLastError();
+}
 
+constexpr int kBQ = 128, kBP = 128;
 
+// Rows per expert on average; the runs themselves are known on the device only.
+int64_t mean_rows(const LinearArgs& a) { return (a.rows + a.E - 1) / a.E; }
+
+// Rows per expert up to which the depth-split kernel is taken.
+constexpr int64_t kFewRows = 32;
+
+template <bool FP8, bool GATED>
+hipError_t forward_by_shape(const LinearArgs& a, hipStream_t s) {
+  if (mean_rows(a) <= kFewRows) return a.y_scale != nullptr ? run_few<FP8, GATED, 8, 2>(a, s) : run_few<FP8, GATED, 1, 16>(a, s);
+  // 256-wide tiles read each operand byte half as often as 128-wide ones, but are
+  // four times the work: taken where they fill the GPU and the runs fill them
+  const int64_t tiles = (a.rows / 256 + 1) * ((a.parts * (int64_t)a.N + 255) / 256);
+  const bool codes = a.y_scale != nullptr;  // a SwiGLU tile with whole scale blocks has 256 weight rows
+  if constexpr (FP8 && GATED) {
+    if (tiles >= 128 || codes) return run_forward<FP8, GATED, 128, 256, 2, 4, 128, 2>(a, s);
+  } else if constexpr (!FP8) {
+    if ((tiles >= 256 && mean_rows(a) >= 160) || (GATED && codes)) return run_forward<FP8, GATED, 256, 256, 2, 4, 128, 2>(a, s);
+  }
+  return run_forward<FP8, GATED, 128, 128, 2, 2, 128, 2>(a, s);
+}
+
+// The weight gradient's tiles: 256 x 256 where they fill the GPU, else 128 x 128.
+bool big_w_tiles(int E, int N, int K, int parts) {
+  return (int64_t)E * parts * ((N + 255) / 256) * ((K + 255) / 256) >= 256;
+}
 }  // namespace
 
 hipError_t launch_linear(const LinearArgs& a, bool fp8, hipStream_t s) {
-  if (fp8) return a.parts == 2 ? run_forward<true, true, 128, 256, 2, 4, 128, 2>(a, s) : run_forward<true, false, 128, 128, 2, 2, 128, 2>(a, s);
-  return a.parts == 2 ? run_forward<false, true, 128, 256, 2, 4, 64, 3>(a, s) : run_forward<false, false, 128, 128, 2, 2, 128, 2>(a, s);
+  if (fp8) return a.parts == 2 ? forward_by_shape<true, true>(a, s) : forward_by_shape<true, false>(a, s);
+  return a.parts == 2 ? forward_by_shape<false, true>(a, s) : forward_by_shape<false, false>(a, s);
 }
 
 hipError_t launch_linear_backward_x(const LinearArgs& a, hipStream_t s) {
   static std::atomic<size_t> allowed[kMaxCachedDevices];
   const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, kBQ) * ((a.K + kBP - 1) / kBP);
-  return launch(linear_backward_x_kernel<kBQ, kBP, 2, 2, kStages>, items, 256, kStages * (kBQ + kBP) * 128, a, s, allowed);
+  return launch(&linear_backward_x_kernel<kBQ, kBP, 2, 2, 2>, items, 256, 2 * (kBQ + kBP) * 128, a, s, allowed);
 }
 
 int backward_w_splits(int64_t rows, int E, int N, int K, int parts) {
+  if (big_w_tiles(E, N, K, parts)) return 1;
   const int64_t tiles = (int64_t)E * parts * ((N + kBQ - 1) / kBQ) * ((K + kBP - 1) / kBP);
   if (tiles >= 256) return 1;
   // workgroups for two rounds of the GPU, as long as a split keeps 256 rows on average
   return (int)std::max<int64_t>(1, std::min<int64_t>((512 + tiles - 1) / tiles, rows / E / 256));
 }
 
-hipError_t launch_linear_backward_w(const LinearArgs& a, hipStream_t s) {
+template <int BQ, int BP, int WQ, int WP>
+hipError_t run_backward_w(const LinearArgs& a, hipStream_t s) {
   static std::atomic<size_t> allowed[kMaxCachedDevices];
-  const int64_t items = (int64_t)a.E * a.parts * ((a.N + kBQ - 1) / kBQ) * ((a.K + kBP - 1) / kBP) * a.splits;
-  const hipError_t e =
-      launch(linear_backward_w_kernel<kBQ, kBP, 2, 2, kStages>, items, 256, kStages * (kBQ + kBP) * 128, a, s, allowed);
+  const int64_t items = (int64_t)a.E * a.parts * ((a.N + BQ - 1) / BQ) * ((a.K + BP - 1) / BP) * a.splits;
+  return launch(&linear_backward_w_kernel<BQ, BP, WQ, WP, 2>, items, WQ * WP * 64, 2 * (BQ + BP) * 128, a, s, allowed);
+}
+
+hipError_t launch_linear_backward_w(const LinearArgs& a, hipStream_t s) {
+  const hipError_t e = big_w_tiles(a.E, a.N, a.K, a.parts) ? run_backward_w<256, 256, 2, 4>(a, s) : run_backward_w<kBQ, kBP, 2, 2>(a, s);
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t total = (int64_t)a.parts * a.E * a.N * (a.K + (a.db[0] != nullptr ? 1 : 0));
   hipLaunchKernelGGL(join_splits_kernel, dim3((unsigned)((total / 4 + 255) / 256)), dim3(256), 0, s, a);

@@ -28,8 +28,6 @@ namespace tile {
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 using mma::bf16x8;
 using mma::f32x4;
 
@@ -141,9 +139,15 @@ struct RowTile {
   static constexpr int kLoads = kBytes / 1024 / WAVES;
   static constexpr int kPieces = DB / 16;
   static_assert(kBytes % (1024 * WAVES) == 0, "whole loads per wave");
-  // Piece g of line r sits at g ^ swz(r): 256 bytes of LDS hold 256 / DB lines, and
-  // the 16 lines a wave reads at one piece index land on 16 different pieces of them.
-  __device__ static __forceinline__ int swz(int r) { return (r / (256 / DB)) & (kPieces - 1); }
+  static_assert(DB == 64 || DB == 128, "line lengths the swizzle is made for");
+  // Piece g of line r sits at g ^ swz(r).  256 bytes of LDS (all banks) hold 256 /
+  // DB lines; a 16-byte read is served 16 lanes at a time, lanes 0-3 and 12-15 of
+  // one quad together with lanes 4-11 of the next, and both forms put those on 16
+  // different pieces (measured: no bank conflicts; r / 4 for the 64-byte lines
+  // conflicted on half of the cycles).
+  __device__ static __forceinline__ int swz(int r) {
+    return DB == 64 ? -(r / 4) & 3 : (r / 2) & 7;
+  }
 
   uint32_t off[kLoads];  // this lane's byte offset of each of its loads at depth 0, or kNoFetch
   int piece;             // and the depth byte its piece starts at
@@ -163,13 +167,16 @@ struct RowTile {
     // loads take the same piece where the loads are that far apart
     static_assert(kLoads == 1 || (WAVES * kLines) % (kPieces * (256 / DB)) == 0, "one piece index per lane");
   }
-  // Fill `lds` from depth byte `d` on; pieces at or past `left` bytes from there are zero.
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* lds, int wave, uint32_t d, int left) const {
+  // Fill `lds` from depth byte `d` on; pieces at or past `left` bytes from there are
+  // zero.  Loads of lines at or past `live` (the same for the workgroup) are not
+  // issued: what LDS holds there feeds only output rows that are not stored.
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* lds, int wave, uint32_t d, int left, int live = R) const {
     const bool cut = piece >= left;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (i * WAVES + wave) * 1024), 16,
-                                               cut ? kNoFetch : off[i], d, 0, 0);
+      if ((i * WAVES + wave) * kLines < live)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (i * WAVES + wave) * 1024), 16,
+                                                 cut ? kNoFetch : off[i], d, 0, 0);
   }
   // Piece g of line r.
   __device__ static __forceinline__ const char* at(const char* lds, int r, int g) {
@@ -179,11 +186,17 @@ struct RowTile {
   __device__ static __forceinline__ bf16x8 frag(const char* lds, int r0, int kk, int lane) {
     return *reinterpret_cast<const bf16x8*>(at(lds, r0 + (lane & 15), kk * 4 + (lane >> 4)));
   }
-  // 32 bytes of 8-bit depth elements (pieces q and q + 4) for operand row r0 + l % 16.
-  __device__ static __forceinline__ i32x8 frag8(const char* lds, int r0, int lane) {
-    const i32x4 lo = *reinterpret_cast<const i32x4*>(at(lds, r0 + (lane & 15), lane >> 4));
-    const i32x4 hi = *reinterpret_cast<const i32x4*>(at(lds, r0 + (lane & 15), (lane >> 4) + 4));
-    return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  // A stage of 128 8-bit depth elements for operand row r0 + l % 16, as the bf16
+  // operands of four 32-deep steps: pieces q and q + 4, 16 elements each (e4m3 is
+  // exact in bf16; which element meets which step does not matter as long as both
+  // operands agree).
+  __device__ static __forceinline__ void frag8(const char* lds, int r0, int lane, bf16x8 (&f)[4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 v = *reinterpret_cast<const uint4*>(at(lds, r0 + (lane & 15), (lane >> 4) + 4 * h));
+      f[2 * h] = mma::fp8x8_to_bf16(v.x, v.y);
+      f[2 * h + 1] = mma::fp8x8_to_bf16(v.z, v.w);
+    }
   }
 };
 

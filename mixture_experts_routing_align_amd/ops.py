@@ -58,44 +58,61 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> int:
+# The decode-width kernels take 2-5 us, so the binding keeps its own share small:
+# the raw handle of the current stream and the device index are read from torch's
+# C layer (0.1 us each; torch.cuda.current_stream() builds an object, 2.8 us), and
+# each tensor is checked in one expression that only a refusal looks into.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _stream(stream, dev: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(dev)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
 
 
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """A device tensor whose memory belongs to the stream the call runs on."""
+def _device(t, what: str) -> int:
+    """Index of the GPU `t` lives on, which must be the current one."""
+    _need(isinstance(t, torch.Tensor), f"{what} must be a tensor")
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{what} must be on the current GPU")
+    return dev
+
+
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """A tensor on the device of `like` whose memory belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        if dtype is like.dtype and shape == like.shape:
+            return torch.empty_like(like, memory_format=torch.contiguous_format)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _matrix(t, what: str, dtypes, shape=None) -> None:
-    """`t` is a contiguous tensor of one of `dtypes` (and `shape`) on the current device."""
+def _matrix(t, what: str, dtypes, shape, dev: int) -> None:
+    """`t` is a contiguous tensor of one of `dtypes` and of `shape` (None: any) on device `dev`."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and (shape is None or t.shape == shape) and t.is_contiguous()
+            and t.get_device() == dev):
+        return
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         raise ValueError(f"{what} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    _on_device(t, what)
+    raise ValueError(f"{what} must be on the current GPU")
 
 
-def _on_device(t, what: str) -> None:
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} must be on the current GPU")
-
-
-def _out(t, shape, dtype, device, stream, what: str) -> torch.Tensor:
+def _out(t, shape, dtype, like, stream, what: str, dev: int) -> torch.Tensor:
     if t is None:
-        return _new(shape, dtype, device, stream)
-    _matrix(t, what, (dtype,), shape)
+        return _new(shape, dtype, like, stream)
+    _matrix(t, what, (dtype,), shape, dev)
     return t
 
 
@@ -103,6 +120,9 @@ _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _E4M3 = torch.float8_e4m3fn
+_STREAM = (torch.bfloat16, torch.float32)
+_ROWS = (torch.bfloat16, _E4M3)
+_WEIGHTS = (torch.bfloat16, torch.uint8, _E4M3)
 
 
 # -------------------------------------------------------------------- norm --
@@ -122,27 +142,26 @@ def moe_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual
     M, H = x.shape
     ldx = x.stride(0) if M > 1 else H
     _need((H == 1 or x.stride(1) == 1) and ldx >= H, "x must have contiguous rows that do not overlap")
-    _on_device(x, "x")
-    _matrix(weight, "weight", _BF16, (H,))
-    dev = x.device
+    dev = _device(x, "x")
+    _matrix(weight, "weight", _BF16, (H,), dev)
     rdt = MOE_DT_BF16
     if residual is not None:
-        _matrix(residual, "residual", (torch.bfloat16, torch.float32), (M, H))
+        _matrix(residual, "residual", _STREAM, (M, H), dev)
         rdt = _STREAM_TYPES[residual.dtype]
-        residual_out = _out(residual_out, (M, H), residual.dtype, dev, stream, "residual_out")
+        residual_out = _out(residual_out, (M, H), residual.dtype, residual, stream, "residual_out", dev)
     else:
         _need(residual_out is None, "residual_out without residual")
     _need(not fp8 or H % BLOCK == 0, "8-bit rows need H in whole blocks of 128")
-    out = _out(out, (M, H), _E4M3 if fp8 else torch.bfloat16, dev, stream, "out")
+    out = _out(out, (M, H), _E4M3 if fp8 else torch.bfloat16, x, stream, "out", dev)
     if fp8:
-        out_scale = _out(out_scale, (M, H // BLOCK), torch.float32, dev, stream, "out_scale")
+        out_scale = _out(out_scale, (M, H // BLOCK), torch.float32, x, stream, "out_scale", dev)
     else:
         _need(out_scale is None, "out_scale without fp8")
     if save_rstd or rstd is not None:
-        rstd = _out(rstd, (M,), torch.float32, dev, stream, "rstd")
+        rstd = _out(rstd, (M,), torch.float32, x, stream, "rstd", dev)
     _check(_ffi.load().moe_add_rms_norm(
         x.data_ptr(), ldx, _ptr(residual), rdt, _ptr(residual_out), weight.data_ptr(), eps, out.data_ptr(),
-        MOE_DT_E4M3 if fp8 else MOE_DT_BF16, _ptr(out_scale), _ptr(rstd), M, H, _stream(stream)))
+        MOE_DT_E4M3 if fp8 else MOE_DT_BF16, _ptr(out_scale), _ptr(rstd), M, H, _stream(stream, dev)))
     return out, out_scale, residual_out, rstd
 
 
@@ -153,32 +172,33 @@ def moe_add_rms_norm_backward(dy: torch.Tensor, z: torch.Tensor, weight: torch.T
     stream, dz (type of z): ``(dx, dweight)``, dx (type of z) for x and the
     residual alike, dweight float32 [H] (None without `need_dweight`).  z is what
     the forward call returned (x itself where there was no residual)."""
-    _matrix(z, "z", (torch.bfloat16, torch.float32))
+    dev = _device(z, "z")
+    _matrix(z, "z", _STREAM, None, dev)
     _need(z.dim() == 2, "z must be [M, H]")
     M, H = z.shape
-    _matrix(dy, "dy", _BF16, (M, H))
-    _matrix(weight, "weight", _BF16, (H,))
-    _matrix(rstd, "rstd", _F32, (M,))
+    _matrix(dy, "dy", _BF16, (M, H), dev)
+    _matrix(weight, "weight", _BF16, (H,), dev)
+    _matrix(rstd, "rstd", _F32, (M,), dev)
     if dz is not None:
-        _matrix(dz, "dz", (z.dtype,), (M, H))
-    dx = _out(dx, (M, H), z.dtype, z.device, stream, "dx")
+        _matrix(dz, "dz", (z.dtype,), (M, H), dev)
+    dx = _out(dx, (M, H), z.dtype, z, stream, "dx", dev)
     dweight = ws = None
     nbytes = 0
     lib = _ffi.load()
     if need_dweight:
-        dweight = _new((H,), torch.float32, z.device, stream)
+        dweight = _new((H,), torch.float32, z, stream)
         nbytes = lib.moe_add_rms_norm_backward_workspace_bytes(M, H)
-        ws = _new((nbytes,), torch.uint8, z.device, stream) if nbytes else None
+        ws = _new((nbytes,), torch.uint8, z, stream) if nbytes else None
     _check(lib.moe_add_rms_norm_backward(
         dy.data_ptr(), z.data_ptr(), _STREAM_TYPES[z.dtype], weight.data_ptr(), rstd.data_ptr(), _ptr(dz),
-        dx.data_ptr(), _ptr(dweight), M, H, _ptr(ws), nbytes, _stream(stream)))
+        dx.data_ptr(), _ptr(dweight), M, H, _ptr(ws), nbytes, _stream(stream, dev)))
     return dx, dweight
 
 
 # ---------------------------------------------- rows by expert, back again --
 
-def _slots(token_to_perm, top_k: int) -> int:
-    _matrix(token_to_perm, "token_to_perm", _I32)
+def _slots(token_to_perm, top_k: int, dev: int) -> int:
+    _matrix(token_to_perm, "token_to_perm", _I32, None, dev)
     _need(top_k >= 1 and token_to_perm.numel() % top_k == 0, "token_to_perm must hold M * top_k entries")
     return token_to_perm.numel() // top_k
 
@@ -190,8 +210,9 @@ def moe_permute(x: torch.Tensor, token_to_perm: torch.Tensor, top_k: int, rows: 
     `scale`.  `rows` is the height of the sorted matrix (the length of
     ``AlignTables.sorted_token_ids``).  Returns ``(out, out_scale)`` (None for
     bf16).  The gradient is moe_unpermute without weights."""
-    M = _slots(token_to_perm, top_k)
-    _matrix(x, "x", (torch.bfloat16, _E4M3))
+    dev = _device(x, "x")
+    M = _slots(token_to_perm, top_k, dev)
+    _matrix(x, "x", _ROWS, None, dev)
     _need(x.dim() == 2 and x.shape[0] == M, "x must be [M, H]")
     _need(rows >= 0, "rows must not be negative")
     H = x.shape[1]
@@ -199,14 +220,14 @@ def moe_permute(x: torch.Tensor, token_to_perm: torch.Tensor, top_k: int, rows: 
     _need(fp8 == (scale is not None), "8-bit rows come with scales, bf16 rows without")
     if fp8:
         _need(H % BLOCK == 0, "8-bit rows need H in whole blocks of 128")
-        _matrix(scale, "scale", _F32, (M, H // BLOCK))
-        out_scale = _out(out_scale, (rows, H // BLOCK), torch.float32, x.device, stream, "out_scale")
+        _matrix(scale, "scale", _F32, (M, H // BLOCK), dev)
+        out_scale = _out(out_scale, (rows, H // BLOCK), torch.float32, x, stream, "out_scale", dev)
     else:
         _need(out_scale is None, "out_scale without 8-bit rows")
-    out = _out(out, (rows, H), x.dtype, x.device, stream, "out")
+    out = _out(out, (rows, H), x.dtype, x, stream, "out", dev)
     _check(_ffi.load().moe_permute(x.data_ptr(), MOE_DT_E4M3 if fp8 else MOE_DT_BF16, _ptr(scale),
                                    token_to_perm.data_ptr(), M, top_k, H, out.data_ptr(), _ptr(out_scale), rows,
-                                   _stream(stream)))
+                                   _stream(stream, dev)))
     return out, out_scale
 
 
@@ -216,15 +237,16 @@ def moe_unpermute(y: torch.Tensor, token_to_perm: torch.Tensor, top_k: int,
     """out[t] = sum_k w[t, k] y[token_to_perm[t*top_k + k]], bf16 [M, H], slots
     without a row skipped; without weights every weight is 1 (the gradient of
     moe_permute)."""
-    M = _slots(token_to_perm, top_k)
-    _matrix(y, "y", _BF16)
+    dev = _device(y, "y")
+    M = _slots(token_to_perm, top_k, dev)
+    _matrix(y, "y", _BF16, None, dev)
     _need(y.dim() == 2, "y must be [rows, H]")
     rows, H = y.shape
     if topk_weights is not None:
-        _matrix(topk_weights, "topk_weights", _F32, (M, top_k))
-    out = _out(out, (M, H), torch.bfloat16, y.device, stream, "out")
+        _matrix(topk_weights, "topk_weights", _F32, (M, top_k), dev)
+    out = _out(out, (M, H), torch.bfloat16, y, stream, "out", dev)
     _check(_ffi.load().moe_unpermute(y.data_ptr(), token_to_perm.data_ptr(), _ptr(topk_weights), M, top_k, H,
-                                     out.data_ptr(), rows, _stream(stream)))
+                                     out.data_ptr(), rows, _stream(stream, dev)))
     return out
 
 
@@ -234,47 +256,51 @@ def moe_unpermute_backward(dout: torch.Tensor, y: torch.Tensor, token_to_perm: t
     """Gradients of the weighted moe_unpermute: ``(dy, dweights)``, dy bf16
     [rows, H] (may be `y` itself), dweights float32 [M, top_k] (0 for a slot
     without a row)."""
-    _matrix(topk_weights, "topk_weights", _F32)
+    dev = _device(y, "y")
+    _matrix(topk_weights, "topk_weights", _F32, None, dev)
     _need(topk_weights.dim() == 2, "topk_weights must be [M, top_k]")
     M, top_k = topk_weights.shape
-    _matrix(token_to_perm, "token_to_perm", _I32)
+    _matrix(token_to_perm, "token_to_perm", _I32, None, dev)
     _need(token_to_perm.numel() == M * top_k, "token_to_perm must hold M * top_k entries")
-    _matrix(y, "y", _BF16)
+    _matrix(y, "y", _BF16, None, dev)
     _need(y.dim() == 2, "y must be [rows, H]")
     rows, H = y.shape
-    _matrix(dout, "dout", _BF16, (M, H))
-    dy = _out(dy, (rows, H), torch.bfloat16, y.device, stream, "dy")
-    dweights = _out(dweights, (M, top_k), torch.float32, y.device, stream, "dweights")
+    _matrix(dout, "dout", _BF16, (M, H), dev)
+    dy = _out(dy, (rows, H), torch.bfloat16, y, stream, "dy", dev)
+    dweights = _out(dweights, (M, top_k), torch.float32, y, stream, "dweights", dev)
     _check(_ffi.load().moe_unpermute_backward(dout.data_ptr(), y.data_ptr(), token_to_perm.data_ptr(),
                                               topk_weights.data_ptr(), M, top_k, H, dy.data_ptr(),
-                                              dweights.data_ptr(), rows, _stream(stream)))
+                                              dweights.data_ptr(), rows, _stream(stream, dev)))
     return dy, dweights
 
 
 # ---------------------------------------------------- the experts' products --
 
-def _runs(expert_offsets, expert_counts, E: int) -> None:
-    _need((expert_offsets is None) == (expert_counts is None), "expert_offsets and expert_counts go together")
-    if expert_offsets is None:
+def _runs(expert_offsets, expert_counts, E: int, dev: int) -> None:
+    if expert_offsets is None and expert_counts is None:
         _need(E == 1, "without expert_offsets there is one expert")
         return
-    _matrix(expert_counts, "expert_counts", _I32, (E,))
-    _matrix(expert_offsets, "expert_offsets", _I32, (E + 1,))
+    _need(expert_offsets is not None and expert_counts is not None, "expert_offsets and expert_counts go together")
+    _matrix(expert_counts, "expert_counts", _I32, (E,), dev)
+    _matrix(expert_offsets, "expert_offsets", _I32, (E + 1,), dev)
 
 
-def _expert_weight(wt, what: str):
+def _expert_weight(wt, what: str, dev: int):
     """(codes or bf16 [E, N, K], scales or None, E, N, K) of a weight pair or a bare bf16 tensor."""
     w, s = wt if isinstance(wt, tuple) else (wt, None)
-    _matrix(w, what, (torch.bfloat16, torch.uint8, _E4M3))
-    _need(w.dim() in (2, 3), f"{what} must be [E, N, K] or [N, K]")
-    E, N, K = (1,) + tuple(w.shape) if w.dim() == 2 else tuple(w.shape)
-    if w.dtype == torch.bfloat16:
-        _need(s is None, f"bf16 {what} takes no scales")
+    _matrix(w, what, _WEIGHTS, None, dev)
+    if w.dim() == 3:
+        E, N, K = w.shape
     else:
-        _need(N % BLOCK == 0 and K % BLOCK == 0, f"8-bit {what} comes in whole 128x128 blocks")
+        _need(w.dim() == 2, what + " must be [E, N, K] or [N, K]")
+        E, (N, K) = 1, w.shape
+    if w.dtype == torch.bfloat16:
+        _need(s is None, "bf16 weights take no scales")
+    else:
+        _need(N % BLOCK == 0 and K % BLOCK == 0, "8-bit weights come in whole 128x128 blocks")
         lead = () if w.dim() == 2 else (E,)
-        _need(s is not None, f"8-bit {what} needs float32 scales, one per 128x128 block")
-        _matrix(s, f"{what} scales", _F32, lead + (N // BLOCK, K // BLOCK))
+        _need(s is not None, "8-bit weights need float32 scales, one per 128x128 block")
+        _matrix(s, what + " scales", _F32, lead + (N // BLOCK, K // BLOCK), dev)
     return w, s, E, N, K
 
 
@@ -294,48 +320,48 @@ def moe_grouped_linear(x: torch.Tensor, w, expert_offsets: Optional[torch.Tensor
     `fp8_out` (or an 8-bit `out`) 8-bit rows with their scales; preact, with
     `save_preact` or given as a buffer, the bf16 pre-activations ([rows, 2N] for
     swiglu) that moe_grouped_act_backward takes."""
-    _need(act in ACTIVATIONS, f"act must be one of {', '.join(ACTIVATIONS)}")
+    _need(act in ACTIVATIONS, "act must be one of none, silu, gelu, swiglu")
     gated = act == "swiglu"
-    wt, ws, E, N, K = _expert_weight(w, "w")
-    _runs(expert_offsets, expert_counts, E)
+    dev = _device(x, "x")
+    wt, ws, E, N, K = _expert_weight(w, "w", dev)
+    _runs(expert_offsets, expert_counts, E, dev)
     fp8 = wt.dtype != torch.bfloat16
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be [rows, K]")
+    _need(x.dim() == 2, "x must be [rows, K]")
     rows = x.shape[0]
-    _matrix(x, "x", (_E4M3,) if fp8 else _BF16, (rows, K))
+    _matrix(x, "x", (_E4M3,) if fp8 else _BF16, (rows, K), dev)
     _need(fp8 == (x_scale is not None), "8-bit rows come with x_scale, bf16 rows without")
     if fp8:
-        _matrix(x_scale, "x_scale", _F32, (rows, K // BLOCK))
+        _matrix(x_scale, "x_scale", _F32, (rows, K // BLOCK), dev)
     _need(gated == (up is not None), "up goes with act='swiglu'")
     ut = us = None
     if gated:
-        ut, us, E2, N2, K2 = _expert_weight(up, "up")
+        ut, us, E2, N2, K2 = _expert_weight(up, "up", dev)
         _need((E2, N2, K2) == (E, N, K) and ut.dtype == wt.dtype, "up must match w")
     else:
         _need(up_bias is None, "up_bias goes with act='swiglu'")
     if bias is not None:
-        _matrix(bias, "bias", _BF16)
+        _matrix(bias, "bias", _BF16, None, dev)
         _need(bias.numel() == E * N, "bias must be [E, N]")
     if up_bias is not None:
         _need(bias is not None, "up_bias goes with bias")
-        _matrix(up_bias, "up_bias", _BF16)
+        _matrix(up_bias, "up_bias", _BF16, None, dev)
         _need(up_bias.numel() == E * N, "up_bias must be [E, N]")
     if residual is not None:
-        _matrix(residual, "residual", _BF16, (rows, N))
-    dev = x.device
+        _matrix(residual, "residual", _BF16, (rows, N), dev)
     fp8_out = fp8_out or (out is not None and out.dtype == _E4M3)
     _need(not fp8_out or N % BLOCK == 0, "8-bit rows need N in whole blocks of 128")
-    out = _out(out, (rows, N), _E4M3 if fp8_out else torch.bfloat16, dev, stream, "out")
+    out = _out(out, (rows, N), _E4M3 if fp8_out else torch.bfloat16, x, stream, "out", dev)
     if fp8_out:
-        out_scale = _out(out_scale, (rows, N // BLOCK), torch.float32, dev, stream, "out_scale")
+        out_scale = _out(out_scale, (rows, N // BLOCK), torch.float32, x, stream, "out_scale", dev)
     else:
         _need(out_scale is None, "out_scale without 8-bit output")
     if save_preact or preact is not None:
-        preact = _out(preact, (rows, (2 if gated else 1) * N), torch.bfloat16, dev, stream, "preact")
+        preact = _out(preact, (rows, (2 if gated else 1) * N), torch.bfloat16, x, stream, "preact", dev)
     d = MoeLinearDesc(rows, E, N, K, MOE_W_FP8_E4M3 if fp8 else MOE_W_BF16, ACTIVATIONS[act],
                       MOE_DT_E4M3 if fp8_out else MOE_DT_BF16, _ptr(expert_offsets), _ptr(expert_counts),
                       x.data_ptr(), _ptr(x_scale), MoeWeight(wt.data_ptr(), _ptr(ws)), MoeWeight(_ptr(ut), _ptr(us)),
                       _ptr(bias), _ptr(up_bias), _ptr(residual), out.data_ptr(), _ptr(out_scale), _ptr(preact))
-    _check(_ffi.load().moe_grouped_linear(ctypes.byref(d), _stream(stream)))
+    _check(_ffi.load().moe_grouped_linear(ctypes.byref(d), _stream(stream, dev)))
     return out, out_scale, preact
 
 
@@ -346,17 +372,18 @@ def moe_grouped_act_backward(dy: torch.Tensor, preact: torch.Tensor, act: str,
     """The gradient of the pre-activations from that of act's result: bf16, the
     shape of `preact` (which may be `dz` itself)."""
     _need(act in ("silu", "gelu", "swiglu"), "act must be silu, gelu or swiglu")
-    _matrix(dy, "dy", _BF16)
+    dev = _device(dy, "dy")
+    _matrix(dy, "dy", _BF16, None, dev)
     _need(dy.dim() == 2, "dy must be [rows, N]")
     rows, N = dy.shape
     wide = 2 if act == "swiglu" else 1
-    _matrix(preact, "preact", _BF16, (rows, wide * N))
+    _matrix(preact, "preact", _BF16, (rows, wide * N), dev)
     E = 1 if expert_counts is None else expert_counts.numel()
-    _runs(expert_offsets, expert_counts, E)
-    dz = _out(dz, (rows, wide * N), torch.bfloat16, dy.device, stream, "dz")
+    _runs(expert_offsets, expert_counts, E, dev)
+    dz = _out(dz, (rows, wide * N), torch.bfloat16, preact, stream, "dz", dev)
     _check(_ffi.load().moe_grouped_act_backward(dy.data_ptr(), preact.data_ptr(), ACTIVATIONS[act],
                                                 _ptr(expert_offsets), _ptr(expert_counts), rows, E, N, dz.data_ptr(),
-                                                _stream(stream)))
+                                                _stream(stream, dev)))
     return dz
 
 
@@ -365,20 +392,21 @@ def moe_grouped_linear_backward_x(dz: torch.Tensor, w, expert_offsets: Optional[
                                   dx: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """dx[p] = W[e]^T dz[p], plus W_up[e]^T of dz's second half with `up` (dz
     [rows, 2N]); bf16 throughout."""
-    wt, _, E, N, K = _expert_weight(w, "w")
+    dev = _device(dz, "dz")
+    wt, _, E, N, K = _expert_weight(w, "w", dev)
     _need(wt.dtype == torch.bfloat16, "gradients take bf16 weights")
-    _runs(expert_offsets, expert_counts, E)
+    _runs(expert_offsets, expert_counts, E, dev)
     ut = None
     if up is not None:
-        ut, _, E2, N2, K2 = _expert_weight(up, "up")
+        ut, _, E2, N2, K2 = _expert_weight(up, "up", dev)
         _need((E2, N2, K2) == (E, N, K) and ut.dtype == wt.dtype, "up must match w")
-    _need(isinstance(dz, torch.Tensor) and dz.dim() == 2, "dz must be [rows, N]")
+    _need(dz.dim() == 2, "dz must be [rows, N]")
     rows = dz.shape[0]
-    _matrix(dz, "dz", _BF16, (rows, N if up is None else 2 * N))
-    dx = _out(dx, (rows, K), torch.bfloat16, dz.device, stream, "dx")
+    _matrix(dz, "dz", _BF16, (rows, N if up is None else 2 * N), dev)
+    dx = _out(dx, (rows, K), torch.bfloat16, dz, stream, "dx", dev)
     _check(_ffi.load().moe_grouped_linear_backward_x(dz.data_ptr(), wt.data_ptr(), _ptr(ut), _ptr(expert_offsets),
                                                      _ptr(expert_counts), rows, E, N, K, dx.data_ptr(),
-                                                     _stream(stream)))
+                                                     _stream(stream, dev)))
     return dx
 
 
@@ -391,23 +419,23 @@ def moe_grouped_linear_backward_w(dz: torch.Tensor, x: torch.Tensor, expert_offs
     [E, N, K] of `dtype` (bf16 or float32); with `bias` db float32 [E, N]; with
     `gated` dz is [rows, 2N] and its second half gives dup and dup_b."""
     _need(dtype in _STREAM_TYPES, "dtype must be bfloat16 or float32")
-    _matrix(dz, "dz", _BF16)
-    _matrix(x, "x", _BF16)
+    dev = _device(x, "x")
+    _matrix(dz, "dz", _BF16, None, dev)
+    _matrix(x, "x", _BF16, None, dev)
     _need(dz.dim() == 2 and x.dim() == 2 and dz.shape[0] == x.shape[0], "dz and x must have the same rows")
     rows, K = x.shape
     parts = 2 if gated else 1
     _need(dz.shape[1] % parts == 0, "dz must be [rows, 2N]")
     N = dz.shape[1] // parts
     E = 1 if expert_counts is None else expert_counts.numel()
-    _runs(expert_offsets, expert_counts, E)
-    dev = x.device
-    dw = [_new((E, N, K), dtype, dev, stream) for _ in range(parts)] + [None]
-    db = [_new((E, N), torch.float32, dev, stream) if bias else None for _ in range(parts)] + [None]
+    _runs(expert_offsets, expert_counts, E, dev)
+    dw = [_new((E, N, K), dtype, x, stream) for _ in range(parts)] + [None]
+    db = [_new((E, N), torch.float32, x, stream) if bias else None for _ in range(parts)] + [None]
     lib = _ffi.load()
     nbytes = lib.moe_grouped_linear_backward_w_workspace_bytes(rows, E, N, K, int(gated), int(bias))
-    ws = _new((nbytes,), torch.uint8, dev, stream) if nbytes else None
+    ws = _new((nbytes,), torch.uint8, x, stream) if nbytes else None
     _check(lib.moe_grouped_linear_backward_w(
         dz.data_ptr(), x.data_ptr(), int(gated), _ptr(expert_offsets), _ptr(expert_counts), rows, E, N, K,
         _STREAM_TYPES[dtype], dw[0].data_ptr(), _ptr(dw[1]), _ptr(db[0]), _ptr(db[1]), _ptr(ws), nbytes,
-        _stream(stream)))
+        _stream(stream, dev)))
     return dw[0], dw[1], db[0], db[1]

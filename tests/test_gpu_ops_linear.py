@@ -168,6 +168,52 @@ def test_forward_8bit(moe, rows, act, bias, res, fp8_out, N, K):
     assert_untouched(out, k, "y")
 
 
+# (rows, N, K) that reach the 256-wide tiles and the depth-split kernel of a few rows, whole and partly filled
+WIDE = [(1100, 2048, 264), ((520, 8, 4, 16, "skew", 0.0), 1040, 200), ((700, 6, 4, 1, "random", 0.1), 1032, 136),
+        (33, 520, 264), (64, 136, 2056), ((40, 4, 2, 16, "random", 0.0), 264, 4104), (16, 24, 2184)]
+
+
+@pytest.mark.parametrize("rows,N,K", WIDE, ids=str)
+@pytest.mark.parametrize("act,bias,res,save", [("none", True, True, False), ("swiglu", True, False, True)])
+def test_forward_tiles(moe, rows, N, K, act, bias, res, save):
+    test_forward(moe, rows, act, bias, res, save, N, K)
+
+
+@pytest.mark.parametrize("rows", [1, 40, 300, (70, 6, 3, 16, "skew", 0.1), (600, 4, 2, 16, "random", 0.0)], ids=str)
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("N,K", [(128, 136), (640, 520)])
+def test_bf16_operands_to_8bit_rows(moe, rows, act, N, K):
+    r = rows_of(moe, rows, N)
+    g = gen(N + K)
+    gated = act == "swiglu"
+    x = poison(randn(g, r.rows, K), r.kept)
+    w = (randn(g, r.E, N, K, scale=K ** -0.5), None)
+    up = (randn(g, r.E, N, K, scale=K ** -0.5), None) if gated else None
+    out = untouched_buffer(r.rows, N, dtype=torch.float8_e4m3fn)
+    out_scale = untouched_buffer(r.rows, N // BLOCK, dtype=torch.float32)
+    moe.moe_grouped_linear(x, w, r.offsets, r.counts, act=act, up=up, out=out, out_scale=out_scale)
+    torch.cuda.synchronize()
+    ref, err, _, _ = reference(r, x.double(), w, up, None, None, None, act)
+    k = r.kept
+    check_fp8_rows(out.view(torch.uint8)[k], out_scale[k], ref[k], err[k], "y")
+    assert_untouched(out, k, "y")
+    assert_untouched(out_scale, k, "y_scale")
+
+
+@pytest.mark.parametrize("rows", [1, 33, 300, (700, 6, 4, 1, "skew", 0.1)], ids=str)
+@pytest.mark.parametrize("fp8_out", [False, True])
+def test_8bit_wide_depth(moe, rows, fp8_out):
+    """Scales of a small and a large block stay exact to float32 sums: each scale
+    holds to the bound of the products."""
+    test_forward_8bit(moe, rows, "swiglu", False, False, fp8_out, 256, 2048)
+
+
+@pytest.mark.parametrize("rows,N,K,gated", [((520, 32, 4, 16, "skew", 0.0), 1040, 520, False),
+                                            ((300, 16, 4, 16, "random", 0.0), 600, 1032, True)], ids=str)
+def test_backward_tiles(moe, rows, N, K, gated):
+    test_backward(moe, rows, gated, N, K)
+
+
 @pytest.mark.parametrize("rows", ROWS, ids=str)
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("N,K", [(8, 8), (200, 520), (520, 264)])
