@@ -42,7 +42,8 @@ __device__ __forceinline__ uint2 pack4(const float (&f)[4]) { return make_uint2(
 // ---------------------------------------------------------------- forward --
 
 // 4 consecutive columns n ... n + 3 of row r of expert e: bias, activation and
-// residual on float32 sums (z and u are rounded only into preact), `in`: stored.
+// residual on float32 sums; z and u come back as the pre-activations.  `in`: the
+// columns and the row exist.
 template <bool GATED>
 __device__ __forceinline__ void epilogue4(const LinearArgs& a, int e, int64_t r, int n, bool in, float (&z)[4], float (&u)[4],
                                           float (&y)[4]) {
@@ -58,14 +59,9 @@ __device__ __forceinline__ void epilogue4(const LinearArgs& a, int e, int64_t r,
 #pragma unroll
       for (int c = 0; c < 4; ++c) u[c] += f[c];
     }
-    if (a.preact != nullptr && in) {
-      *reinterpret_cast<uint2*>(a.preact + r * 2 * a.N + n) = pack4(z);
-      *reinterpret_cast<uint2*>(a.preact + r * 2 * a.N + a.N + n) = pack4(u);
-    }
 #pragma unroll
     for (int c = 0; c < 4; ++c) y[c] = silu(z[c]) * u[c];
   } else {
-    if (a.preact != nullptr && in) *reinterpret_cast<uint2*>(a.preact + r * a.N + n) = pack4(z);
     if (a.act == MOE_ACT_SILU) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) y[c] = silu(z[c]);
@@ -84,12 +80,10 @@ __device__ __forceinline__ void epilogue4(const LinearArgs& a, int e, int64_t r,
   }
 }
 
-// 4 columns of an 8-bit row (n a multiple of 4), and the block's scale with its first.
-__device__ __forceinline__ void store_codes(const LinearArgs& a, int64_t r, int n, const float (&y)[4], float scale) {
-  uint32_t code = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] / scale, y[1] / scale, 0, false);
-  code = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] / scale, y[3] / scale, code, true);
-  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + r * a.N + n) = code;
-  if (n % row::kScaleBlock == 0) a.y_scale[r * (a.N / row::kScaleBlock) + n / row::kScaleBlock] = scale;
+// 4 values over their block's scale as e4m3fn codes.
+__device__ __forceinline__ uint32_t codes4(const float (&y)[4], float scale) {
+  const uint32_t lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] / scale, y[1] / scale, 0, false);
+  return __builtin_amdgcn_cvt_pk_fp8_f32(y[2] / scale, y[3] / scale, lo, true);
 }
 
 // Calls f with the smallest of kQ / 4, kQ / 2, 3 kQ / 4 and kQ subtiles that covers `live`.
@@ -109,8 +103,9 @@ __device__ __forceinline__ void by_live_subtiles(int live, F f) {
 
 // A workgroup's tile: BQ rows by BP weight rows (SwiGLU: BP / 2 of the gate and
 // the same BP / 2 of the up weight, so that a lane holds z and u of its elements),
-// WQ x WP waves, DB bytes of depth per stage, STAGES stages in LDS.
-template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int STAGES>
+// WQ x WP waves, DB bytes of depth per stage, QS stages of rows and PS of weights
+// in LDS.
+template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int QS, int PS>
 struct Forward {
   static constexpr int kWaves = WQ * WP, kThreads = kWaves * 64;
   static constexpr int kParts = GATED ? 2 : 1;
@@ -120,10 +115,20 @@ struct Forward {
   static constexpr int kC = kP / kParts;         // of them per part
   using QTile = RowTile<BQ, DB, kWaves>;
   using PTile = RowTile<kCols, DB, kWaves>;
-  static constexpr int kStage = QTile::kBytes + kParts * PTile::kBytes;
-  static constexpr int kLoads = QTile::kLoads + kParts * PTile::kLoads;
-  static constexpr int kLds = kStage * STAGES;
+  static constexpr int kPBytes = kParts * PTile::kBytes;
+  static constexpr int kPLoads = kParts * PTile::kLoads;
+  static constexpr int kLds = QS * QTile::kBytes + PS * kPBytes;
 };
+
+// Loads of a wave that may be outstanding when step s begins.  Each step issues the
+// rows of step s + QS - 1 and then the weights of step s + PS - 1.  With two stages
+// of rows only weights may be: those of step s + 1 where there is a third weight
+// stage (weights come from HBM, rows mostly from L2, where several column tiles read
+// them).  With more stages of rows there are as many of weights, and all stages but
+// the next may be.
+constexpr int in_flight(int QS, int PS, int q_loads, int p_loads) {
+  return QS == 2 ? (PS - 2) * p_loads : (PS - 2) * (q_loads + p_loads);
+}
 
 // Rows of a tile are dealt to the WQ rows of waves in subtiles of 16 in turn, so a
 // partly filled tile leaves every wave the same share (at most one subtile apart);
@@ -131,9 +136,10 @@ struct Forward {
 template <int WQ>
 __device__ __forceinline__ int q_row(int wq, int i) { return (i * WQ + wq) * 16; }
 
-template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int STAGES>
+template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int QS, int PS>
 __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
-  using T = Forward<FP8, GATED, BQ, BP, WQ, WP, DB, STAGES>;
+  using T = Forward<FP8, GATED, BQ, BP, WQ, WP, DB, QS, PS>;
+  static_assert((QS == 2 && (PS == 2 || PS == 3)) || (QS > 2 && QS == PS), "the waits are counted for these");
   constexpr int kQ = T::kQ, kP = T::kP, kC = T::kC, kParts = T::kParts, kCols = T::kCols;
   static_assert(!FP8 || DB == row::kScaleBlock, "a stage of 8-bit depth is one scale block");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -155,12 +161,16 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
   qt.init(wave, lane, [&](int r) { return r < live ? (uint32_t)(r * ld) : kNoFetch; });
   pt.init(wave, lane, [&](int r) { return p0 + r < a.N ? (uint32_t)((p0 + r) * ld) : kNoFetch; });
   const int steps = (ld + DB - 1) / DB;
-  auto issue = [&](int s, int stage) {
-    char* b = smem + stage * T::kStage;
-    const int left = ld - s * DB;  // not positive past the last step: zeros
-    qt.load(rx, b, wave, s * DB, left, STAGES == 2 ? live : BQ);
+  // past the last step nothing is left: the loads are issued and fetch nothing
+  auto issue_q = [&](int s, int stage) {
+    // a number of loads that depends on `live` must not be counted on
+    qt.load(rx, smem + stage * T::QTile::kBytes, wave, s * DB, ld - s * DB, QS == 2 ? live : BQ);
+  };
+  char* const weights = smem + QS * T::QTile::kBytes;
+  auto issue_p = [&](int s, int stage) {
 #pragma unroll
-    for (int h = 0; h < kParts; ++h) pt.load(rw[h], b + T::QTile::kBytes + h * T::PTile::kBytes, wave, s * DB, left);
+    for (int h = 0; h < kParts; ++h)
+      pt.load(rw[h], weights + stage * T::kPBytes + h * T::PTile::kBytes, wave, s * DB, ld - s * DB);
   };
 
   f32x4 acc[kQ][kP];
@@ -184,8 +194,17 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
     for (int h = 0; h < kParts; ++h) sw[h] = a.ws[h] + ((int64_t)it.e * nb + cb) * blocks;
   }
 
+  if (QS == 2) {
+    if (PS == 3) issue_p(0, 0);
+    issue_q(0, 0);
+    issue_p(PS - 2, PS - 2);
+  } else {
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
+    for (int s = 0; s < QS - 1; ++s) {
+      issue_q(s, s);
+      issue_p(s, s);
+    }
+  }
 
   auto p_row = [&](int j) { return wp * (kCols / WP) + (j % kC) * 16; };
   auto multiply = [&](auto live_subtiles) {
@@ -195,9 +214,9 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
 #pragma unroll
       for (int i = 0; i < L; ++i) sn[i] = sx[i][0];
     }
-    int stage = 0;
+    int stage = 0, qstage = 0;
     for (int s = 0; s < steps; ++s) {
-      wait_and_meet<(STAGES - 2) * T::kLoads>();
+      wait_and_meet<in_flight(QS, PS, T::QTile::kLoads, T::kPLoads)>();
       float swc[kParts];
       if constexpr (FP8) {
         const int nx = min(s + 1, steps - 1);
@@ -209,10 +228,12 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
 #pragma unroll
         for (int h = 0; h < kParts; ++h) swc[h] = sw[h][s];
       }
-      issue(s + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-      const char* b = smem + stage * T::kStage;
-      const char* pb = b + T::QTile::kBytes;
-      stage = stage == STAGES - 1 ? 0 : stage + 1;
+      issue_q(s + QS - 1, qstage == 0 ? QS - 1 : qstage - 1);
+      issue_p(s + PS - 1, stage == 0 ? PS - 1 : stage - 1);
+      const char* b = smem + qstage * T::QTile::kBytes;
+      const char* pb = weights + stage * T::kPBytes;
+      qstage = qstage == QS - 1 ? 0 : qstage + 1;
+      stage = stage == PS - 1 ? 0 : stage + 1;
       if constexpr (FP8) {
         // The matrix cores' own 8-bit products lose the low bits of their sums
         // (measured 1.5e-5 of the result on 128 terms), so the codes are widened to
@@ -257,64 +278,99 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
   by_live_subtiles<kQ>((live - wq * 16 + 16 * WQ - 1) / (16 * WQ), multiply);
   wait_and_meet<0>();  // the loads past the last step have landed: LDS is free
 
-  // a tile can write 8-bit rows if it holds whole scale blocks of columns
-  constexpr bool kCodes = kCols % row::kScaleBlock == 0;
   // Epilogue: lane l holds row l % 16 and 4 consecutive columns of each subtile.
-  const int quad = lane >> 4;
-  const int colw = p0 + wp * (kCols / WP) + quad * 4;
-  float* red = reinterpret_cast<float*>(smem);  // [WP][BQ] absolute maxima
+  const int quad = lane >> 4, row16 = lane & 15;
+  const int colw = wp * (kCols / WP) + quad * 4;  // this lane's first column of the tile
+  const int cols = min(kCols, a.N - p0);
+  using Rows = OutTile<BQ, kCols * 2, T::kThreads>;
+  static_assert(BQ * kCols * 2 <= T::kLds, "the output tile fits where the stages were");
+  auto columns = [&](auto f) {  // f(subtile row i, subtile column j, tile row, tile column)
 #pragma unroll
-  for (int i = 0; i < kQ; ++i) {
-    const int m = q_row<WQ>(wq, i) + (lane & 15);
-    const int64_t r = first + m;
-    uint32_t mx = 0;
+    for (int i = 0; i < kQ; ++i)
 #pragma unroll
-    for (int j = 0; j < kC; ++j) {
-      const int n = colw + j * 16;
-      const bool in = m < live && n < a.N;
-      float z[4], u[4], y[4];
+      for (int j = 0; j < kC; ++j) f(i, j, q_row<WQ>(wq, i) + row16, colw + j * 16);
+  };
+  // act(z, u) + residual in place of z; the pre-activations, where they are kept,
+  // need the bias on both
+  columns([&](int i, int j, int m, int n) {
+    float z[4], u[4], y[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        z[c] = acc[i][j][c];
-        u[c] = acc[i][(GATED ? kC : 0) + j][c];
-      }
-      epilogue4<GATED>(a, it.e, r, n, in, z, u, y);
-      if (!kCodes || a.y_scale == nullptr) {
-        if (in) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + r * a.N + n) = pack4(y);
-      } else {
+    for (int c = 0; c < 4; ++c) {
+      z[c] = acc[i][j][c];
+      u[c] = acc[i][(GATED ? kC : 0) + j][c];
+    }
+    epilogue4<GATED>(a, it.e, first + m, p0 + n, m < live && n < cols, z, u, y);
+    if (a.preact != nullptr) {
+      Rows::put(smem, m, n * 2, pack4(z));
+      if (GATED) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          acc[i][j][c] = y[c];
-          mx = max(mx, row::abs_bits(y[c]));
-        }
+        for (int c = 0; c < 4; ++c) acc[i][kC + j][c] = u[c];
       }
     }
-    if (kCodes && a.y_scale != nullptr) {
-      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16));
-      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
-      if (lane < 16) red[wp * BQ + m] = __uint_as_float(mx);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[i][j][c] = y[c];
+  });
+  if (a.preact != nullptr) {
+    char* pre = reinterpret_cast<char*>(a.preact + first * kParts * a.N + p0);
+    __syncthreads();
+    Rows::flush(smem, pre, (int64_t)kParts * a.N * 2, live, cols * 2);
+    __syncthreads();
+    if constexpr (GATED) {
+      columns([&](int i, int j, int m, int n) {
+        const float u[4] = {acc[i][kC + j][0], acc[i][kC + j][1], acc[i][kC + j][2], acc[i][kC + j][3]};
+        Rows::put(smem, m, n * 2, pack4(u));
+      });
+      __syncthreads();
+      Rows::flush(smem, pre + (int64_t)a.N * 2, (int64_t)2 * a.N * 2, live, cols * 2);
+      __syncthreads();
     }
   }
+  // a tile can write 8-bit rows if it holds whole scale blocks of columns
+  constexpr bool kCodes = kCols % row::kScaleBlock == 0;
+  if (!kCodes || a.y_scale == nullptr) {
+    columns([&](int i, int j, int m, int n) {
+      const float y[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      Rows::put(smem, m, n * 2, pack4(y));
+    });
+    __syncthreads();
+    Rows::flush(smem, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + first * a.N + p0), (int64_t)a.N * 2, live, cols * 2);
+    return;
+  }
   if constexpr (kCodes) {
-    if (a.y_scale == nullptr) return;
-    // 8-bit rows: the tile's columns come in whole scale blocks, each spread over
-    // the waves that hold its columns
+    // each scale block is spread over the waves that hold its columns
     constexpr int kShare = row::kScaleBlock * WP / kCols;  // waves per block
+    uint32_t* red = reinterpret_cast<uint32_t*>(smem);     // [WP][BQ] absolute maxima
+    char* codes = smem + WP * BQ * 4;
+    using Codes = OutTile<BQ, kCols, T::kThreads>;
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) {
+      uint32_t mx = 0;
+#pragma unroll
+      for (int j = 0; j < kC; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx = max(mx, row::abs_bits(acc[i][j][c]));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
+      if (lane < 16) red[wp * BQ + q_row<WQ>(wq, i) + lane] = mx;
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kQ; ++i) {
-      const int m = q_row<WQ>(wq, i) + (lane & 15);
+      const int m = q_row<WQ>(wq, i) + row16;
       uint32_t mx = 0;
 #pragma unroll
-      for (int w = 0; w < kShare; ++w) mx = max(mx, __float_as_uint(red[(wp / kShare * kShare + w) * BQ + m]));
+      for (int w = 0; w < kShare; ++w) mx = max(mx, red[(wp / kShare * kShare + w) * BQ + m]);
       const float scale = row::block_scale(mx);
+      if (m < live && colw < cols && colw % row::kScaleBlock == 0)
+        a.y_scale[(first + m) * (a.N / row::kScaleBlock) + (p0 + colw) / row::kScaleBlock] = scale;
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
-        const int n = colw + j * 16;
         const float y[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        if (m < live && n < a.N) store_codes(a, first + m, n, y, scale);
+        Codes::put(codes, m, colw + j * 16, codes4(y, scale));
       }
     }
+    __syncthreads();
+    Codes::flush(codes, static_cast<char*>(a.y) + first * a.N + p0, a.N, live, cols);
   }
 }
 
@@ -419,6 +475,11 @@ __global__ __launch_bounds__(WC* WK * 64) void linear_few_kernel(LinearArgs a) {
       for (int c = 0; c < 4; ++c) (h == 0 ? z[c] : u[c]) = s[c];
     }
     epilogue4<GATED>(a, it.e, first + m, n, in, z, u, y);
+    if (a.preact != nullptr && in) {
+      uint16_t* pre = a.preact + (first + m) * kParts * a.N + n;
+      *reinterpret_cast<uint2*>(pre) = pack4(z);
+      if (GATED) *reinterpret_cast<uint2*>(pre + a.N) = pack4(u);
+    }
     if (a.y_scale == nullptr && in) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + (first + m) * a.N + n) = pack4(y);
   }
   if constexpr (WC == 8) {
@@ -436,19 +497,21 @@ __global__ __launch_bounds__(WC* WK * 64) void linear_few_kernel(LinearArgs a) {
       uint32_t mx = 0;
 #pragma unroll
       for (int i = 0; i < WC; ++i) mx = max(mx, red[i][m]);
-      store_codes(a, first + m, n, y, row::block_scale(mx));
+      const float scale = row::block_scale(mx);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + (first + m) * a.N + n) = codes4(y, scale);
+      if (n % row::kScaleBlock == 0) a.y_scale[(first + m) * (a.N / row::kScaleBlock) + n / row::kScaleBlock] = scale;
     }
   }
 }
 
 // ------------------------------------------------------------- backward x --
 
-template <int BQ, int BP, int WQ, int WP, int STAGES>
+template <int BQ, int BP, int WQ, int WP, int PS>
 __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_x_kernel(LinearArgs a) {
   constexpr int kWaves = WQ * WP, kQ = BQ / WQ / 16, kP = BP / WP / 16, kD = 64;
+  static_assert(PS == 2 || PS == 3, "waits are counted for two or three weight stages");
   using QTile = RowTile<BQ, kD * 2, kWaves>;
   using PTile = DepthTile<BP, kD, kWaves>;
-  constexpr int kStage = QTile::kBytes + PTile::kBytes, kLoads = QTile::kLoads + PTile::kLoads;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wq = wave / WP, wp = wave % WP;
   const Item it = find_item(a, blockIdx.x, BQ, (a.K + BP - 1) / BP);
@@ -466,36 +529,42 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_x_kernel(Linea
   // the depth runs over the N columns of dz's first part, then of its second
   const int per = (a.N + kD - 1) / kD, steps = per * a.parts;
   const __amdgpu_buffer_rsrc_t rq = resource(dz);
-  auto issue = [&](int s, int stage) {
-    char* b = smem + stage * kStage;
+  // past the last step nothing is left: the loads are issued and fetch nothing
+  auto issue_q = [&](int s) {
     const int h = s >= per ? 1 : 0, k = s - h * per;
-    const int left = s < steps ? a.N - k * kD : 0;
-    qt.load(rq, b, wave, (h * a.N + k * kD) * 2, left * 2, STAGES == 2 ? live : BQ);
-    pt.load(resource(static_cast<const char*>(a.w[s < steps ? h : 0]) + expert + (int64_t)k * kD * ldp), b + QTile::kBytes,
-            wave, 0, left);
+    qt.load(rq, smem + (s & 1) * QTile::kBytes, wave, (h * a.N + k * kD) * 2, s < steps ? (a.N - k * kD) * 2 : 0, live);
+  };
+  char* const weights = smem + 2 * QTile::kBytes;
+  auto issue_p = [&](int s, int stage) {
+    const int h = s >= per ? 1 : 0, k = s - h * per;
+    pt.load(resource(static_cast<const char*>(a.w[s < steps ? h : 0]) + expert + (int64_t)k * kD * ldp),
+            weights + stage * PTile::kBytes, wave, 0, s < steps ? a.N - k * kD : 0);
   };
   f32x4 acc[kQ][kP];
 #pragma unroll
   for (int i = 0; i < kQ; ++i)
 #pragma unroll
     for (int j = 0; j < kP; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
+  if (PS == 3) issue_p(0, 0);
+  issue_q(0);
+  issue_p(PS - 2, PS - 2);
   auto multiply = [&](auto live_subtiles) {
     constexpr int L = decltype(live_subtiles)::value;
     int stage = 0;
     for (int s = 0; s < steps; ++s) {
-      wait_and_meet<(STAGES - 2) * kLoads>();
-      issue(s + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-      const char* b = smem + stage * kStage;
-      stage = stage == STAGES - 1 ? 0 : stage + 1;
+      wait_and_meet<in_flight(2, PS, QTile::kLoads, PTile::kLoads)>();
+      issue_q(s + 1);
+      issue_p(s + PS - 1, stage == 0 ? PS - 1 : stage - 1);
+      const char* b = smem + (s & 1) * QTile::kBytes;
+      const char* pb = weights + stage * PTile::kBytes;
+      stage = stage == PS - 1 ? 0 : stage + 1;
 #pragma unroll
       for (int kk = 0; kk < kD / 32; ++kk) {
         bf16x8 q[L], p[kP];
 #pragma unroll
         for (int i = 0; i < L; ++i) q[i] = QTile::frag(b, q_row<WQ>(wq, i), kk, lane);
 #pragma unroll
-        for (int j = 0; j < kP; ++j) p[j] = PTile::frag(b + QTile::kBytes, wp * (BP / WP) + j * 16, kk, lane);
+        for (int j = 0; j < kP; ++j) p[j] = PTile::frag(pb, wp * (BP / WP) + j * 16, kk, lane);
 #pragma unroll
         for (int j = 0; j < kP; ++j)
 #pragma unroll
@@ -505,27 +574,27 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_x_kernel(Linea
   };
   by_live_subtiles<kQ>((live - wq * 16 + 16 * WQ - 1) / (16 * WQ), multiply);
   wait_and_meet<0>();
-  uint16_t* dx = static_cast<uint16_t*>(a.y);
+  using Rows = OutTile<BQ, BP * 2, kWaves * 64>;
+  static_assert(BQ * BP * 2 <= 2 * QTile::kBytes + PS * PTile::kBytes, "the output tile fits where the stages were");
 #pragma unroll
-  for (int i = 0; i < kQ; ++i) {
-    const int m = q_row<WQ>(wq, i) + (lane & 15);
-    if (m >= live) continue;
+  for (int i = 0; i < kQ; ++i)
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
-      const int n = p0 + wp * (BP / WP) + j * 16 + (lane >> 4) * 4;
       const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      if (n < a.K) *reinterpret_cast<uint2*>(dx + (first + m) * a.K + n) = pack4(v);
+      Rows::put(smem, q_row<WQ>(wq, i) + (lane & 15), (wp * (BP / WP) + j * 16 + (lane >> 4) * 4) * 2, pack4(v));
     }
-  }
+  __syncthreads();
+  Rows::flush(smem, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + first * a.K + p0), (int64_t)a.K * 2, live,
+              min(BP, a.K - p0) * 2);
 }
 
 // ------------------------------------------------------------- backward w --
 
 // One workgroup: BQ weight rows by BP columns of one expert's gradient, over one of
 // `splits` equal parts of its rows.
-template <int BQ, int BP, int WQ, int WP, int STAGES>
-__global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_w_kernel(LinearArgs a) {
-  constexpr int kWaves = WQ * WP, kQ = BQ / WQ / 16, kP = BP / WP / 16, kD = 64;
+template <bool BIAS, int BQ, int BP, int WQ, int WP, int kD, int STAGES, int OCC>
+__global__ __launch_bounds__(WQ* WP * 64, OCC) void linear_backward_w_kernel(LinearArgs a) {
+  constexpr int kWaves = WQ * WP, kQ = BQ / WQ / 16, kP = BP / WP / 16;
   using QTile = DepthTile<BQ, kD, kWaves>;
   using PTile = DepthTile<BP, kD, kWaves>;
   constexpr int kStage = QTile::kBytes + PTile::kBytes, kLoads = QTile::kLoads + PTile::kLoads;
@@ -563,16 +632,16 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_w_kernel(Linea
     qt.load(resource(dz + (int64_t)s * kD * ldq), b, wave, 0, left);
     pt.load(resource(x + (int64_t)s * kD * ldp), b + QTile::kBytes, wave, 0, left);
   };
-  f32x4 acc[kQ][kP], ones_acc[kQ];
+  f32x4 acc[kQ][kP], ones_acc[BIAS ? kQ : 1];
 #pragma unroll
   for (int q = 0; q < kQ; ++q) {
-    ones_acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (BIAS) ones_acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int p = 0; p < kP; ++p) acc[q][p] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   // the bias gradient is the product with a column of ones: by the workgroups of
   // the first column tile, in their first column of waves
-  const bool sums = a.db[0] != nullptr && tp == 0 && wp == 0;
+  const bool sums = BIAS && tp == 0 && wp == 0;
   const __bf16 one = (__bf16)1.0f;
   const bf16x8 ones{one, one, one, one, one, one, one, one};
 #pragma unroll
@@ -592,7 +661,7 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_w_kernel(Linea
       for (int c = 0; c < kP; ++c) p[c] = PTile::frag(b + QTile::kBytes, wp * (BP / WP) + c * 16, kk, lane);
       if (sums) {
 #pragma unroll
-        for (int r = 0; r < kQ; ++r) ones_acc[r] = mma::mfma(ones, q[r], ones_acc[r]);
+        for (int r = 0; r < (BIAS ? kQ : 0); ++r) ones_acc[r] = mma::mfma(ones, q[r], ones_acc[r]);
       }
 #pragma unroll
       for (int c = 0; c < kP; ++c)
@@ -604,28 +673,43 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_w_kernel(Linea
   // with splits the sums go to the workspace: per split dw (all parts), then db
   const int64_t weight = (int64_t)a.E * a.N * a.K;
   const bool whole = a.splits == 1;
-  float* part = whole ? nullptr : a.part + split * (a.parts * (weight + (a.db[0] != nullptr ? (int64_t)a.E * a.N : 0)));
+  float* part = whole ? nullptr : a.part + split * (a.parts * (weight + (BIAS ? (int64_t)a.E * a.N : 0)));
+  const int64_t line0 = (int64_t)e * a.N + q0;
+  if constexpr (BIAS) {
+    if (sums && lane < 16) {
+      float* db = (whole ? a.db[h] : part + a.parts * weight + (int64_t)h * a.E * a.N) + line0;
+#pragma unroll
+      for (int r = 0; r < kQ; ++r) {
+        const int n = wq * (BQ / WQ) + r * 16 + lane;
+        if (q0 + n < a.N) db[n] = ones_acc[r][0];
+      }
+    }
+  }
+  if (whole && !a.dw_f32) {
+    using Rows = OutTile<BQ, BP * 2, kWaves * 64>;
+    static_assert(BQ * BP * 2 <= STAGES * kStage, "the output tile fits where the stages were");
+#pragma unroll
+    for (int r = 0; r < kQ; ++r)
+#pragma unroll
+      for (int c = 0; c < kP; ++c) {
+        const float v[4] = {acc[r][c][0], acc[r][c][1], acc[r][c][2], acc[r][c][3]};
+        Rows::put(smem, wq * (BQ / WQ) + r * 16 + (lane & 15), (wp * (BP / WP) + c * 16 + (lane >> 4) * 4) * 2, pack4(v));
+      }
+    __syncthreads();
+    Rows::template flush<true>(smem, reinterpret_cast<char*>(static_cast<uint16_t*>(a.dw[h]) + line0 * a.K + p0), (int64_t)a.K * 2,
+                min(BQ, a.N - q0), min(BP, a.K - p0) * 2);
+    return;
+  }
+  // float32: a lane's 16 bytes go out as they are, 64 bytes of each of 16 rows at a time
+  float* out = (whole ? static_cast<float*>(a.dw[h]) : part + h * weight) + line0 * a.K;
 #pragma unroll
   for (int r = 0; r < kQ; ++r) {
-    const int n = q0 + wq * (BQ / WQ) + r * 16 + (lane & 15);
-    if (n >= a.N) continue;
-    const int64_t line = (int64_t)e * a.N + n;
-    if (sums && lane < 16) {
-      float* db = whole ? a.db[h] : part + a.parts * weight + (int64_t)h * a.E * a.N;
-      db[line] = ones_acc[r][0];
-    }
+    const int n = wq * (BQ / WQ) + r * 16 + (lane & 15);
+    if (q0 + n >= a.N) continue;
 #pragma unroll
     for (int c = 0; c < kP; ++c) {
       const int k = p0 + wp * (BP / WP) + c * 16 + (lane >> 4) * 4;
-      if (k >= a.K) continue;
-      const int64_t at = line * a.K + k;
-      const float v[4] = {acc[r][c][0], acc[r][c][1], acc[r][c][2], acc[r][c][3]};
-      if (!whole)
-        *reinterpret_cast<f32x4*>(part + h * weight + at) = acc[r][c];
-      else if (a.dw_f32)
-        *reinterpret_cast<f32x4*>(static_cast<float*>(a.dw[h]) + at) = acc[r][c];
-      else
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dw[h]) + at) = pack4(v);
+      if (k < a.K) __builtin_nontemporal_store(acc[r][c], reinterpret_cast<f32x4*>(out + (int64_t)n * a.K + k));
     }
   }
 }
@@ -705,21 +789,22 @@ __global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs a, const u
 
 // Instantiated by name: the host pass of this compiler otherwise leaves out the
 // launch stubs of some kernel templates that are only reached through pointers.
-#define MOE_TILES(F, G)                                                     \
-  template __global__ void linear_kernel<F, G, 128, 128, 2, 2, 128, 2>(LinearArgs); \
-  template __global__ void linear_few_kernel<F, G, 1, 16>(LinearArgs);      \
+#define MOE_TILES(F, G)                                                        \
+  template __global__ void linear_kernel<F, G, 64, 64, 2, 2, 128, 4, 4>(LinearArgs);   \
+  template __global__ void linear_kernel<F, G, 128, 128, 2, 2, 128, 2, 3>(LinearArgs); \
+  template __global__ void linear_few_kernel<F, G, 1, 16>(LinearArgs);         \
   template __global__ void linear_few_kernel<F, G, 8, 2>(LinearArgs);
 MOE_TILES(false, false)
 MOE_TILES(false, true)
 MOE_TILES(true, false)
 MOE_TILES(true, true)
 #undef MOE_TILES
-template __global__ void linear_kernel<false, false, 256, 256, 2, 4, 128, 2>(LinearArgs);
-template __global__ void linear_kernel<false, true, 256, 256, 2, 4, 128, 2>(LinearArgs);
-template __global__ void linear_kernel<true, true, 128, 256, 2, 4, 128, 2>(LinearArgs);
-template __global__ void linear_backward_x_kernel<128, 128, 2, 2, 2>(LinearArgs);
-template __global__ void linear_backward_w_kernel<128, 128, 2, 2, 2>(LinearArgs);
-template __global__ void linear_backward_w_kernel<256, 256, 2, 4, 2>(LinearArgs);
+template __global__ void linear_kernel<false, false, 256, 256, 4, 4, 128, 2, 3>(LinearArgs);
+template __global__ void linear_kernel<false, true, 256, 256, 4, 4, 128, 2, 3>(LinearArgs);
+template __global__ void linear_kernel<true, true, 64, 256, 1, 4, 128, 2, 2>(LinearArgs);
+template __global__ void linear_backward_x_kernel<128, 128, 2, 2, 3>(LinearArgs);
+template __global__ void linear_backward_w_kernel<false, 128, 128, 2, 2, 32, 2, 4>(LinearArgs);
+template __global__ void linear_backward_w_kernel<true, 128, 128, 2, 2, 32, 2, 3>(LinearArgs);
 
 template <typename K>
 hipError_t launch(K kern, int64_t items, int threads, int lds, const LinearArgs& a, hipStream_t s,
@@ -730,12 +815,12 @@ hipError_t launch(K kern, int64_t items, int threads, int lds, const LinearArgs&
   return hipGetLastError();
 }
 
-template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int STAGES>
+template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int QS, int PS>
 hipError_t run_forward(const LinearArgs& a, hipStream_t s) {
-  using T = Forward<FP8, GATED, BQ, BP, WQ, WP, DB, STAGES>;
+  using T = Forward<FP8, GATED, BQ, BP, WQ, WP, DB, QS, PS>;
   static std::atomic<size_t> allowed[kMaxCachedDevices];
   const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, BQ) * ((a.N + T::kCols - 1) / T::kCols);
-  void (*const kern)(LinearArgs) = &linear_kernel<FP8, GATED, BQ, BP, WQ, WP, DB, STAGES>;
+  void (*const kern)(LinearArgs) = &linear_kernel<FP8, GATED, BQ, BP, WQ, WP, DB, QS, PS>;
   return launch(kern, items, T::kThreads, T::kLds, a, s, allowed);
 }
 
@@ -757,21 +842,17 @@ constexpr int64_t kFewRows = 32;
 template <bool FP8, bool GATED>
 hipError_t forward_by_shape(const LinearArgs& a, hipStream_t s) {
   if (mean_rows(a) <= kFewRows) return a.y_scale != nullptr ? run_few<FP8, GATED, 8, 2>(a, s) : run_few<FP8, GATED, 1, 16>(a, s);
-  // 256-wide tiles read each operand byte half as often as 128-wide ones, but are
-  // four times the work: taken where they fill the GPU and the runs fill them
-  const int64_t tiles = (a.rows / 256 + 1) * ((a.parts * (int64_t)a.N + 255) / 256);
-  const bool codes = a.y_scale != nullptr;  // a SwiGLU tile with whole scale blocks has 256 weight rows
-  if constexpr (FP8 && GATED) {
-    if (tiles >= 128 || codes) return run_forward<FP8, GATED, 128, 256, 2, 4, 128, 2>(a, s);
-  } else if constexpr (!FP8) {
-    if ((tiles >= 256 && mean_rows(a) >= 160) || (GATED && codes)) return run_forward<FP8, GATED, 256, 256, 2, 4, 128, 2>(a, s);
+  const bool codes = a.y_scale != nullptr;  // 8-bit rows need whole scale blocks of columns in a tile
+  auto tiles = [&](int64_t bq, int64_t bp) { return (a.rows + bq - 1) / bq * ((a.parts * (int64_t)a.N + bp - 1) / bp); };
+  if (GATED && codes) {
+    // a tile with 128 columns of SwiGLU takes 256 weight rows
+    if constexpr (FP8 && GATED) return run_forward<FP8, GATED, 64, 256, 1, 4, 128, 2, 2>(a, s);
+    if constexpr (!FP8 && GATED) return run_forward<FP8, GATED, 256, 256, 4, 4, 128, 2, 3>(a, s);
   }
-  return run_forward<FP8, GATED, 128, 128, 2, 2, 128, 2>(a, s);
-}
-
-// The weight gradient's tiles: 256 x 256 where they fill the GPU, else 128 x 128.
-bool big_w_tiles(int E, int N, int K, int parts) {
-  return (int64_t)E * parts * ((N + 255) / 256) * ((K + 255) / 256) >= 256;
+  if (!codes && tiles(128, 128) < 256) return run_forward<FP8, GATED, 64, 64, 2, 2, 128, 4, 4>(a, s);
+  if constexpr (!FP8)
+    if (tiles(256, 256) >= 256 && mean_rows(a) >= 160) return run_forward<FP8, GATED, 256, 256, 4, 4, 128, 2, 3>(a, s);
+  return run_forward<FP8, GATED, 128, 128, 2, 2, 128, 2, 3>(a, s);
 }
 }  // namespace
 
@@ -783,26 +864,30 @@ hipError_t launch_linear(const LinearArgs& a, bool fp8, hipStream_t s) {
 hipError_t launch_linear_backward_x(const LinearArgs& a, hipStream_t s) {
   static std::atomic<size_t> allowed[kMaxCachedDevices];
   const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, kBQ) * ((a.K + kBP - 1) / kBP);
-  return launch(&linear_backward_x_kernel<kBQ, kBP, 2, 2, 2>, items, 256, 2 * (kBQ + kBP) * 128, a, s, allowed);
+  return launch(&linear_backward_x_kernel<kBQ, kBP, 2, 2, 3>, items, 256, (2 * kBQ + 3 * kBP) * 128, a, s, allowed);
 }
 
 int backward_w_splits(int64_t rows, int E, int N, int K, int parts) {
-  if (big_w_tiles(E, N, K, parts)) return 1;
   const int64_t tiles = (int64_t)E * parts * ((N + kBQ - 1) / kBQ) * ((K + kBP - 1) / kBP);
   if (tiles >= 256) return 1;
   // workgroups for two rounds of the GPU, as long as a split keeps 256 rows on average
   return (int)std::max<int64_t>(1, std::min<int64_t>((512 + tiles - 1) / tiles, rows / E / 256));
 }
 
-template <int BQ, int BP, int WQ, int WP>
+// Stages of 32 rows: an expert's run is short (256 rows: 8 steps), so what counts is
+// that 4 workgroups share a compute unit and one's stores overlap another's loads
+// (128 experts x 1536 x 2048: 296 us; 64-row stages 340, 256 x 256 tiles 338).
+template <bool BIAS, int OCC>
 hipError_t run_backward_w(const LinearArgs& a, hipStream_t s) {
   static std::atomic<size_t> allowed[kMaxCachedDevices];
-  const int64_t items = (int64_t)a.E * a.parts * ((a.N + BQ - 1) / BQ) * ((a.K + BP - 1) / BP) * a.splits;
-  return launch(&linear_backward_w_kernel<BQ, BP, WQ, WP, 2>, items, WQ * WP * 64, 2 * (BQ + BP) * 128, a, s, allowed);
+  constexpr int kD = 32, kStages = 2;
+  const int64_t items = (int64_t)a.E * a.parts * ((a.N + kBQ - 1) / kBQ) * ((a.K + kBP - 1) / kBP) * a.splits;
+  return launch(&linear_backward_w_kernel<BIAS, kBQ, kBP, 2, 2, kD, kStages, OCC>, items, 256, kStages * (kBQ + kBP) * kD * 2, a, s,
+                allowed);
 }
 
 hipError_t launch_linear_backward_w(const LinearArgs& a, hipStream_t s) {
-  const hipError_t e = big_w_tiles(a.E, a.N, a.K, a.parts) ? run_backward_w<256, 256, 2, 4>(a, s) : run_backward_w<kBQ, kBP, 2, 2>(a, s);
+  const hipError_t e = a.db[0] != nullptr ? run_backward_w<true, 3>(a, s) : run_backward_w<false, 4>(a, s);
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t total = (int64_t)a.parts * a.E * a.N * (a.K + (a.db[0] != nullptr ? 1 : 0));
   hipLaunchKernelGGL(join_splits_kernel, dim3((unsigned)((total / 4 + 255) / 256)), dim3(256), 0, s, a);

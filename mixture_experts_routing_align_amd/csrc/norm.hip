@@ -5,10 +5,11 @@
 //   t = dy w, n = z rstd, dx = dz + rstd (t - n mean(t n)), dw = sum_rows dy n
 //
 // Both are bound by HBM: a row is read once and stays in registers between the
-// sum and its use, so each element moves once.  A row belongs to one wave (up to
-// 2048 columns, 8 per lane and piece, at most 4 pieces) or to a workgroup of 4 or
-// 16 waves; with one wave per row the sum needs no LDS and no barrier.  A few
-// rows take the wider form, which has fewer dependent loads per lane.
+// sum and its use, so each element moves once.  A row belongs to one wave or to a
+// workgroup of 4, 8 or 16 waves, in pieces of 8 columns per lane; with one wave per
+// row the sum needs no LDS and no barrier.  Measured (16384 x 2048): 44 us forward,
+// 50 us backward plus 5 us for the columns' sums, 6.1 and 4.9 TB/s of the bytes
+// that have to move.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -137,71 +138,84 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
   }
 }
 
-// Each row group of the workgroup walks rows g, g + groups, ...; the columns' sums
-// of dy n stay in registers, the workgroup's groups add theirs in order through
-// LDS, and each workgroup leaves one partial row (or, when it is the only one,
-// the result).
+// Each row group of the workgroup walks rows g, g + groups, ..., the next row's
+// loads in flight while this one is reduced; the columns' sums of dy n stay in
+// registers, the workgroup's groups add theirs in order through LDS, and each
+// workgroup leaves one partial row (or, when it is the only one, the result).
+// 8 columns a thread (2048 columns: 4 waves a row) measured faster than a wave per
+// row with 32, whose column sums leave room for half the waves: 50 against 93 us
+// at 16384 x 2048.
 template <int TPR, int NV, int THREADS, typename ZT, bool DW>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormBackwardArgs a) {
-  constexpr int R = THREADS / TPR;
-  __shared__ float red[THREADS / 64];
+  constexpr int R = THREADS / TPR, W = TPR / 64;
+  // rows that need the workgroup's barrier have it to themselves
+  static_assert(TPR == 64 || R == 1, "one row at a time where waves share it");
+  __shared__ float red[2][THREADS / 64];
   __shared__ float cols[DW && R > 1 ? TPR * NV * 8 : 1];
   const int sub = threadIdx.x / TPR, j = threadIdx.x % TPR;
   const int H = a.H;
-  uint32_t w[NV][4];
+  struct Row {
+    Piece<ZT> z[NV], dz[NV];
+    Piece<uint16_t> dy[NV];
+    float rstd;
+  };
+  auto load = [&](int64_t m, Row& r) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + j) * 8;
+      r.z[v].load(static_cast<const ZT*>(a.z) + m * H, c, H);
+      r.dy[v].load(static_cast<const uint16_t*>(a.dy) + m * H, c, H);
+      if (a.dz != nullptr) r.dz[v].load(static_cast<const ZT*>(a.dz) + m * H, c, H);
+    }
+    r.rstd = a.rstd[m];
+  };
+  Piece<uint16_t> w[NV];
   float acc[NV][8];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    float t[8];
-    load8(static_cast<const uint16_t*>(a.w), (v * TPR + j) * 8, H, t);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[v][i] = pack_bf16(t[2 * i], t[2 * i + 1]);
+    w[v].load(static_cast<const uint16_t*>(a.w), (v * TPR + j) * 8, H);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[v][i] = 0.f;
   }
   const int64_t step = (int64_t)gridDim.x * R;
-  for (int64_t m0 = (int64_t)blockIdx.x * R; m0 < a.M; m0 += step) {
-    const int64_t m = m0 + sub;
-    const bool live = m < a.M;
-    const int64_t mm = live ? m : a.M - 1;
-    const ZT* zp = static_cast<const ZT*>(a.z) + mm * H;
-    const ZT* dzp = static_cast<const ZT*>(a.dz) + mm * H;
-    float n[NV][8], dy[NV][8], dz[NV][8];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * TPR + j) * 8;
-      load8(zp, c, H, n[v]);
-      load8(static_cast<const uint16_t*>(a.dy) + mm * H, c, H, dy[v]);
-      if (a.dz != nullptr) load8(dzp, c, H, dz[v]);
-    }
-    const float rstd = a.rstd[mm];
+  int64_t m = (int64_t)blockIdx.x * R + sub;
+  constexpr bool kAhead = TPR < 1024;  // 1024 threads leave no registers for a second row
+  Row r, next;
+  if (kAhead && m < a.M) load(m, r);
+  for (int parity = 0; m < a.M; m += step, parity ^= 1) {
+    if (!kAhead) load(m, r);
+    if (kAhead && m + step < a.M) load(m + step, next);
+    const float rstd = r.rstd;
     float dot = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        n[v][i] *= rstd;
-        const float g = dy[v][i] * n[v][i];
-        if (DW && live) acc[v][i] += g;
-        const float wv = i & 1 ? bf16_hi(w[v][i / 2]) : bf16_lo(w[v][i / 2]);
-        dy[v][i] *= wv;
-        dot = fmaf(dy[v][i], n[v][i], dot);
+        const float n = r.z[v].get(i) * rstd, g = r.dy[v].get(i);
+        if (DW) acc[v][i] = fmaf(g, n, acc[v][i]);
+        dot = fmaf(g * w[v].get(i), n, dot);
       }
-    if constexpr (TPR > 64) __syncthreads();  // red is read to the end of the last row
-    dot = row_sum<TPR>(dot, red) / (float)H;
-    if (live) {
-      ZT* dx = static_cast<ZT*>(a.dx) + m * H;
+    dot = wave_sum(dot);
+    if constexpr (TPR > 64) {
+      // two sets of wave sums in turn: one barrier a row
+      if ((threadIdx.x & 63) == 0) red[parity][threadIdx.x >> 6] = dot;
+      __syncthreads();
+      dot = red[parity][0];
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i] = rstd * fmaf(-n[v][i], dot, dy[v][i]);
-          if (a.dz != nullptr) o[i] += dz[v][i];
-        }
-        store8(dx, (v * TPR + j) * 8, H, o);
-      }
+      for (int i = 1; i < W; ++i) dot += red[parity][i];
     }
+    dot /= (float)H;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i] = rstd * fmaf(-(r.z[v].get(i) * rstd), dot, r.dy[v].get(i) * w[v].get(i));
+        if (a.dz != nullptr) o[i] += r.dz[v].get(i);
+      }
+      store8(static_cast<ZT*>(a.dx) + m * H, (v * TPR + j) * 8, H, o);
+    }
+    if (kAhead) r = next;
   }
   if constexpr (DW) {
     if constexpr (R > 1) {
@@ -269,19 +283,22 @@ hipError_t run_norm(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// A row's threads: one wave up to 2048 columns when there are rows enough to fill
-// the GPU with such waves, else 256 threads (up to 8192 columns), else 1024.
+// A row's threads: one wave up to 512 columns, and up to 1024 where there are rows
+// enough to fill the GPU with such waves (16384 x 1024: 23 against 26 us); else
+// 256 threads (up to 4096 columns), 512 (8192) or 1024.  More threads with fewer
+// columns each measured faster for long rows (16384 x 2048: 44 us with 8 columns a
+// thread against 52 with a wave per row; 8192 x 7168 to 8 bits: 80 us with 512
+// threads against 102 with 256).
 constexpr int64_t kWaveRows = 2048;
 
 template <typename RT, bool HAS_R>
 hipError_t norm_by_width(const NormArgs& a, hipStream_t s) {
   const int p = (a.H + 7) / 8;
   if (p <= 64) return run_norm<64, 1, 256, RT, HAS_R>(a, s);
-  if (p <= 256 && a.M >= kWaveRows)
-    return p <= 128 ? run_norm<64, 2, 256, RT, HAS_R>(a, s) : run_norm<64, 4, 256, RT, HAS_R>(a, s);
+  if (p <= 128 && a.M >= kWaveRows) return run_norm<64, 2, 256, RT, HAS_R>(a, s);
   if (p <= 256) return run_norm<256, 1, 256, RT, HAS_R>(a, s);
   if (p <= 512) return run_norm<256, 2, 256, RT, HAS_R>(a, s);
-  if (p <= 1024) return run_norm<256, 4, 256, RT, HAS_R>(a, s);
+  if (p <= 1024) return run_norm<512, 2, 512, RT, HAS_R>(a, s);
   if (p <= 2048) return run_norm<1024, 2, 1024, RT, HAS_R>(a, s);
   return run_norm<1024, 4, 1024, RT, HAS_R>(a, s);
 }
@@ -293,11 +310,12 @@ struct BackwardShape {
 BackwardShape backward_shape(int64_t M, int H) {
   const int p = (H + 7) / 8;
   BackwardShape b;
-  b.tpr = p <= 256 ? 64 : (p <= 1024 ? 256 : 1024);
-  b.nv = p <= 64 ? 1 : p <= 128 ? 2 : p <= 256 ? 4 : p <= 512 ? 2 : p <= 1024 ? 4 : p <= 2048 ? 2 : 4;
-  b.threads = b.tpr == 1024 ? 1024 : 512;
+  b.tpr = p <= 64 ? 64 : p <= 512 ? 256 : p <= 1024 ? 512 : 1024;
+  b.nv = p <= 256 ? 1 : p <= 2048 ? 2 : 4;
+  b.threads = std::max(b.tpr, 256);
   const int64_t per = b.threads / b.tpr;
-  b.groups = (int)std::min<int64_t>((M + per - 1) / per, 512);
+  // about as many workgroups as the GPU holds at once: each leaves one partial row
+  b.groups = (int)std::min<int64_t>((M + per - 1) / per, 1024 * 256 / b.threads);
   return b;
 }
 
@@ -311,15 +329,10 @@ void run_backward(const NormBackwardArgs& a, int groups, bool dw, hipStream_t s)
 
 template <typename ZT>
 void backward_by_width(const NormBackwardArgs& a, const BackwardShape& b, bool dw, hipStream_t s) {
-  if (b.tpr == 64) {
-    if (b.nv == 1) return run_backward<64, 1, 512, ZT>(a, b.groups, dw, s);
-    if (b.nv == 2) return run_backward<64, 2, 512, ZT>(a, b.groups, dw, s);
-    return run_backward<64, 4, 512, ZT>(a, b.groups, dw, s);
-  }
-  if (b.tpr == 256) {
-    if (b.nv == 2) return run_backward<256, 2, 512, ZT>(a, b.groups, dw, s);
-    return run_backward<256, 4, 512, ZT>(a, b.groups, dw, s);
-  }
+  if (b.tpr == 64) return run_backward<64, 1, 256, ZT>(a, b.groups, dw, s);
+  if (b.tpr == 256 && b.nv == 1) return run_backward<256, 1, 256, ZT>(a, b.groups, dw, s);
+  if (b.tpr == 256) return run_backward<256, 2, 256, ZT>(a, b.groups, dw, s);
+  if (b.tpr == 512) return run_backward<512, 2, 512, ZT>(a, b.groups, dw, s);
   if (b.nv == 2) return run_backward<1024, 2, 1024, ZT>(a, b.groups, dw, s);
   return run_backward<1024, 4, 1024, ZT>(a, b.groups, dw, s);
 }

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(UnpermuteArgs a) {
       const int kn = min(kBatch, a.top_k - k0);
       int p[kBatch];
       float w[kBatch];
-      float v[kBatch][8];
+      Piece<uint16_t> v[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         p[k] = k < kn ? position(a.perm, t * a.top_k + k0 + k, a.rows) : -1;
@@ -109,12 +109,12 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(UnpermuteArgs a) {
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (p[k] >= 0) load8(a.y + (int64_t)p[k] * H, c, H, v[k]);
+        if (p[k] >= 0) v[k].load(a.y + (int64_t)p[k] * H, c, H);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
         if (p[k] >= 0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = WEIGHTED ? fmaf(w[k], v[k][i], o[i]) : o[i] + v[k][i];
+          for (int i = 0; i < 8; ++i) o[i] = WEIGHTED ? fmaf(w[k], v[k].get(i), o[i]) : o[i] + v[k].get(i);
         }
     }
     store8(a.out + t * H, c, H, o);
@@ -139,18 +139,19 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(UnpermuteB
       dot[k] = 0.f;
     }
     for (int c = j * 8; c < H; c += TPT * 8) {
-      float d[8], v[kBatch][8];
-      load8(a.dout + t * H, c, H, d);
+      float d[8];
+      Piece<uint16_t> v[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (p[k] >= 0) load8(a.y + (int64_t)p[k] * H, c, H, v[k]);
+        if (p[k] >= 0) v[k].load(a.y + (int64_t)p[k] * H, c, H);
+      load8(a.dout + t * H, c, H, d);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
         if (p[k] >= 0) {
           float o[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            dot[k] = fmaf(d[i], v[k][i], dot[k]);
+            dot[k] = fmaf(d[i], v[k].get(i), dot[k]);
             o[i] = w[k] * d[i];
           }
           store8(a.dy + (int64_t)p[k] * H, c, H, o);

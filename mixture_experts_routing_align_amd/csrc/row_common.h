@@ -90,6 +90,33 @@ __device__ __forceinline__ void store8(float* __restrict__ p, int c, int H, cons
   }
 }
 
+// 8 consecutive elements as they lie in memory: half the registers of their float32
+// values for bf16, so that a wave can hold several rows.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<uint16_t> {
+  uint32_t d[4];
+  __device__ __forceinline__ void load(const uint16_t* __restrict__ p, int c, int H) {
+    if (c + 8 <= H) {
+      const u32x4_e2 v = *reinterpret_cast<const u32x4_e2*>(p + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        d[i] = (c + 2 * i < H ? p[c + 2 * i] : 0u) | (c + 2 * i + 1 < H ? (uint32_t)p[c + 2 * i + 1] << 16 : 0u);
+    }
+  }
+  __device__ __forceinline__ float get(int i) const { return i & 1 ? bf16_hi(d[i / 2]) : bf16_lo(d[i / 2]); }
+};
+template <>
+struct Piece<float> {
+  float d[8];
+  __device__ __forceinline__ void load(const float* __restrict__ p, int c, int H) { load8(p, c, H, d); }
+  __device__ __forceinline__ float get(int i) const { return d[i]; }
+};
+
 template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ float dpp0(float v) {  // lanes without a source read 0
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROW_MASK, 0xF, false));
