@@ -27,9 +27,22 @@ using row::pack_bf16;
 
 extern __shared__ __attribute__((aligned(1024))) char smem[];
 
-__device__ __forceinline__ float silu(float z) { return z / (1.0f + expf(-z)); }
-__device__ __forceinline__ float gelu_tanh_arg(float z) { return 0.7978845608028654f * fmaf(0.044715f * z * z, z, z); }
-__device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.0f + tanhf(gelu_tanh_arg(z))); }
+// 1 / (1 + exp(-x)) on the hardware's exponential and reciprocal: -x log2(e) as a
+// rounded product and its remainder, so that far arguments keep their relative
+// precision (a few 2^-24 in all; expf and a division take four times as long, 45 of
+// 325 us in the gate+up product's epilogue).
+__device__ __forceinline__ float sigmoid(float x) {
+  const float t = x * -1.44269504f, rest = fmaf(x, -1.44269504f, -t) + x * -1.92596303e-8f;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_amdgcn_rcpf(1.0f + fmaf(e, rest * 0.69314718f, e));
+}
+// The same for any x: past 87 on either side (and at the infinities) the correction
+// would meet an infinity, and float32's normal range has only 0 and 1 there.
+__device__ __forceinline__ float sigmoid_all(float x) { return x > 87.0f ? 1.0f : x < -87.0f ? 0.0f : sigmoid(x); }
+__device__ __forceinline__ float silu(float z) { return z * sigmoid_all(z); }
+// the tanh form of gelu: z/2 (1 + tanh(a)) = z sigmoid(2 a), a = sqrt(2/pi) (z + 0.044715 z^3)
+__device__ __forceinline__ float gelu_2a(float z) { return 1.5957691216057308f * fmaf(0.044715f * z * z, z, z); }
+__device__ __forceinline__ float gelu(float z) { return z * sigmoid_all(gelu_2a(z)); }
 
 __device__ __forceinline__ void unpack4(uint2 v, float (&f)[4]) {
   f[0] = row::bf16_lo(v.x);
@@ -80,10 +93,10 @@ __device__ __forceinline__ void epilogue4(const LinearArgs& a, int e, int64_t r,
   }
 }
 
-// 4 values over their block's scale as e4m3fn codes.
-__device__ __forceinline__ uint32_t codes4(const float (&y)[4], float scale) {
-  const uint32_t lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] / scale, y[1] / scale, 0, false);
-  return __builtin_amdgcn_cvt_pk_fp8_f32(y[2] / scale, y[3] / scale, lo, true);
+// 4 values times the reciprocal of their block's scale as e4m3fn codes.
+__device__ __forceinline__ uint32_t codes4(const float (&y)[4], float inv) {
+  const uint32_t lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * inv, y[1] * inv, 0, false);
+  return __builtin_amdgcn_cvt_pk_fp8_f32(y[2] * inv, y[3] * inv, lo, true);
 }
 
 // Calls f with the smallest of kQ / 4, kQ / 2, 3 kQ / 4 and kQ subtiles that covers `live`.
@@ -120,14 +133,24 @@ struct Forward {
   static constexpr int kLds = QS * QTile::kBytes + PS * kPBytes;
 };
 
-// Loads of a wave that may be outstanding when step s begins.  Each step issues the
-// rows of step s + QS - 1 and then the weights of step s + PS - 1.  With two stages
-// of rows only weights may be: those of step s + 1 where there is a third weight
-// stage (weights come from HBM, rows mostly from L2, where several column tiles read
-// them).  With more stages of rows there are as many of weights, and all stages but
-// the next may be.
+// The loop's order.  All stages are filled ahead of it; half-way through step s, when
+// its last operands are in registers, the waves meet, the buffers of step s are
+// filled with rows of step s + QS and weights of step s + PS, and the first operands
+// of step s + 1 are read, so that a wave's LDS reads and the next stages' loads run
+// beside its matrix instructions.  (With the reads in front of the instructions that
+// use them the matrix cores idled through them: 57% busy without any loads.)
+//
+// Loads of a wave that may be outstanding at that meeting: with two stages of rows
+// the weights of step s + 2 where there is a third weight stage (weights come from
+// HBM, rows mostly from L2, where several column tiles read them); with more, as
+// many of each, all stages but the next.
 constexpr int in_flight(int QS, int PS, int q_loads, int p_loads) {
   return QS == 2 ? (PS - 2) * p_loads : (PS - 2) * (q_loads + p_loads);
+}
+// ... and before step 0: those of the stages behind the first.  With two stages of
+// rows their number depends on the rows, so only the weights' are counted on.
+constexpr int in_flight_first(int QS, int PS, int q_loads, int p_loads) {
+  return QS == 2 ? (PS - 1) * p_loads : (PS - 1) * (q_loads + p_loads);
 }
 
 // Rows of a tile are dealt to the WQ rows of waves in subtiles of 16 in turn, so a
@@ -163,8 +186,11 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
   const int steps = (ld + DB - 1) / DB;
   // past the last step nothing is left: the loads are issued and fetch nothing
   auto issue_q = [&](int s, int stage) {
-    // a number of loads that depends on `live` must not be counted on
-    qt.load(rx, smem + stage * T::QTile::kBytes, wave, s * DB, ld - s * DB, QS == 2 ? live : BQ);
+    char* b = smem + stage * T::QTile::kBytes;
+    if constexpr (QS == 2)
+      qt.load_live(rx, b, wave, s * DB, ld - s * DB, live);
+    else  // the waits count on every load
+      qt.load(rx, b, wave, s * DB, ld - s * DB);
   };
   char* const weights = smem + QS * T::QTile::kBytes;
   auto issue_p = [&](int s, int stage) {
@@ -194,16 +220,11 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
     for (int h = 0; h < kParts; ++h) sw[h] = a.ws[h] + ((int64_t)it.e * nb + cb) * blocks;
   }
 
-  if (QS == 2) {
-    if (PS == 3) issue_p(0, 0);
-    issue_q(0, 0);
-    issue_p(PS - 2, PS - 2);
-  } else {
 #pragma unroll
-    for (int s = 0; s < QS - 1; ++s) {
-      issue_q(s, s);
-      issue_p(s, s);
-    }
+  for (int s = 0; s < PS; ++s) {
+    if (QS == 2 && s == 0) issue_p(0, 0);
+    if (s < QS) issue_q(s, s);
+    if (QS != 2 || s > 0) issue_p(s, s);
   }
 
   auto p_row = [&](int j) { return wp * (kCols / WP) + (j % kC) * 16; };
@@ -214,11 +235,26 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
 #pragma unroll
       for (int i = 0; i < L; ++i) sn[i] = sx[i][0];
     }
+    constexpr int kFirst = in_flight_first(QS, PS, T::QTile::kLoads, T::kPLoads);
+    constexpr int kNext = in_flight(QS, PS, T::QTile::kLoads, T::kPLoads);
     int stage = 0, qstage = 0;
-    for (int s = 0; s < steps; ++s) {
-      wait_and_meet<in_flight(QS, PS, T::QTile::kLoads, T::kPLoads)>();
-      float swc[kParts];
-      if constexpr (FP8) {
+    // fills the buffers of step s and moves on to those of step s + 1
+    auto advance = [&](int s) {
+      wait_and_meet<kNext>();
+      issue_q(s + QS, qstage);
+      issue_p(s + PS, stage);
+      qstage = qstage == QS - 1 ? 0 : qstage + 1;
+      stage = stage == PS - 1 ? 0 : stage + 1;
+    };
+    auto q_lds = [&] { return smem + qstage * T::QTile::kBytes; };
+    auto p_lds = [&](int j) { return weights + stage * T::kPBytes + j / kC * T::PTile::kBytes; };
+    wait_and_meet<kFirst>();
+    if constexpr (FP8) {
+      // The matrix cores' own 8-bit products lose the low bits of their sums
+      // (measured 1.5e-5 of the result on 128 terms), so the codes are widened to
+      // bf16, which is exact, and each scale block is scaled as it is added.
+      for (int s = 0; s < steps; ++s) {
+        float swc[kParts];
         const int nx = min(s + 1, steps - 1);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
@@ -227,24 +263,24 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
         }
 #pragma unroll
         for (int h = 0; h < kParts; ++h) swc[h] = sw[h][s];
-      }
-      issue_q(s + QS - 1, qstage == 0 ? QS - 1 : qstage - 1);
-      issue_p(s + PS - 1, stage == 0 ? PS - 1 : stage - 1);
-      const char* b = smem + qstage * T::QTile::kBytes;
-      const char* pb = weights + stage * T::kPBytes;
-      qstage = qstage == QS - 1 ? 0 : qstage + 1;
-      stage = stage == PS - 1 ? 0 : stage + 1;
-      if constexpr (FP8) {
-        // The matrix cores' own 8-bit products lose the low bits of their sums
-        // (measured 1.5e-5 of the result on 128 terms), so the codes are widened to
-        // bf16, which is exact, and each scale block is scaled as it is added.
         bf16x8 q[L][4];
+        {
+          typename T::QTile::Raw8 raw[L];
 #pragma unroll
-        for (int i = 0; i < L; ++i) T::QTile::frag8(b, q_row<WQ>(wq, i), lane, q[i]);
+          for (int i = 0; i < L; ++i) raw[i] = T::QTile::raw8(q_lds(), q_row<WQ>(wq, i), lane);
+#pragma unroll
+          for (int i = 0; i < L; ++i) T::QTile::widen(raw[i], q[i]);
+        }
+        typename T::PTile::Raw8 next = T::PTile::raw8(p_lds(0), p_row(0), lane);
 #pragma unroll
         for (int j = 0; j < kP; ++j) {
+          const typename T::PTile::Raw8 raw = next;
+          if (j + 1 < kP)
+            next = T::PTile::raw8(p_lds(j + 1), p_row(j + 1), lane);
+          else
+            advance(s);  // the stage's last operands are in registers
           bf16x8 p[4];
-          T::PTile::frag8(pb + j / kC * T::PTile::kBytes, p_row(j), lane, p);
+          T::PTile::widen(raw, p);
           f32x4 t[L];
 #pragma unroll
           for (int i = 0; i < L; ++i) t[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -259,19 +295,33 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
             for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(t[i][c], f, acc[i][j][c]);
           }
         }
-      } else {
+      }
+    } else {
+      static_assert(FP8 || DB == 128, "two 32-deep halves a stage");
+      bf16x8 q[2][L], p[2][kP];
+      auto read = [&](int kk) {
 #pragma unroll
-        for (int kk = 0; kk < DB / 64; ++kk) {
-          bf16x8 q[L], p[kP];
+        for (int i = 0; i < L; ++i) q[kk][i] = T::QTile::frag(q_lds(), q_row<WQ>(wq, i), kk, lane);
 #pragma unroll
-          for (int i = 0; i < L; ++i) q[i] = T::QTile::frag(b, q_row<WQ>(wq, i), kk, lane);
+        for (int j = 0; j < kP; ++j) p[kk][j] = T::PTile::frag(p_lds(j), p_row(j), kk, lane);
+      };
+      auto products = [&](int kk) {
 #pragma unroll
-          for (int j = 0; j < kP; ++j) p[j] = T::PTile::frag(pb + j / kC * T::PTile::kBytes, p_row(j), kk, lane);
+        for (int j = 0; j < kP; ++j)
 #pragma unroll
-          for (int j = 0; j < kP; ++j)
-#pragma unroll
-            for (int i = 0; i < L; ++i) acc[i][j] = mma::mfma(p[j], q[i], acc[i][j]);
-        }
+          for (int i = 0; i < L; ++i) acc[i][j] = mma::mfma(p[kk][j], q[kk][i], acc[i][j]);
+      };
+      read(0);
+      for (int s = 0; s < steps; ++s) {
+        read(1);
+        __builtin_amdgcn_sched_barrier(0);  // the reads are on their way before the products
+        products(0);
+        __builtin_amdgcn_sched_barrier(0);
+        advance(s);
+        read(0);  // of step s + 1; past the last one whatever lies there, unused
+        __builtin_amdgcn_sched_barrier(0);
+        products(1);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
@@ -363,10 +413,11 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
       const float scale = row::block_scale(mx);
       if (m < live && colw < cols && colw % row::kScaleBlock == 0)
         a.y_scale[(first + m) * (a.N / row::kScaleBlock) + (p0 + colw) / row::kScaleBlock] = scale;
+      const float inv = 1.0f / scale;
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
         const float y[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        Codes::put(codes, m, colw + j * 16, codes4(y, scale));
+        Codes::put(codes, m, colw + j * 16, codes4(y, inv));
       }
     }
     __syncthreads();
@@ -498,7 +549,7 @@ __global__ __launch_bounds__(WC* WK * 64) void linear_few_kernel(LinearArgs a) {
 #pragma unroll
       for (int i = 0; i < WC; ++i) mx = max(mx, red[i][m]);
       const float scale = row::block_scale(mx);
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + (first + m) * a.N + n) = codes4(y, scale);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + (first + m) * a.N + n) = codes4(y, 1.0f / scale);
       if (n % row::kScaleBlock == 0) a.y_scale[(first + m) * (a.N / row::kScaleBlock) + n / row::kScaleBlock] = scale;
     }
   }
@@ -532,7 +583,7 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_x_kernel(Linea
   // past the last step nothing is left: the loads are issued and fetch nothing
   auto issue_q = [&](int s) {
     const int h = s >= per ? 1 : 0, k = s - h * per;
-    qt.load(rq, smem + (s & 1) * QTile::kBytes, wave, (h * a.N + k * kD) * 2, s < steps ? (a.N - k * kD) * 2 : 0, live);
+    qt.load_live(rq, smem + (s & 1) * QTile::kBytes, wave, (h * a.N + k * kD) * 2, s < steps ? (a.N - k * kD) * 2 : 0, live);
   };
   char* const weights = smem + 2 * QTile::kBytes;
   auto issue_p = [&](int s, int stage) {
@@ -545,31 +596,43 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_x_kernel(Linea
   for (int i = 0; i < kQ; ++i)
 #pragma unroll
     for (int j = 0; j < kP; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (PS == 3) issue_p(0, 0);
-  issue_q(0);
-  issue_p(PS - 2, PS - 2);
+#pragma unroll
+  for (int s = 0; s < PS; ++s) {
+    issue_p(s, s);
+    if (s < 2) issue_q(s);
+  }
   auto multiply = [&](auto live_subtiles) {
     constexpr int L = decltype(live_subtiles)::value;
     int stage = 0;
-    for (int s = 0; s < steps; ++s) {
-      wait_and_meet<in_flight(2, PS, QTile::kLoads, PTile::kLoads)>();
-      issue_q(s + 1);
-      issue_p(s + PS - 1, stage == 0 ? PS - 1 : stage - 1);
+    bf16x8 q[2][L], p[2][kP];
+    auto read = [&](int s, int kk) {
       const char* b = smem + (s & 1) * QTile::kBytes;
-      const char* pb = weights + stage * PTile::kBytes;
+#pragma unroll
+      for (int i = 0; i < L; ++i) q[kk][i] = QTile::frag(b, q_row<WQ>(wq, i), kk, lane);
+#pragma unroll
+      for (int j = 0; j < kP; ++j) p[kk][j] = PTile::frag(weights + stage * PTile::kBytes, wp * (BP / WP) + j * 16, kk, lane);
+    };
+    auto products = [&](int kk) {
+#pragma unroll
+      for (int j = 0; j < kP; ++j)
+#pragma unroll
+        for (int i = 0; i < L; ++i) acc[i][j] = mma::mfma(p[kk][j], q[kk][i], acc[i][j]);
+    };
+    wait_and_meet<in_flight_first(2, PS, QTile::kLoads, PTile::kLoads)>();
+    read(0, 0);
+    for (int s = 0; s < steps; ++s) {  // in the forward kernel's order
+      read(s, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      products(0);
+      __builtin_amdgcn_sched_barrier(0);
+      wait_and_meet<in_flight(2, PS, QTile::kLoads, PTile::kLoads)>();
+      issue_q(s + 2);
+      issue_p(s + PS, stage);
       stage = stage == PS - 1 ? 0 : stage + 1;
-#pragma unroll
-      for (int kk = 0; kk < kD / 32; ++kk) {
-        bf16x8 q[L], p[kP];
-#pragma unroll
-        for (int i = 0; i < L; ++i) q[i] = QTile::frag(b, q_row<WQ>(wq, i), kk, lane);
-#pragma unroll
-        for (int j = 0; j < kP; ++j) p[j] = PTile::frag(pb, wp * (BP / WP) + j * 16, kk, lane);
-#pragma unroll
-        for (int j = 0; j < kP; ++j)
-#pragma unroll
-          for (int i = 0; i < L; ++i) acc[i][j] = mma::mfma(p[j], q[i], acc[i][j]);
-      }
+      read(s + 1, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      products(1);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
   by_live_subtiles<kQ>((live - wq * 16 + 16 * WQ - 1) / (16 * WQ), multiply);
@@ -756,21 +819,21 @@ __global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs a, const u
     row::load8(dy + r * a.N, c, a.N, g);
     row::load8(pre + r * a.parts * a.N, c, a.N, z);
     if (a.act == MOE_ACT_GELU) {
+      // s + 2 z s (1 - s) a', s = sigmoid(2 a)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float t = tanhf(gelu_tanh_arg(z[j]));
-        const float d = 0.7978845608028654f * fmaf(3.0f * 0.044715f * z[j], z[j], 1.0f);
-        // where tanh has reached 1 its slope is 0, also where d overflows
-        const float bend = 1.0f - t * t;
-        o[j] = g[j] * (0.5f * (1.0f + t) + (bend > 0.f ? 0.5f * z[j] * bend * d : 0.f));
+        const float s = sigmoid_all(gelu_2a(z[j]));
+        const float d = 1.5957691216057308f * fmaf(3.0f * 0.044715f * z[j], z[j], 1.0f);
+        // where the sigmoid has reached 0 or 1 its slope is 0, also where a' overflows
+        const float bend = s * (1.0f - s);
+        o[j] = g[j] * (s + (bend > 0.f ? z[j] * bend * d : 0.f));
       }
     } else {
-      float u[8];
+      float u[8], o2[8];
       if (a.act == MOE_ACT_SWIGLU) row::load8(pre + r * 2 * a.N + a.N, c, a.N, u);
-      float o2[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float s = 1.0f / (1.0f + expf(-z[j]));
+        const float s = sigmoid_all(z[j]);
         const float d = s * fmaf(z[j], 1.0f - s, 1.0f);
         if (a.act == MOE_ACT_SWIGLU) {
           o[j] = g[j] * u[j] * d;
@@ -789,20 +852,21 @@ __global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs a, const u
 
 // Instantiated by name: the host pass of this compiler otherwise leaves out the
 // launch stubs of some kernel templates that are only reached through pointers.
-#define MOE_TILES(F, G)                                                        \
-  template __global__ void linear_kernel<F, G, 64, 64, 2, 2, 128, 4, 4>(LinearArgs);   \
-  template __global__ void linear_kernel<F, G, 128, 128, 2, 2, 128, 2, 3>(LinearArgs); \
-  template __global__ void linear_few_kernel<F, G, 1, 16>(LinearArgs);         \
+#define MOE_TILES(F, G)                                                              \
+  template __global__ void linear_kernel<F, G, 64, 64, 2, 2, 128, 4, 4>(LinearArgs);         \
+  template __global__ void linear_kernel<F, G, 128, 128, F ? 4 : 2, 2, 128, 2, 3>(LinearArgs); \
+  template __global__ void linear_few_kernel<F, G, 1, 16>(LinearArgs);               \
   template __global__ void linear_few_kernel<F, G, 8, 2>(LinearArgs);
 MOE_TILES(false, false)
 MOE_TILES(false, true)
 MOE_TILES(true, false)
 MOE_TILES(true, true)
 #undef MOE_TILES
-template __global__ void linear_kernel<false, false, 256, 256, 4, 4, 128, 2, 3>(LinearArgs);
-template __global__ void linear_kernel<false, true, 256, 256, 4, 4, 128, 2, 3>(LinearArgs);
-template __global__ void linear_kernel<true, true, 64, 256, 1, 4, 128, 2, 2>(LinearArgs);
+template __global__ void linear_kernel<false, false, 256, 256, 2, 4, 128, 2, 3>(LinearArgs);
+template __global__ void linear_kernel<false, true, 256, 256, 2, 4, 128, 2, 3>(LinearArgs);
+template __global__ void linear_kernel<true, true, 64, 256, 2, 4, 128, 2, 2>(LinearArgs);
 template __global__ void linear_backward_x_kernel<128, 128, 2, 2, 3>(LinearArgs);
+template __global__ void linear_backward_x_kernel<256, 256, 2, 4, 3>(LinearArgs);
 template __global__ void linear_backward_w_kernel<false, 128, 128, 2, 2, 32, 2, 4>(LinearArgs);
 template __global__ void linear_backward_w_kernel<true, 128, 128, 2, 2, 32, 2, 3>(LinearArgs);
 
@@ -836,6 +900,17 @@ constexpr int kBQ = 128, kBP = 128;
 // Rows per expert on average; the runs themselves are known on the device only.
 int64_t mean_rows(const LinearArgs& a) { return (a.rows + a.E - 1) / a.E; }
 
+// Square tiles of `edge` that the rows and `cols` columns make.
+int64_t tiles(const LinearArgs& a, int64_t cols, int64_t edge) {
+  return (a.rows + edge - 1) / edge * ((cols + edge - 1) / edge);
+}
+
+// 256-wide tiles read each operand byte half as often as 128-wide ones and are four
+// times the work: taken where they fill the GPU and the runs fill most of them
+// (32768 dense rows, gate+up of 1536 x 2048: 177 against 196 us; 128 experts of 256
+// rows on average: 303 against 309).
+bool wide_tiles(const LinearArgs& a, int64_t cols) { return tiles(a, cols, 256) >= 256 && mean_rows(a) >= 160; }
+
 // Rows per expert up to which the depth-split kernel is taken.
 constexpr int64_t kFewRows = 32;
 
@@ -843,16 +918,18 @@ template <bool FP8, bool GATED>
 hipError_t forward_by_shape(const LinearArgs& a, hipStream_t s) {
   if (mean_rows(a) <= kFewRows) return a.y_scale != nullptr ? run_few<FP8, GATED, 8, 2>(a, s) : run_few<FP8, GATED, 1, 16>(a, s);
   const bool codes = a.y_scale != nullptr;  // 8-bit rows need whole scale blocks of columns in a tile
-  auto tiles = [&](int64_t bq, int64_t bp) { return (a.rows + bq - 1) / bq * ((a.parts * (int64_t)a.N + bp - 1) / bp); };
   if (GATED && codes) {
-    // a tile with 128 columns of SwiGLU takes 256 weight rows
-    if constexpr (FP8 && GATED) return run_forward<FP8, GATED, 64, 256, 1, 4, 128, 2, 2>(a, s);
-    if constexpr (!FP8 && GATED) return run_forward<FP8, GATED, 256, 256, 4, 4, 128, 2, 3>(a, s);
+    // a tile with 128 columns of SwiGLU takes 256 weight rows; 8-bit operands: 32 x 64
+    // per wave, which leaves room for 4 waves per SIMD (291 us at 32768 rows; 64 x 64
+    // with 2: 322)
+    if constexpr (FP8 && GATED) return run_forward<FP8, GATED, 64, 256, 2, 4, 128, 2, 2>(a, s);
+    if constexpr (!FP8 && GATED) return run_forward<FP8, GATED, 256, 256, 2, 4, 128, 2, 3>(a, s);
   }
-  if (!codes && tiles(128, 128) < 256) return run_forward<FP8, GATED, 64, 64, 2, 2, 128, 4, 4>(a, s);
+  // few tiles: smaller ones, and more stages ahead of the one workgroup a compute unit has
+  if (!codes && tiles(a, a.parts * (int64_t)a.N, 128) < 256) return run_forward<FP8, GATED, 64, 64, 2, 2, 128, 4, 4>(a, s);
   if constexpr (!FP8)
-    if (tiles(256, 256) >= 256 && mean_rows(a) >= 160) return run_forward<FP8, GATED, 256, 256, 4, 4, 128, 2, 3>(a, s);
-  return run_forward<FP8, GATED, 128, 128, 2, 2, 128, 2, 3>(a, s);
+    if (wide_tiles(a, a.parts * (int64_t)a.N)) return run_forward<FP8, GATED, 256, 256, 2, 4, 128, 2, 3>(a, s);
+  return run_forward<FP8, GATED, 128, 128, FP8 ? 4 : 2, 2, 128, 2, 3>(a, s);
 }
 }  // namespace
 
@@ -861,10 +938,16 @@ hipError_t launch_linear(const LinearArgs& a, bool fp8, hipStream_t s) {
   return a.parts == 2 ? forward_by_shape<false, true>(a, s) : forward_by_shape<false, false>(a, s);
 }
 
-hipError_t launch_linear_backward_x(const LinearArgs& a, hipStream_t s) {
+template <int B, int WQ, int WP>
+hipError_t run_backward_x(const LinearArgs& a, hipStream_t s) {
   static std::atomic<size_t> allowed[kMaxCachedDevices];
-  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, kBQ) * ((a.K + kBP - 1) / kBP);
-  return launch(&linear_backward_x_kernel<kBQ, kBP, 2, 2, 3>, items, 256, (2 * kBQ + 3 * kBP) * 128, a, s, allowed);
+  constexpr int kPS = 3;
+  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, B) * ((a.K + B - 1) / B);
+  return launch(&linear_backward_x_kernel<B, B, WQ, WP, kPS>, items, WQ * WP * 64, (2 + kPS) * B * 128, a, s, allowed);
+}
+
+hipError_t launch_linear_backward_x(const LinearArgs& a, hipStream_t s) {
+  return wide_tiles(a, a.K) ? run_backward_x<256, 2, 4>(a, s) : run_backward_x<128, 2, 2>(a, s);
 }
 
 int backward_w_splits(int64_t rows, int E, int N, int K, int parts) {

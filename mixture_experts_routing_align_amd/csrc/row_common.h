@@ -156,13 +156,14 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
   return fmaxf(__uint_as_float(amax_bits) / kE4m3Max, kMinScale);
 }
 
-// 8 values over the block's scale as e4m3fn codes, round to nearest even.  The
-// quotient is at most 448 (1 + 2^-23), which rounds to 448; with a NaN scale
-// every code is NaN.
+// 8 values times the reciprocal of the block's scale as e4m3fn codes, round to
+// nearest even.  The product is at most 448 (1 + 2^-22), which rounds to 448; with
+// a NaN scale every code is NaN.
 __device__ __forceinline__ void e4m3x8(const float (&v)[8], float scale, uint32_t& lo, uint32_t& hi) {
+  const float inv = 1.0f / scale;
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = v[i] / scale;
+  for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
   hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
