@@ -7,8 +7,11 @@
 //
 // All three are bound by HBM and walk tokens, not sorted rows: a token's own row
 // is then read or written once whatever top_k is, each sorted row is touched by
-// one wave, and nothing needs an atomic.  Many tokens: a wave per token.  Few: a
-// workgroup of 4 waves per token, so that a row's loads are issued side by side.
+// one wave, and nothing needs an atomic.  Many tokens with short rows: a wave per
+// token; else a workgroup of 4 waves, whose loads of a long row run side by side.
+// Measured at 2048 columns and top-8: 8-bit rows of 16384 tokens laid out in 50 us
+// (5.7 TB/s of what has to move), rows of 8192 tokens back in 53 us (5.7 TB/s), the
+// gradient in 124 us (4.6 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -24,6 +27,7 @@ using namespace row;
 constexpr int kThreads = 256;
 constexpr int kBatch = 8;          // slots of a token handled side by side
 constexpr int64_t kWaveTokens = 2048;  // from here on a wave per token
+constexpr int64_t kCacheBytes = 192 << 20;  // rows past this do not stay in the 256 MB memory-side cache
 
 // A row of `bytes` moves 16 bytes per lane at any 2-byte alignment; the last
 // piece may be shorter (an even number of bytes).
@@ -41,9 +45,15 @@ __device__ __forceinline__ uint4 load_piece(const uint8_t* p, int c, int bytes) 
   }
   return v;
 }
+// PAST_CACHE: not kept in the caches.
+template <bool PAST_CACHE>
 __device__ __forceinline__ void store_piece(uint8_t* p, int c, int bytes, uint4 v) {
   if (c + 16 <= bytes) {
-    *reinterpret_cast<u32x4_e2*>(p + c) = u32x4_e2{v.x, v.y, v.z, v.w};
+    const u32x4_e2 q{v.x, v.y, v.z, v.w};
+    if constexpr (PAST_CACHE)
+      __builtin_nontemporal_store(q, reinterpret_cast<u32x4_e2*>(p + c));
+    else
+      *reinterpret_cast<u32x4_e2*>(p + c) = q;
   } else {
     const uint32_t d[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -60,7 +70,7 @@ __device__ __forceinline__ int position(const int32_t* perm, int64_t i, int64_t 
 }
 
 // TPT threads a token (64 or 256).
-template <int TPT>
+template <int TPT, bool PAST_CACHE>
 __global__ __launch_bounds__(kThreads) void permute_kernel(PermuteArgs a) {
   const int64_t t = (int64_t)blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;
   if (t >= a.M) return;
@@ -76,7 +86,7 @@ __global__ __launch_bounds__(kThreads) void permute_kernel(PermuteArgs a) {
       const uint4 v = load_piece(x, c, a.row_bytes);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (p[k] >= 0) store_piece(out + (int64_t)p[k] * a.row_bytes, c, a.row_bytes, v);
+        if (p[k] >= 0) store_piece<PAST_CACHE>(out + (int64_t)p[k] * a.row_bytes, c, a.row_bytes, v);
     }
     if (a.scales) {
       for (int c = j; c < a.scales; c += TPT) {
@@ -178,20 +188,30 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(UnpermuteB
   }
 }
 
+// Back to token order: a wave per token where there are many and its row keeps no more
+// than half a workgroup busy (8192 tokens x 2048, top-8: 53 us with a workgroup, 66
+// with a wave, the gradient 124 and 140; 16384 x 1024, top-4: 30 and 27, 85 and 55).
+bool wave_per_token(int64_t M, int H) { return M >= kWaveTokens && H <= 1024; }
+
 unsigned blocks_for(int64_t M, int per) { return (unsigned)((M + per - 1) / per); }
 
 }  // namespace
 
 hipError_t launch_permute(const PermuteArgs& a, hipStream_t s) {
-  if (a.M >= kWaveTokens)
-    hipLaunchKernelGGL((permute_kernel<64>), dim3(blocks_for(a.M, 4)), dim3(kThreads), 0, s, a);
+  // Rows that the caches cannot keep for their reader go past them (277 MB of 8-bit
+  // rows: 50 against 64 us).
+  const bool past = a.rows * a.row_bytes > kCacheBytes;
+  if (a.M < kWaveTokens)
+    hipLaunchKernelGGL((permute_kernel<256, false>), dim3(blocks_for(a.M, 1)), dim3(kThreads), 0, s, a);
+  else if (past)
+    hipLaunchKernelGGL((permute_kernel<64, true>), dim3(blocks_for(a.M, 4)), dim3(kThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((permute_kernel<256>), dim3(blocks_for(a.M, 1)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((permute_kernel<64, false>), dim3(blocks_for(a.M, 4)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_unpermute(const UnpermuteArgs& a, hipStream_t s) {
-  const bool wave = a.M >= kWaveTokens;
+  const bool wave = wave_per_token(a.M, a.H);
   const dim3 grid(blocks_for(a.M, wave ? 4 : 1)), block(kThreads);
   if (a.w != nullptr) {
     if (wave)
@@ -208,7 +228,7 @@ hipError_t launch_unpermute(const UnpermuteArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_unpermute_backward(const UnpermuteBackwardArgs& a, hipStream_t s) {
-  if (a.M >= kWaveTokens)
+  if (wave_per_token(a.M, a.H))
     hipLaunchKernelGGL((unpermute_backward_kernel<64>), dim3(blocks_for(a.M, 4)), dim3(kThreads), 0, s, a);
   else
     hipLaunchKernelGGL((unpermute_backward_kernel<256>), dim3(blocks_for(a.M, 1)), dim3(kThreads), 0, s, a);
