@@ -74,7 +74,7 @@ int check_product(const char* fn, int64_t rows, int32_t E, int32_t N, int32_t K,
     return fail_status(MOE_ERR_LIMIT, "%s: one expert's weights, %d x %d, reach 2^31 bytes", fn, N, K);
   if ((int64_t)std::max(K, N * (int64_t)parts > INT32_MAX ? INT32_MAX : N * parts) * item * 256 >= kInt32Limit)
     return fail_status(MOE_ERR_LIMIT, "%s: 256 rows of %d or %d x %d elements reach 2^31 bytes", fn, K, parts, N);
-  // tiles of all experts, one workgroup each (128-row tiles of 64 columns at the least)
+  // the smallest tiles there are, 16 rows by 16 columns, counted in 31 bits
   const int64_t tiles = (rows / 16 + std::min<int64_t>(E, rows)) * ((std::max(N, K) + 15) / 16);
   if (tiles >= kInt32Limit) return fail_status(MOE_ERR_LIMIT, "%s: %lld tiles reach 2^31", fn, (long long)tiles);
   return MOE_OK;
@@ -230,7 +230,6 @@ int moe_grouped_linear(const moe_linear_desc* d, hipStream_t stream) {
     return fail_status(MOE_ERR_SHAPE, "%s: 8-bit rows need N=%d in whole 128-column blocks", fn, d->N);
   if (!gated && (d->up.w != nullptr || d->up_bias != nullptr))
     return fail_status(MOE_ERR_SHAPE, "%s: up weights or bias without the SwiGLU activation", fn);
-  if (d->up_bias != nullptr && d->bias == nullptr) return fail_status(MOE_ERR_SHAPE, "%s: up_bias without bias", fn);
   if (d->rows == 0) return MOE_OK;
   if (d->x == nullptr) return null_arg(fn, "x");
   if (d->w.w == nullptr) return null_arg(fn, "w");

@@ -343,7 +343,6 @@ def moe_grouped_linear(x: torch.Tensor, w, expert_offsets: Optional[torch.Tensor
         _matrix(bias, "bias", _BF16, None, dev)
         _need(bias.numel() == E * N, "bias must be [E, N]")
     if up_bias is not None:
-        _need(bias is not None, "up_bias goes with bias")
         _matrix(up_bias, "up_bias", _BF16, None, dev)
         _need(up_bias.numel() == E * N, "up_bias must be [E, N]")
     if residual is not None:

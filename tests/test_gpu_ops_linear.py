@@ -362,3 +362,41 @@ def test_graph_replay(moe):
         torch.cuda.synchronize()
         for a, b in zip(outs, step()):
             assert torch.equal(a, b)
+
+
+def test_biases_are_independent(moe):
+    """Either bias of a gated product may be left out."""
+    g = gen(3)
+    r = Routed(moe, 60, 4, 2, 16, 1)
+    N, K = 72, 136
+    x, w, up = poison(randn(g, r.rows, K), r.kept), (randn(g, 4, N, K, scale=0.1), None), (randn(g, 4, N, K, scale=0.1), None)
+    b = randn(g, 4, N)
+    for bias, up_bias in ((b, None), (None, b)):
+        y, _, _ = moe.moe_grouped_linear(x, w, r.offsets, r.counts, act="swiglu", up=up, bias=bias, up_bias=up_bias)
+        ref, err, _, _ = reference(r, x.double(), w, up, bias, up_bias, None, "swiglu")
+        k = r.kept
+        assert_within(y[k], ref[k], BF * (ref[k].abs() + err[k]) + err[k] + 1e-37, "y")
+
+
+def test_rows_of_a_tile_do_not_mix(moe):
+    """A NaN or an infinity in one row stays in that row's results, whole and partly
+    filled tiles alike; far activations keep their limits."""
+    g = gen(8)
+    for rows in (20, 300, 1000):
+        x, w = randn(g, rows, 264), randn(g, 1, 520, 264, scale=0.1)
+        a, _, _ = moe.moe_grouped_linear(x, w, act="silu")
+        x[7] = float("nan")
+        x[rows - 1, 3] = float("inf")
+        b, _, _ = moe.moe_grouped_linear(x, w, act="silu")
+        torch.cuda.synchronize()
+        assert bool(b[7].isnan().all())
+        rest = [i for i in range(rows) if i not in (7, rows - 1)]
+        assert torch.equal(a[rest], b[rest])
+    # identity weights: z itself through the activations
+    z = torch.tensor([0.0, -0.0, 90.0, -90.0, 3e38, -3e38, float("inf"), float("nan")], device="cuda").to(torch.bfloat16)
+    eye = torch.eye(8, device="cuda").to(torch.bfloat16)[None]
+    x = torch.diag(z.nan_to_num(1.0, 1.0)).to(torch.bfloat16)
+    for act in ("silu", "gelu"):
+        y, _, _ = moe.moe_grouped_linear(x, eye, act=act)
+        d = torch.diagonal(y).float()
+        assert d[0] == 0 and d[1] == 0 and d[2] == 90 and abs(float(d[3])) < 1e-35 and d[4] == z[4].float() and d[5] == 0, act

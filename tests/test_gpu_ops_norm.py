@@ -148,6 +148,10 @@ def test_backward(moe, M, H, zt, with_dz):
     mag = r * (t.abs() + n.abs() * (t * n).abs().mean(1, keepdim=True)) + (dz.double().abs() if with_dz else 0.0)
     assert_within(dx, ref, half(zt) * ref.abs() + (DEPTH + 8) * SUM * mag + 1e-37, "dx")
     assert_within(dw, (dy.double() * n).sum(0), (M + 16) * SUM * (dy.double() * n).abs().sum(0) + 1e-37, "dw")
+    if zt == torch.bfloat16:  # over the buffer of dy
+        own = dy.clone()
+        again, dw2 = moe.moe_add_rms_norm_backward(own, z, w, rstd, dz=dz, dx=own)
+        assert torch.equal(again, dx) and torch.equal(dw2, dw)
     # without the weight's gradient, and over the buffer of dz
     again, none = moe.moe_add_rms_norm_backward(dy, z, w, rstd, dz=dz, need_dweight=False, dx=dz)
     assert none is None and torch.equal(again, dx)

@@ -19,6 +19,7 @@ CASES = [  # M, E, k, BS, H, mode, drop
     (129, 4, 2, 64, 4096, "one", 0.0),
     (2500, 32, 4, 16, 520, "skew", 0.1),
     (2300, 64, 9, 16, 2047, "random", 0.0),
+    (2200, 16, 11, 16, 264, "random", 0.1),
     (40, 8, 2, 16, 256, "random", 1.0),  # every slot dropped
 ]
 
@@ -86,6 +87,19 @@ def test_permute_8bit(moe, M, E, k, BS, H):
     assert torch.equal(out_scale[p[slots]], scale[slots // k])
     assert_untouched(out, r.kept)
     assert_untouched(out_scale, r.kept)
+
+
+def test_permute_past_the_caches(moe):
+    """Sorted rows too large for the caches take stores of their own."""
+    M, E, k, H = 2100, 16, 8, 6200
+    r = Routed(moe, M, E, k, 1, 2)
+    assert r.rows * H * 2 > 192 << 20
+    x = randn(gen(1), M, H)
+    out, _ = moe.moe_permute(x, r.perm, k, r.rows)
+    torch.cuda.synchronize()
+    p = r.perm.long()
+    for lo in range(0, M * k, 4000):
+        assert torch.equal(out[p[lo:lo + 4000]], x[torch.arange(lo, min(lo + 4000, M * k), device="cuda") // k])
 
 
 def test_positions_out_of_range_are_skipped(moe):
