@@ -30,7 +30,6 @@ from ._ffi import (
     MOE_DT_BF16,
     MOE_DT_E4M3,
     MOE_DT_F32,
-    MOE_OK,
     MOE_W_BF16,
     MOE_W_FP8_E4M3,
     MoeLinearDesc,
@@ -48,7 +47,7 @@ def _need(cond: bool, msg: str) -> None:
 
 
 def _check(rc: int) -> None:
-    if rc != MOE_OK:
+    if rc:  # not MOE_OK
         from . import MoeError
 
         raise MoeError(rc, _ffi.load().moe_last_error().decode())
@@ -62,8 +61,8 @@ def _ptr(t: Optional[torch.Tensor]):
 # the raw handle of the current stream and the device index are read from torch's
 # C layer (0.1 us each; torch.cuda.current_stream() builds an object, 2.8 us), and
 # each tensor is checked in one expression that only a refusal looks into.
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream, dev: int) -> int:
@@ -76,19 +75,20 @@ def _stream(stream, dev: int) -> int:
 
 def _device(t, what: str) -> int:
     """Index of the GPU `t` lives on, which must be the current one."""
-    _need(isinstance(t, torch.Tensor), f"{what} must be a tensor")
-    dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError(f"{what} must be on the current GPU")
-    return dev
+    if isinstance(t, torch.Tensor):
+        dev = t.get_device()
+        if dev >= 0 and dev == _current_device():
+            return dev
+        raise ValueError(what + " must be on the current GPU")
+    raise ValueError(what + " must be a tensor")
 
 
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """A tensor on the device of `like` whose memory belongs to the stream the call runs on."""
     if stream is None:
-        if dtype is like.dtype and shape == like.shape:
-            return torch.empty_like(like, memory_format=torch.contiguous_format)
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        if dtype is like.dtype:
+            return like.new_empty(shape)
+        return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
@@ -97,16 +97,16 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
 
 def _matrix(t, what: str, dtypes, shape, dev: int) -> None:
     """`t` is a contiguous tensor of one of `dtypes` and of `shape` (None: any) on device `dev`."""
-    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and (shape is None or t.shape == shape) and t.is_contiguous()
-            and t.get_device() == dev):
-        return
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
-        raise ValueError(f"{what} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{what} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    raise ValueError(f"{what} must be on the current GPU")
+    if isinstance(t, torch.Tensor):
+        if t.dtype in dtypes and (shape is None or t.shape == shape) and t.is_contiguous() and t.get_device() == dev:
+            return
+        if t.dtype in dtypes:
+            if shape is not None and t.shape != shape:
+                raise ValueError(f"{what} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+            if not t.is_contiguous():
+                raise ValueError(f"{what} must be contiguous")
+            raise ValueError(f"{what} must be on the current GPU")
+    raise ValueError(f"{what} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
 
 
 def _out(t, shape, dtype, like, stream, what: str, dev: int) -> torch.Tensor:
