@@ -116,9 +116,8 @@ __device__ __forceinline__ void by_live_subtiles(int live, F f) {
 
 // A workgroup's tile: BQ rows by BP weight rows (SwiGLU: BP / 2 of the gate and
 // the same BP / 2 of the up weight, so that a lane holds z and u of its elements),
-// WQ x WP waves, DB bytes of depth per stage, QS stages of rows and PS of weights
-// in LDS.
-template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int QS, int PS>
+// WQ x WP waves, QS stages of rows and PS of weights in LDS.
+template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int QS, int PS>
 struct Forward {
   static constexpr int kWaves = WQ * WP, kThreads = kWaves * 64;
   static constexpr int kParts = GATED ? 2 : 1;
@@ -126,8 +125,8 @@ struct Forward {
   static constexpr int kQ = BQ / WQ / 16;        // 16-row subtiles per wave
   static constexpr int kP = BP / WP / 16;        // 16-column subtiles per wave, all parts
   static constexpr int kC = kP / kParts;         // of them per part
-  using QTile = RowTile<BQ, DB, kWaves>;
-  using PTile = RowTile<kCols, DB, kWaves>;
+  using QTile = RowTile<BQ, kWaves>;
+  using PTile = RowTile<kCols, kWaves>;
   static constexpr int kPBytes = kParts * PTile::kBytes;
   static constexpr int kPLoads = kParts * PTile::kLoads;
   static constexpr int kLds = QS * QTile::kBytes + PS * kPBytes;
@@ -159,12 +158,12 @@ constexpr int in_flight_first(int QS, int PS, int q_loads, int p_loads) {
 template <int WQ>
 __device__ __forceinline__ int q_row(int wq, int i) { return (i * WQ + wq) * 16; }
 
-template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int QS, int PS>
+template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int QS, int PS>
 __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
-  using T = Forward<FP8, GATED, BQ, BP, WQ, WP, DB, QS, PS>;
+  using T = Forward<FP8, GATED, BQ, BP, WQ, WP, QS, PS>;
   static_assert((QS == 2 && (PS == 2 || PS == 3)) || (QS > 2 && QS == PS), "the waits are counted for these");
   constexpr int kQ = T::kQ, kP = T::kP, kC = T::kC, kParts = T::kParts, kCols = T::kCols;
-  static_assert(!FP8 || DB == row::kScaleBlock, "a stage of 8-bit depth is one scale block");
+  static_assert(kDB == row::kScaleBlock, "a stage of 8-bit depth is one scale block");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wq = wave / WP, wp = wave % WP;
   const Item it = find_item(a, blockIdx.x, BQ, (a.N + kCols - 1) / kCols);
@@ -183,20 +182,20 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
   typename T::PTile pt;
   qt.init(wave, lane, [&](int r) { return r < live ? (uint32_t)(r * ld) : kNoFetch; });
   pt.init(wave, lane, [&](int r) { return p0 + r < a.N ? (uint32_t)((p0 + r) * ld) : kNoFetch; });
-  const int steps = (ld + DB - 1) / DB;
+  const int steps = (ld + kDB - 1) / kDB;
   // past the last step nothing is left: the loads are issued and fetch nothing
   auto issue_q = [&](int s, int stage) {
     char* b = smem + stage * T::QTile::kBytes;
     if constexpr (QS == 2)
-      qt.load_live(rx, b, wave, s * DB, ld - s * DB, live);
+      qt.load_live(rx, b, wave, s * kDB, ld - s * kDB, live);
     else  // the waits count on every load
-      qt.load(rx, b, wave, s * DB, ld - s * DB);
+      qt.load(rx, b, wave, s * kDB, ld - s * kDB);
   };
   char* const weights = smem + QS * T::QTile::kBytes;
   auto issue_p = [&](int s, int stage) {
 #pragma unroll
     for (int h = 0; h < kParts; ++h)
-      pt.load(rw[h], weights + stage * T::kPBytes + h * T::PTile::kBytes, wave, s * DB, ld - s * DB);
+      pt.load(rw[h], weights + stage * T::kPBytes + h * T::PTile::kBytes, wave, s * kDB, ld - s * kDB);
   };
 
   f32x4 acc[kQ][kP];
@@ -297,7 +296,7 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
         }
       }
     } else {
-      static_assert(FP8 || DB == 128, "two 32-deep halves a stage");
+      static_assert(kDB == 128, "two 32-deep halves a stage");
       bf16x8 q[2][L], p[2][kP];
       auto read = [&](int kk) {
 #pragma unroll
@@ -561,7 +560,7 @@ template <int BQ, int BP, int WQ, int WP, int PS>
 __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_x_kernel(LinearArgs a) {
   constexpr int kWaves = WQ * WP, kQ = BQ / WQ / 16, kP = BP / WP / 16, kD = 64;
   static_assert(PS == 2 || PS == 3, "waits are counted for two or three weight stages");
-  using QTile = RowTile<BQ, kD * 2, kWaves>;
+  using QTile = RowTile<BQ, kWaves>;
   using PTile = DepthTile<BP, kD, kWaves>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wq = wave / WP, wp = wave % WP;
@@ -586,10 +585,12 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_x_kernel(Linea
     qt.load_live(rq, smem + (s & 1) * QTile::kBytes, wave, (h * a.N + k * kD) * 2, s < steps ? (a.N - k * kD) * 2 : 0, live);
   };
   char* const weights = smem + 2 * QTile::kBytes;
+  const char* const w0 = static_cast<const char*>(a.w[0]) + expert;
+  const char* const w1 = a.parts == 2 ? static_cast<const char*>(a.w[1]) + expert : w0;
   auto issue_p = [&](int s, int stage) {
     const int h = s >= per ? 1 : 0, k = s - h * per;
-    pt.load(resource(static_cast<const char*>(a.w[s < steps ? h : 0]) + expert + (int64_t)k * kD * ldp),
-            weights + stage * PTile::kBytes, wave, 0, s < steps ? a.N - k * kD : 0);
+    pt.load(resource((h ? w1 : w0) + (int64_t)k * kD * ldp), weights + stage * PTile::kBytes, wave, 0,
+            s < steps ? a.N - k * kD : 0);
   };
   f32x4 acc[kQ][kP];
 #pragma unroll
@@ -853,8 +854,8 @@ __global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs a, const u
 // Instantiated by name: the host pass of this compiler otherwise leaves out the
 // launch stubs of some kernel templates that are only reached through pointers.
 #define MOE_TILES(F, G)                                                              \
-  template __global__ void linear_kernel<F, G, 64, 64, 2, 2, 128, 4, 4>(LinearArgs);         \
-  template __global__ void linear_kernel<F, G, 128, 128, F ? 4 : 2, 2, 128, 2, 3>(LinearArgs); \
+  template __global__ void linear_kernel<F, G, 64, 64, 2, 2, 4, 4>(LinearArgs);         \
+  template __global__ void linear_kernel<F, G, 128, 128, F ? 4 : 2, 2, 2, 3>(LinearArgs); \
   template __global__ void linear_few_kernel<F, G, 1, 16>(LinearArgs);               \
   template __global__ void linear_few_kernel<F, G, 8, 2>(LinearArgs);
 MOE_TILES(false, false)
@@ -862,9 +863,9 @@ MOE_TILES(false, true)
 MOE_TILES(true, false)
 MOE_TILES(true, true)
 #undef MOE_TILES
-template __global__ void linear_kernel<false, false, 256, 256, 2, 4, 128, 2, 3>(LinearArgs);
-template __global__ void linear_kernel<false, true, 256, 256, 2, 4, 128, 2, 3>(LinearArgs);
-template __global__ void linear_kernel<true, true, 64, 256, 2, 4, 128, 2, 2>(LinearArgs);
+template __global__ void linear_kernel<false, false, 256, 256, 2, 4, 2, 3>(LinearArgs);
+template __global__ void linear_kernel<false, true, 256, 256, 2, 4, 2, 3>(LinearArgs);
+template __global__ void linear_kernel<true, true, 64, 256, 2, 4, 2, 2>(LinearArgs);
 template __global__ void linear_backward_x_kernel<128, 128, 2, 2, 3>(LinearArgs);
 template __global__ void linear_backward_x_kernel<256, 256, 2, 4, 3>(LinearArgs);
 template __global__ void linear_backward_w_kernel<false, 128, 128, 2, 2, 32, 2, 4>(LinearArgs);
@@ -879,12 +880,12 @@ hipError_t launch(K kern, int64_t items, int threads, int lds, const LinearArgs&
   return hipGetLastError();
 }
 
-template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int DB, int QS, int PS>
+template <bool FP8, bool GATED, int BQ, int BP, int WQ, int WP, int QS, int PS>
 hipError_t run_forward(const LinearArgs& a, hipStream_t s) {
-  using T = Forward<FP8, GATED, BQ, BP, WQ, WP, DB, QS, PS>;
+  using T = Forward<FP8, GATED, BQ, BP, WQ, WP, QS, PS>;
   static std::atomic<size_t> allowed[kMaxCachedDevices];
   const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, BQ) * ((a.N + T::kCols - 1) / T::kCols);
-  void (*const kern)(LinearArgs) = &linear_kernel<FP8, GATED, BQ, BP, WQ, WP, DB, QS, PS>;
+  void (*const kern)(LinearArgs) = &linear_kernel<FP8, GATED, BQ, BP, WQ, WP, QS, PS>;
   return launch(kern, items, T::kThreads, T::kLds, a, s, allowed);
 }
 
@@ -922,14 +923,14 @@ hipError_t forward_by_shape(const LinearArgs& a, hipStream_t s) {
     // a tile with 128 columns of SwiGLU takes 256 weight rows; 8-bit operands: 32 x 64
     // per wave, which leaves room for 4 waves per SIMD (291 us at 32768 rows; 64 x 64
     // with 2: 322)
-    if constexpr (FP8 && GATED) return run_forward<FP8, GATED, 64, 256, 2, 4, 128, 2, 2>(a, s);
-    if constexpr (!FP8 && GATED) return run_forward<FP8, GATED, 256, 256, 2, 4, 128, 2, 3>(a, s);
+    if constexpr (FP8 && GATED) return run_forward<FP8, GATED, 64, 256, 2, 4, 2, 2>(a, s);
+    if constexpr (!FP8 && GATED) return run_forward<FP8, GATED, 256, 256, 2, 4, 2, 3>(a, s);
   }
   // few tiles: smaller ones, and more stages ahead of the one workgroup a compute unit has
-  if (!codes && tiles(a, a.parts * (int64_t)a.N, 128) < 256) return run_forward<FP8, GATED, 64, 64, 2, 2, 128, 4, 4>(a, s);
+  if (!codes && tiles(a, a.parts * (int64_t)a.N, 128) < 256) return run_forward<FP8, GATED, 64, 64, 2, 2, 4, 4>(a, s);
   if constexpr (!FP8)
-    if (wide_tiles(a, a.parts * (int64_t)a.N)) return run_forward<FP8, GATED, 256, 256, 2, 4, 128, 2, 3>(a, s);
-  return run_forward<FP8, GATED, 128, 128, FP8 ? 4 : 2, 2, 128, 2, 3>(a, s);
+    if (wide_tiles(a, a.parts * (int64_t)a.N)) return run_forward<FP8, GATED, 256, 256, 2, 4, 2, 3>(a, s);
+  return run_forward<FP8, GATED, 128, 128, FP8 ? 4 : 2, 2, 2, 3>(a, s);
 }
 }  // namespace
 

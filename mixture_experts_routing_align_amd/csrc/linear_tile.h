@@ -7,7 +7,7 @@
 // P columns as its A operand and 16 Q rows as its B operand, so lane l ends up
 // with row l % 16 and the 4 consecutive columns 4 (l / 16) ... + 3 of the tile.
 // An operand tile sits in LDS in one of two orders:
-//  - by rows ("R"): one line per operand row, DB bytes of depth each; a lane's 8
+//  - by rows ("R"): one line per operand row, 128 bytes of depth each; a lane's 8
 //    consecutive depth elements are one 16-byte piece.
 //  - by depth ("D"): one line per depth step, the operand's rows along it (the
 //    memory order of a matrix whose rows are the depth); ds_read_b64_tr_b16
@@ -138,24 +138,24 @@ inline int64_t row_tiles_bound(int64_t rows, int E, bool dense, int bq) {
 
 // ---------------------------------------------------------- staging, "R" --
 
-// A tile of R operand rows by DB bytes of depth, staged by WAVES waves: each
-// direct load of a wave fills 1 KB = 1024 / DB lines.
-template <int R, int DB, int WAVES>
+// Bytes of depth a stage holds of each operand row: 64 bf16 or 128 8-bit elements (one
+// scale block), and one whole cache line.  (64-byte lines ask L2 twice as often and
+// measured slower, 256-byte lines leave too few stages.)
+constexpr int kDB = 128;
+
+// A tile of R operand rows by kDB bytes of depth, staged by WAVES waves: each direct
+// load of a wave fills 1 KB = 8 lines.
+template <int R, int WAVES>
 struct RowTile {
-  static constexpr int kBytes = R * DB;
-  static constexpr int kLines = 1024 / DB;         // lines one load of a wave fills
+  static constexpr int kBytes = R * kDB;
+  static constexpr int kLines = 1024 / kDB;  // lines one load of a wave fills
   static constexpr int kLoads = kBytes / 1024 / WAVES;
-  static constexpr int kPieces = DB / 16;
+  static constexpr int kPieces = kDB / 16;
   static_assert(kBytes % (1024 * WAVES) == 0, "whole loads per wave");
-  static_assert(DB == 64 || DB == 128, "line lengths the swizzle is made for");
-  // Piece g of line r sits at g ^ swz(r).  256 bytes of LDS (all banks) hold 256 /
-  // DB lines; a 16-byte read is served 16 lanes at a time, lanes 0-3 and 12-15 of
-  // one quad together with lanes 4-11 of the next, and both forms put those on 16
-  // different pieces (measured: no bank conflicts; r / 4 for the 64-byte lines
-  // conflicted on half of the cycles).
-  __device__ static __forceinline__ int swz(int r) {
-    return DB == 64 ? -(r / 4) & 3 : (r / 2) & 7;
-  }
+  // Piece g of line r sits at g ^ swz(r): two lines make 256 bytes of LDS (all banks),
+  // and the 16 lines that the lanes of a quad read at one piece land on 16 different
+  // pieces of them (measured: no bank conflicts).
+  __device__ static __forceinline__ int swz(int r) { return (r / 2) & (kPieces - 1); }
 
   uint32_t off[kLoads];  // this lane's byte offset of each of its loads at depth 0, or kNoFetch
   int piece;             // and the depth byte its piece starts at
@@ -171,9 +171,9 @@ struct RowTile {
       off[i] = o == kNoFetch ? kNoFetch : o + g * 16;
       if (i == 0) piece = g * 16;
     }
-    // a line's swizzle repeats every kPieces * 256 / DB lines, so all of a lane's
-    // loads take the same piece where the loads are that far apart
-    static_assert(kLoads == 1 || (WAVES * kLines) % (kPieces * (256 / DB)) == 0, "one piece index per lane");
+    // a line's swizzle repeats every 16 lines, so all of a lane's loads take the same
+    // piece where the loads are that far apart
+    static_assert(kLoads == 1 || (WAVES * kLines) % (2 * kPieces) == 0, "one piece index per lane");
   }
   // Fill `lds` from depth byte `d` on; pieces at or past `left` bytes from there are zero.
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* lds, int wave, uint32_t d, int left) const {
@@ -194,7 +194,7 @@ struct RowTile {
   }
   // Piece g of line r.
   __device__ static __forceinline__ const char* at(const char* lds, int r, int g) {
-    return lds + r * DB + ((g ^ swz(r)) * 16);
+    return lds + r * kDB + ((g ^ swz(r)) * 16);
   }
   // 8 consecutive depth elements of step kk (32 deep) for operand row r0 + l % 16.
   __device__ static __forceinline__ bf16x8 frag(const char* lds, int r0, int kk, int lane) {
