@@ -11,7 +11,7 @@
 // token; else a workgroup of 4 waves, whose loads of a long row run side by side.
 // Measured at 2048 columns and top-8: 8-bit rows of 16384 tokens laid out in 50 us
 // (5.7 TB/s of what has to move), rows of 8192 tokens back in 53 us (5.7 TB/s), the
-// gradient in 124 us (4.6 TB/s).
+// gradient in 120 us (4.7 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
