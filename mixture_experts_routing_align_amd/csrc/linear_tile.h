@@ -93,16 +93,19 @@ __device__ __forceinline__ Item find_item(const LinearArgs& a, int b, int bq, in
   }
   const int lane = threadIdx.x & 63;
   const int J = (a.E + 63) >> 6;
+  // No sum passes what runs that do not overlap can make (row_tiles_bound), so tables
+  // that claim more cannot wrap the products below; their items past it are left out.
+  const int most = a.rows / bq + min(a.E, a.rows);
   int mine = 0;
   for (int j = 0; j < J; ++j) {
     const int e = lane * J + j;
-    if (e < a.E) mine += (run_length(a.offsets[e], a.counts[e], a.rows) + bq - 1) / bq;
+    if (e < a.E) mine = min(most, mine + (run_length(a.offsets[e], a.counts[e], a.rows) + bq - 1) / bq);
   }
   int incl = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int v = __shfl_up(incl, d);
-    if (lane >= d) incl += v;
+    if (lane >= d) incl = min(most, incl + v);
   }
   const int total = __builtin_amdgcn_readlane(incl, 63) * cp, chunk = (total + 7) / 8;
   const int i = (b & 7) * chunk + (b >> 3);

@@ -307,6 +307,37 @@ def test_runs_past_the_matrix_are_cut(moe):
     assert not bool(dw[2:].any()) and not bool(db[2:].any())
 
 
+@pytest.mark.parametrize("rows,N", [(700, 8), (5000, 136), (20000, 64)])
+def test_runs_that_overlap_stay_in_bounds(moe, rows, N):
+    """Every expert claims every row: far more tiles than the rows can make.  The
+    tiles past that are left out and nothing behind the matrix is written; all
+    experts hold the same weights, so whichever of them takes a row gives its value."""
+    E, K = 1024, 16
+    g = gen(6)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    counts = torch.full((E,), rows + 5, dtype=torch.int32, device="cuda")
+    x, dz = randn(g, rows, K), randn(g, rows, N)
+    w = randn(g, 1, N, K).expand(E, N, K).contiguous()
+    pre = randn(g, rows, N)
+    guard = 300
+    whole = [untouched_buffer(rows + guard, c, dtype=torch.bfloat16) for c in (N, K, N)]
+    y, dx, da = (t[:rows] for t in whole)
+    moe.moe_grouped_linear(x, w, offsets, counts, out=y)
+    moe.moe_grouped_linear_backward_x(dz, w, offsets, counts, dx=dx)
+    moe.moe_grouped_act_backward(dz, pre, "silu", offsets, counts, dz=da)
+    torch.cuda.synchronize()
+    kept = torch.arange(rows + guard, device="cuda") < rows
+    for t in whole:
+        assert_untouched(t, kept)
+    wd, zd, xd = w[0].double(), dz.double(), x.double()
+    for got, ref, mag, depth in ((y, xd @ wd.T, xd.abs() @ wd.abs().T, K), (dx, zd @ wd, zd.abs() @ wd.abs(), N)):
+        assert_within(got, ref, BF * ref.abs() + depth * SUM * mag)
+    p = pre.double()
+    sg = torch.sigmoid(p)
+    ref = zd * sg * (1 + p * (1 - sg))
+    assert_within(da, ref, BF * ref.abs() + ACT * zd.abs() * (1 + p.abs()))
+
+
 def test_in_place_residual_and_repeat(moe):
     """y over the residual's buffer, and the same bits on every call."""
     g = gen(9)
