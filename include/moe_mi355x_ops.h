@@ -97,7 +97,9 @@ int moe_add_rms_norm_backward(const void* dy_bf16, const void* z, moe_dtype zdt,
  * [0, rows).  x is [M, H] (bf16 or e4m3fn codes, `dt`) and out [rows, H] of the
  * same type; with e4m3fn rows x_scale [M, H/128] goes to out_scale [rows,
  * H/128] alike (H a multiple of 128).  Rows of `out` no slot maps to are not
- * written.  Its gradient is moe_unpermute without weights.
+ * written.  Positions in [0, rows) differ from slot to slot here and in
+ * moe_unpermute_backward, as moe_align makes them: a row that two slots map to
+ * gets the values of either.  Its gradient is moe_unpermute without weights.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_LIMIT (M*top_k or rows >= 2^31),
  * MOE_ERR_HIP. */
 int moe_permute(const void* x, moe_dtype dt, const float* x_scale, const int32_t* token_to_perm, int64_t M,

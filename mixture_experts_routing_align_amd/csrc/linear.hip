@@ -178,7 +178,7 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
   static_assert(kDB == row::kScaleBlock, "a stage of 8-bit depth is one scale block");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wq = wave / WP, wp = wave % WP;
-  const Item it = find_item(a, blockIdx.x, BQ, (a.N + kCols - 1) / kCols);
+  const Item it = find_item(a, row::block_index(), BQ, (a.N + kCols - 1) / kCols);
   if (it.e < 0) return;
   const int ld = FP8 ? a.K : a.K * 2;
   const int q0 = it.tq * BQ, p0 = it.tp * kCols;
@@ -452,7 +452,7 @@ __global__ __launch_bounds__(WC* WK * 64) void linear_few_kernel(LinearArgs a) {
   __shared__ uint32_t red[WC][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wc = wave % WC, wk = wave / WC, quad = lane >> 4;
-  const Item it = find_item(a, blockIdx.x, 16, (a.N + kCols - 1) / kCols);
+  const Item it = find_item(a, row::block_index(), 16, (a.N + kCols - 1) / kCols);
   if (it.e < 0) return;
   const int live = min(16, it.count - it.tq * 16);
   const int64_t first = (int64_t)it.row0 + it.tq * 16;
@@ -580,7 +580,7 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_backward_x_kernel(Linea
   using PTile = DepthTile<BP, kD, kWaves>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wq = wave / WP, wp = wave % WP;
-  const Item it = find_item(a, blockIdx.x, BQ, (a.K + BP - 1) / BP);
+  const Item it = find_item(a, row::block_index(), BQ, (a.K + BP - 1) / BP);
   if (it.e < 0) return;
   const int q0 = it.tq * BQ, p0 = it.tp * BP;
   const int live = min(BQ, it.count - q0);
@@ -684,8 +684,9 @@ __global__ __launch_bounds__(WQ* WP * 64, OCC) void linear_backward_w_kernel(Lin
   // experts dealt to XCDs in 8 equal runs of workgroups, as find_item does
   const int tn = (a.N + BQ - 1) / BQ, tk = (a.K + BP - 1) / BP;
   const int total = a.E * a.parts * tn * tk * a.splits, chunk = (total + 7) / 8;
-  int i = (blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= chunk || i >= total) return;
+  const int b = (int)row::block_index();
+  int i = (b & 7) * chunk + (b >> 3);
+  if ((b >> 3) >= chunk || i >= total) return;
   const int split = i % a.splits;
   i /= a.splits;
   const int tp = i % tk;
@@ -827,7 +828,7 @@ constexpr int kActRows = 16;  // rows a workgroup takes
 
 __global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs a, const uint16_t* __restrict__ dy,
                                                            const uint16_t* pre, uint16_t* dz) {
-  const Item it = find_item(a, blockIdx.x, kActRows, 1);
+  const Item it = find_item(a, row::block_index(), kActRows, 1);
   if (it.e < 0) return;
   const int per = a.N / 8, rows = min(kActRows, it.count - it.tq * kActRows);
   const int64_t first = (int64_t)it.row0 + it.tq * kActRows;
@@ -894,7 +895,7 @@ hipError_t launch(K kern, int64_t items, int threads, int lds, const LinearArgs&
                   std::atomic<size_t> (&allowed)[kMaxCachedDevices]) {
   const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kern), lds, allowed);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)((items + 7) / 8 * 8)), dim3(threads), lds, s, a);
+  hipLaunchKernelGGL(kern, row::grid_of((items + 7) / 8 * 8), dim3(threads), lds, s, a);
   return hipGetLastError();
 }
 
@@ -910,7 +911,7 @@ hipError_t run_forward(const LinearArgs& a, hipStream_t s) {
 template <bool FP8, bool GATED, int WC, int WK>
 hipError_t run_few(const LinearArgs& a, hipStream_t s) {
   const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, 16) * ((a.N + 16 * WC - 1) / (16 * WC));
-  hipLaunchKernelGGL((linear_few_kernel<FP8, GATED, WC, WK>), dim3((unsigned)((items + 7) / 8 * 8)), dim3(WC * WK * 64), 0, s, a);
+  hipLaunchKernelGGL((linear_few_kernel<FP8, GATED, WC, WK>), row::grid_of((items + 7) / 8 * 8), dim3(WC * WK * 64), 0, s, a);
   return hipGetLastError();
 }
 
@@ -998,7 +999,7 @@ hipError_t launch_linear_backward_w(const LinearArgs& a, hipStream_t s) {
 
 hipError_t launch_act_backward(const LinearArgs& a, const uint16_t* dy, const uint16_t* pre, uint16_t* dz, hipStream_t s) {
   const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, kActRows);
-  hipLaunchKernelGGL(act_backward_kernel, dim3((unsigned)((items + 7) / 8 * 8)), dim3(256), 0, s, a, dy, pre, dz);
+  hipLaunchKernelGGL(act_backward_kernel, row::grid_of((items + 7) / 8 * 8), dim3(256), 0, s, a, dy, pre, dz);
   return hipGetLastError();
 }
 

@@ -67,7 +67,8 @@ template <int TPR, int NV, int THREADS, typename RT, bool HAS_R, bool FP8>
 __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
   __shared__ float red[THREADS / 64];
   const int sub = threadIdx.x / TPR, j = threadIdx.x % TPR;
-  const int64_t m = (int64_t)blockIdx.x * (THREADS / TPR) + sub;
+  const int64_t m = row::block_index() * (THREADS / TPR) + sub;
+  if (m - sub >= a.M) return;  // a whole workgroup past the last row
   const bool live = m < a.M;
   const int64_t mm = live ? m : a.M - 1;  // a row past the last repeats it and stores nothing
   const int H = a.H;
@@ -275,11 +276,11 @@ __global__ __launch_bounds__(256) void zero_kernel(float* p, int n) {
 
 template <int TPR, int NV, int THREADS, typename RT, bool HAS_R>
 hipError_t run_norm(const NormArgs& a, hipStream_t s) {
-  const unsigned blocks = (unsigned)((a.M + THREADS / TPR - 1) / (THREADS / TPR));
+  const dim3 grid = row::grid_of((a.M + THREADS / TPR - 1) / (THREADS / TPR));
   if (a.scale != nullptr)
-    hipLaunchKernelGGL((norm_kernel<TPR, NV, THREADS, RT, HAS_R, true>), dim3(blocks), dim3(THREADS), 0, s, a);
+    hipLaunchKernelGGL((norm_kernel<TPR, NV, THREADS, RT, HAS_R, true>), grid, dim3(THREADS), 0, s, a);
   else
-    hipLaunchKernelGGL((norm_kernel<TPR, NV, THREADS, RT, HAS_R, false>), dim3(blocks), dim3(THREADS), 0, s, a);
+    hipLaunchKernelGGL((norm_kernel<TPR, NV, THREADS, RT, HAS_R, false>), grid, dim3(THREADS), 0, s, a);
   return hipGetLastError();
 }
 

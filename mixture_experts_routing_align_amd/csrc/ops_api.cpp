@@ -74,9 +74,10 @@ int check_product(const char* fn, int64_t rows, int32_t E, int32_t N, int32_t K,
     return fail_status(MOE_ERR_LIMIT, "%s: one expert's weights, %d x %d, reach 2^31 bytes", fn, N, K);
   if ((int64_t)std::max(K, N * (int64_t)parts > INT32_MAX ? INT32_MAX : N * parts) * item * 256 >= kInt32Limit)
     return fail_status(MOE_ERR_LIMIT, "%s: 256 rows of %d or %d x %d elements reach 2^31 bytes", fn, K, parts, N);
-  // the smallest tiles there are, 16 rows by 16 columns, counted in 31 bits
+  // the smallest tiles there are, 16 rows by 16 columns, counted in 31 bits, as are the
+  // workgroups up to a whole second grid dimension (at most 2^21 more)
   const int64_t tiles = (rows / 16 + std::min<int64_t>(E, rows)) * ((std::max(N, K) + 15) / 16);
-  if (tiles >= kInt32Limit) return fail_status(MOE_ERR_LIMIT, "%s: %lld tiles reach 2^31", fn, (long long)tiles);
+  if (tiles >= kInt32Limit - ((int64_t)1 << 22)) return fail_status(MOE_ERR_LIMIT, "%s: %lld tiles reach 2^31", fn, (long long)tiles);
   return MOE_OK;
 }
 

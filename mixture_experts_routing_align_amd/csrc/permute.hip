@@ -72,7 +72,7 @@ __device__ __forceinline__ int position(const int32_t* perm, int64_t i, int64_t 
 // TPT threads a token (64 or 256).
 template <int TPT, bool PAST_CACHE>
 __global__ __launch_bounds__(kThreads) void permute_kernel(PermuteArgs a) {
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;
+  const int64_t t = row::block_index() * (kThreads / TPT) + threadIdx.x / TPT;
   if (t >= a.M) return;
   const int j = threadIdx.x % TPT;
   const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.row_bytes;
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kThreads) void permute_kernel(PermuteArgs a) {
 
 template <int TPT, bool WEIGHTED>
 __global__ __launch_bounds__(kThreads) void unpermute_kernel(UnpermuteArgs a) {
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;
+  const int64_t t = row::block_index() * (kThreads / TPT) + threadIdx.x / TPT;
   if (t >= a.M) return;
   const int j = threadIdx.x % TPT;
   const int H = a.H;
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(UnpermuteArgs a) {
 template <int TPT>
 __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(UnpermuteBackwardArgs a) {
   __shared__ float red[kBatch][kThreads / 64];
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;
+  const int64_t t = row::block_index() * (kThreads / TPT) + threadIdx.x / TPT;
   if (t >= a.M) return;  // whole waves, and with TPT == 256 no workgroup has one
   const int j = threadIdx.x % TPT, lane = threadIdx.x & 63;
   const int H = a.H;
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(UnpermuteB
 // with a wave, the gradient 124 and 140; 16384 x 1024, top-4: 30 and 27, 85 and 55).
 bool wave_per_token(int64_t M, int H) { return M >= kWaveTokens && H <= 1024; }
 
-unsigned blocks_for(int64_t M, int per) { return (unsigned)((M + per - 1) / per); }
+dim3 grid_for(int64_t M, int per) { return row::grid_of((M + per - 1) / per); }
 
 }  // namespace
 
@@ -202,17 +202,17 @@ hipError_t launch_permute(const PermuteArgs& a, hipStream_t s) {
   // rows: 50 against 64 us).
   const bool past = a.rows * a.row_bytes > kCacheBytes;
   if (a.M < kWaveTokens)
-    hipLaunchKernelGGL((permute_kernel<256, false>), dim3(blocks_for(a.M, 1)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((permute_kernel<256, false>), grid_for(a.M, 1), dim3(kThreads), 0, s, a);
   else if (past)
-    hipLaunchKernelGGL((permute_kernel<64, true>), dim3(blocks_for(a.M, 4)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((permute_kernel<64, true>), grid_for(a.M, 4), dim3(kThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((permute_kernel<64, false>), dim3(blocks_for(a.M, 4)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((permute_kernel<64, false>), grid_for(a.M, 4), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_unpermute(const UnpermuteArgs& a, hipStream_t s) {
   const bool wave = wave_per_token(a.M, a.H);
-  const dim3 grid(blocks_for(a.M, wave ? 4 : 1)), block(kThreads);
+  const dim3 grid = grid_for(a.M, wave ? 4 : 1), block(kThreads);
   if (a.w != nullptr) {
     if (wave)
       hipLaunchKernelGGL((unpermute_kernel<64, true>), grid, block, 0, s, a);
@@ -229,9 +229,9 @@ hipError_t launch_unpermute(const UnpermuteArgs& a, hipStream_t s) {
 
 hipError_t launch_unpermute_backward(const UnpermuteBackwardArgs& a, hipStream_t s) {
   if (wave_per_token(a.M, a.H))
-    hipLaunchKernelGGL((unpermute_backward_kernel<64>), dim3(blocks_for(a.M, 4)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((unpermute_backward_kernel<64>), grid_for(a.M, 4), dim3(kThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((unpermute_backward_kernel<256>), dim3(blocks_for(a.M, 1)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((unpermute_backward_kernel<256>), grid_for(a.M, 1), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

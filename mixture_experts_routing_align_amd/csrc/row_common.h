@@ -15,6 +15,15 @@ constexpr int kScaleBlock = 128;             // columns that share one scale of 
 constexpr float kE4m3Max = 448.0f;           // largest e4m3fn value
 constexpr float kMinScale = 0x1p-126f;       // smallest normal float: a scale never underflows
 
+// A dispatch holds fewer than 2^32 threads in a dimension: past 2^21 workgroups (of up
+// to 1024 threads) they go on in a second one.  The last of those may lie past the end.
+constexpr int kGridShift = 21;
+inline dim3 grid_of(int64_t blocks) {
+  const int64_t most = (int64_t)1 << kGridShift;
+  return blocks <= most ? dim3((unsigned)blocks) : dim3((unsigned)most, (unsigned)((blocks + most - 1) >> kGridShift));
+}
+__device__ __forceinline__ int64_t block_index() { return ((int64_t)blockIdx.y << kGridShift) + blockIdx.x; }
+
 // Vectors the compiler may only assume element-aligned: gfx950 serves them with
 // full-width loads and stores at any element alignment, so rows of odd length
 // need no other path; a 16-byte aligned address costs nothing extra.
