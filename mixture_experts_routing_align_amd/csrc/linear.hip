@@ -10,8 +10,8 @@
 //
 // Measured on 128 experts with 32768 rows unevenly routed (17 to 1238 an expert),
 // 2 x 768 weight rows of 2048 columns, on random data:
-//   gate+up, SwiGLU, pre-activations kept    316 us  650 TFLOP/s, 3.5 TB/s of its bytes
-//   the same with 8-bit operands and result  303 us  680 TFLOP/s
+//   gate+up, SwiGLU, pre-activations kept    318 us  650 TFLOP/s, 3.4 TB/s of its bytes
+//   the same with 8-bit operands and result  302 us  680 TFLOP/s
 //   rows' gradient                           377 us  550 TFLOP/s
 //   weights' gradient                        351 us  590 TFLOP/s (805 MB written)
 // and 1.17 PFLOP/s for 32768 dense rows of the first; a square library product of 8192
