@@ -873,7 +873,7 @@ __global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs a, const u
 // Instantiated by name: the host pass of this compiler otherwise leaves out the
 // launch stubs of some kernel templates that are only reached through pointers.
 #define MOE_TILES(F, G)                                                              \
-  template __global__ void linear_kernel<F, G, 64, 64, 2, 2, 4, 4>(LinearArgs);         \
+  template __global__ void linear_kernel<F, G, F ? 32 : 64, 64, 2, 2, 3, 3>(LinearArgs);  \
   template __global__ void linear_kernel<F, G, 128, 128, F ? 4 : 2, 2, 2, 3>(LinearArgs); \
   template __global__ void linear_few_kernel<F, G, 1, 16>(LinearArgs);               \
   template __global__ void linear_few_kernel<F, G, 8, 2>(LinearArgs);
@@ -882,6 +882,7 @@ MOE_TILES(false, true)
 MOE_TILES(true, false)
 MOE_TILES(true, true)
 #undef MOE_TILES
+template __global__ void linear_kernel<false, false, 32, 64, 2, 2, 4, 4>(LinearArgs);
 template __global__ void linear_kernel<false, false, 256, 256, 2, 4, 2, 3>(LinearArgs);
 template __global__ void linear_kernel<false, true, 256, 256, 2, 4, 2, 3>(LinearArgs);
 template __global__ void linear_kernel<true, true, 64, 256, 2, 4, 2, 2>(LinearArgs);
@@ -945,8 +946,19 @@ hipError_t forward_by_shape(const LinearArgs& a, hipStream_t s) {
     if constexpr (FP8 && GATED) return run_forward<FP8, GATED, 64, 256, 2, 4, 2, 2>(a, s);
     if constexpr (!FP8 && GATED) return run_forward<FP8, GATED, 256, 256, 2, 4, 2, 3>(a, s);
   }
-  // few tiles: smaller ones, and more stages ahead of the one workgroup a compute unit has
-  if (!codes && tiles(a, a.parts * (int64_t)a.N, 128) < 256) return run_forward<FP8, GATED, 64, 64, 2, 2, 4, 4>(a, s);
+  // Few tiles: smaller ones, of which more than one shares a compute unit (six stages of
+  // 64 x 64, which leave one: 19.5 against 12.5 us at 1554 rows of 12 experts, 520 x 1000).
+  // 32 x 64 for 8-bit operands, whose widening it spreads (the same, 512 x 1024: 9.0
+  // against 13.0 us with 64 x 64; 256 x 2048 x 2048: 9.6 and 14.6; equal, 18.5, at 1024
+  // rows), and for bf16 while 64 x 64 tiles would not fill the GPU (256 x 2048 x 2048:
+  // 9.1 against 11.7; 1024 rows: 21.4 and 15.9), except under SwiGLU, where it loses
+  // (512 rows of 8 experts, 768 x 2048: 12.7 against 11.8).
+  if (!codes && tiles(a, a.parts * (int64_t)a.N, 128) < 256) {
+    if constexpr (FP8) return run_forward<FP8, GATED, 32, 64, 2, 2, 3, 3>(a, s);
+    if constexpr (!FP8 && !GATED)
+      if (tiles(a, a.N, 64) < 256) return run_forward<FP8, GATED, 32, 64, 2, 2, 4, 4>(a, s);
+    if constexpr (!FP8) return run_forward<FP8, GATED, 64, 64, 2, 2, 3, 3>(a, s);
+  }
   if constexpr (!FP8)
     if (wide_tiles(a, a.parts * (int64_t)a.N)) return run_forward<FP8, GATED, 256, 256, 2, 4, 2, 3>(a, s);
   return run_forward<FP8, GATED, 128, 128, FP8 ? 4 : 2, 2, 2, 3>(a, s);
