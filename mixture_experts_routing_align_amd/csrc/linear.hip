@@ -886,6 +886,8 @@ template __global__ void linear_kernel<false, false, 32, 64, 2, 2, 4, 4>(LinearA
 template __global__ void linear_kernel<false, false, 256, 256, 2, 4, 2, 3>(LinearArgs);
 template __global__ void linear_kernel<false, true, 256, 256, 2, 4, 2, 3>(LinearArgs);
 template __global__ void linear_kernel<true, true, 64, 256, 2, 4, 2, 2>(LinearArgs);
+template __global__ void linear_backward_x_kernel<32, 128, 2, 2, 3>(LinearArgs);
+template __global__ void linear_backward_x_kernel<64, 128, 2, 2, 3>(LinearArgs);
 template __global__ void linear_backward_x_kernel<128, 128, 2, 2, 3>(LinearArgs);
 template __global__ void linear_backward_x_kernel<256, 256, 2, 4, 3>(LinearArgs);
 template __global__ void linear_backward_w_kernel<false, 128, 128, 2, 2, 32, 2, 4>(LinearArgs);
@@ -970,16 +972,22 @@ hipError_t launch_linear(const LinearArgs& a, bool fp8, hipStream_t s) {
   return a.parts == 2 ? forward_by_shape<false, true>(a, s) : forward_by_shape<false, false>(a, s);
 }
 
-template <int B, int WQ, int WP>
+template <int BQ, int BP, int WQ, int WP>
 hipError_t run_backward_x(const LinearArgs& a, hipStream_t s) {
   static std::atomic<size_t> allowed[kMaxCachedDevices];
   constexpr int kPS = 3;
-  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, B) * ((a.K + B - 1) / B);
-  return launch(&linear_backward_x_kernel<B, B, WQ, WP, kPS>, items, WQ * WP * 64, (2 + kPS) * B * 128, a, s, allowed);
+  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, BQ) * ((a.K + BP - 1) / BP);
+  return launch(&linear_backward_x_kernel<BQ, BP, WQ, WP, kPS>, items, WQ * WP * 64, (2 * BQ + kPS * BP) * 128, a, s, allowed);
 }
 
 hipError_t launch_linear_backward_x(const LinearArgs& a, hipStream_t s) {
-  return wide_tiles(a, a.K) ? run_backward_x<256, 2, 4>(a, s) : run_backward_x<128, 2, 2>(a, s);
+  if (wide_tiles(a, a.K)) return run_backward_x<256, 256, 2, 4>(a, s);
+  // Few tiles: fewer rows each, so that more than one shares a compute unit (1024 x 2048 x
+  // 2048: 24 us with 64 x 128, 27 with 32 x 128, 36 with 128 x 128; 8 experts of 64 rows,
+  // 2 x 768 x 2048: 23, 21 and 23).
+  if (tiles(a, a.K, 128) < 256)
+    return mean_rows(a) <= 64 ? run_backward_x<32, 128, 2, 2>(a, s) : run_backward_x<64, 128, 2, 2>(a, s);
+  return run_backward_x<128, 128, 2, 2>(a, s);
 }
 
 int backward_w_splits(int64_t rows, int E, int N, int K, int parts) {

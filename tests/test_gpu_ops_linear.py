@@ -179,6 +179,30 @@ def test_forward_tiles(moe, rows, N, K, act, bias, res, save):
     test_forward(moe, rows, act, bias, res, save, N, K)
 
 
+SKEW = (2100, 16, 4, 16, "skew", 0.0)  # runs of every length, partly filled tiles
+# (rows, N, K) by the tiles they take without SwiGLU: 64 x 64, 128 x 128, 256 x 256
+FORMS = [(1100, 1040, 200), (2100, 2056, 136), (SKEW, 1032, 136), (4100, 4104, 72), (SKEW, 2056, 200)]
+
+
+@pytest.mark.parametrize("rows,N,K", FORMS, ids=str)
+@pytest.mark.parametrize("act,bias,res,save", [("gelu", True, True, True), ("swiglu", True, True, True)])
+def test_forward_forms(moe, rows, N, K, act, bias, res, save):
+    test_forward(moe, rows, act, bias, res, save, N, K)
+
+
+@pytest.mark.parametrize("rows,N,K", [(1100, 1024, 256), (2100, 2048, 128), (SKEW, 1024, 384)], ids=str)
+@pytest.mark.parametrize("act,bias,res", [("gelu", True, True), ("swiglu", True, True)])
+def test_forward_8bit_forms(moe, rows, N, K, act, bias, res):
+    test_forward_8bit(moe, rows, act, bias, res, False, N, K)
+
+
+# the rows' gradient by 64 x 128, 128 x 128 and 256 x 256 tiles
+@pytest.mark.parametrize("rows,N,K", [(1100, 200, 1032), (SKEW, 136, 1032), (4100, 72, 4104), (SKEW, 200, 2056)], ids=str)
+@pytest.mark.parametrize("gated", [False, True])
+def test_backward_forms(moe, rows, N, K, gated):
+    test_backward(moe, rows, gated, N, K)
+
+
 @pytest.mark.parametrize("rows", [1, 40, 300, (70, 6, 3, 16, "skew", 0.1), (600, 4, 2, 16, "random", 0.0)], ids=str)
 @pytest.mark.parametrize("act", ["none", "swiglu"])
 @pytest.mark.parametrize("N,K", [(128, 136), (640, 520)])
