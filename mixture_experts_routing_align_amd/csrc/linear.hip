@@ -10,7 +10,7 @@
 //
 // Measured on 128 experts with 32768 rows unevenly routed (17 to 1238 an expert),
 // 2 x 768 weight rows of 2048 columns, on random data:
-//   gate+up, SwiGLU, pre-activations kept    318 us  650 TFLOP/s, 3.4 TB/s of its bytes
+//   gate+up, SwiGLU, pre-activations kept    320 us  640 TFLOP/s, 3.4 TB/s of its bytes
 //   the same with 8-bit operands and result  302 us  680 TFLOP/s
 //   rows' gradient                           377 us  550 TFLOP/s
 //   weights' gradient                        351 us  590 TFLOP/s (805 MB written)
