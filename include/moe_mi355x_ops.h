@@ -23,8 +23,9 @@
  *   - 8-bit rows are OCP e4m3fn codes [rows, C] with one float32 scale per 128
  *     columns, [rows, C/128]; a value is code * scale.  The scale of a block is
  *     its absolute maximum over 448, at least 2^-126, and 1 for a block of
- *     zeros; a block with a NaN or an infinity gets a NaN scale, so all of it
- *     reads as NaN.
+ *     zeros, and a code is the nearest (ties to even) to the float32 value over the
+ *     scale, both quotients rounded to float32; a block with a NaN or an infinity
+ *     gets a NaN scale, so all of it reads as NaN.
  *   - Sorted rows: expert e's rows are [expert_offsets[e], expert_offsets[e] +
  *     expert_counts[e]) of a [rows, C] matrix, as moe_align lays them out (the
  *     offsets padded to its block size).  Rows outside every expert's run

@@ -105,12 +105,6 @@ __device__ __forceinline__ void epilogue4(const LinearArgs& a, int e, int64_t r,
   }
 }
 
-// 4 values times the reciprocal of their block's scale as e4m3fn codes.
-__device__ __forceinline__ uint32_t codes4(const float (&y)[4], float inv) {
-  const uint32_t lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * inv, y[1] * inv, 0, false);
-  return __builtin_amdgcn_cvt_pk_fp8_f32(y[2] * inv, y[3] * inv, lo, true);
-}
-
 // Calls f with the smallest of kQ / 4, kQ / 2, 3 kQ / 4 and kQ subtiles that covers `live`.
 template <int N>
 struct Count {
@@ -424,12 +418,10 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
       const float scale = row::block_scale(mx);
       if (m < live && colw < cols && colw % row::kScaleBlock == 0)
         a.y_scale[(first + m) * (a.N / row::kScaleBlock) + (p0 + colw) / row::kScaleBlock] = scale;
-      const float inv = 1.0f / scale;
+      const row::Codes to(scale);
 #pragma unroll
-      for (int j = 0; j < kC; ++j) {
-        const float y[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        Codes::put(codes, m, colw + j * 16, codes4(y, inv));
-      }
+      for (int j = 0; j < kC; ++j)
+        Codes::put(codes, m, colw + j * 16, to.x4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]));
     }
     __syncthreads();
     Codes::flush(codes, static_cast<char*>(a.y) + first * a.N + p0, a.N, live, cols);
@@ -561,7 +553,7 @@ __global__ __launch_bounds__(WC* WK * 64) void linear_few_kernel(LinearArgs a) {
 #pragma unroll
       for (int i = 0; i < WC; ++i) mx = max(mx, red[i][m]);
       const float scale = row::block_scale(mx);
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + (first + m) * a.N + n) = codes4(y, 1.0f / scale);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + (first + m) * a.N + n) = row::Codes(scale).x4(y[0], y[1], y[2], y[3]);
       if (n % row::kScaleBlock == 0) a.y_scale[(first + m) * (a.N / row::kScaleBlock) + n / row::kScaleBlock] = scale;
     }
   }

@@ -128,8 +128,8 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
       for (int i = 0; i < 8; ++i) mx = max(mx, abs_bits(y[i]));
       const float scale = block_scale(row16_umax(mx));
       if (c < H) {
-        uint32_t lo, hi;
-        e4m3x8(y, scale, lo, hi);
+        const Codes codes(scale);
+        const uint32_t lo = codes.x4(y[0], y[1], y[2], y[3]), hi = codes.x4(y[4], y[5], y[6], y[7]);
         *reinterpret_cast<u32x2_e1*>(static_cast<uint8_t*>(a.out) + m * H + c) = u32x2_e1{lo, hi};
         if ((j & 15) == 0) a.scale[m * (H / kScaleBlock) + c / kScaleBlock] = scale;
       }
