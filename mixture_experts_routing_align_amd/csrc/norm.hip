@@ -26,17 +26,32 @@ namespace {
 
 using namespace row;
 
-// The sum of v over the TPR threads of a row; `red` holds one float per wave of
-// the workgroup, and a barrier separates two uses of it.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-  v = wave_sum(v);
+// The sum of the squares of a row that TPR threads hold; `red` holds one float per wave
+// of the workgroup, and a barrier separates two uses of it.  A wave per row adds up each
+// piece over the wave before it adds the pieces: these are the sums of a wave per piece,
+// so a row's bits do not depend on which of the two its batch takes.
+template <int TPR, int NV>
+__device__ __forceinline__ float square_sum(const float (&z)[NV][8], float* red) {
   if constexpr (TPR == 64) {
-    return v;
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float p = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p = fmaf(z[v][i], z[v][i], p);
+      s += wave_sum(p);
+    }
+    return s;
   } else {
     constexpr int W = TPR / 64;
+    float p = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p = fmaf(z[v][i], z[v][i], p);
+    p = wave_sum(p);
     const int wave = threadIdx.x >> 6, base = wave / W * W;
-    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    if ((threadIdx.x & 63) == 0) red[wave] = p;
     __syncthreads();
     float s = red[base];
 #pragma unroll
@@ -75,13 +90,8 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
   const uint16_t* x = static_cast<const uint16_t*>(a.x) + mm * a.ldx;
   const RT* r = static_cast<const RT*>(a.res) + mm * H;
   float z[NV][8];
-  float ss = 0.f;
 #pragma unroll
   for (int v = 0; v < NV; ++v) load_z<RT, HAS_R>(x, r, (v * TPR + j) * 8, H, z[v]);
-#pragma unroll
-  for (int v = 0; v < NV; ++v)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(z[v][i], z[v][i], ss);
   float w[NV][8];
 #pragma unroll
   for (int v = 0; v < NV; ++v) load8(static_cast<const uint16_t*>(a.w), (v * TPR + j) * 8, H, w[v]);
@@ -92,23 +102,20 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
       for (int v = 0; v < NV; ++v) store8(zo, (v * TPR + j) * 8, H, z[v]);
     }
   }
-  float mean = row_sum<TPR>(ss, red) / (float)H, eps = a.eps, unit = 1.f;
+  float mean = square_sum<TPR>(z, red) / (float)H, eps = a.eps, unit = 1.f;
   // Squares that leave float32's range (values past 2^63, or below 2^-50 with
   // next to no eps) are summed once more in a unit that keeps them inside it;
   // the whole row takes the same way.
   const bool large = mean > kLargeMean, small = mean < kSmallMean && eps < kSmallEps;
   if (large || small) {
     unit = large ? 0x1p-64f : 0x1p64f;
-    ss = 0.f;
+    float t[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float t = z[v][i] * unit;
-        ss = fmaf(t, t, ss);
-      }
+      for (int i = 0; i < 8; ++i) t[v][i] = z[v][i] * unit;
     if constexpr (TPR > 64) __syncthreads();  // red is read
-    mean = row_sum<TPR>(ss, red) / (float)H;
+    mean = square_sum<TPR>(t, red) / (float)H;
     eps = eps * unit * unit;
   }
   const float rstd = unit / sqrtf(mean + eps);
