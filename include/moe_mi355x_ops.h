@@ -63,8 +63,9 @@ typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_E4M3 = 2 } moe_dtype;
  * that was normalised.  y goes to `out`: bf16 (odt MOE_DT_BF16; may be x itself
  * where ldx == H) or 8-bit rows (odt MOE_DT_E4M3, out_scale [M, H/128], H a
  * multiple of 128).  rstd (NULL: not wanted) gets (mean(z^2) + eps)^(-1/2),
- * float32 [M], for the backward call.  Sums are float32.  A row's bits do not
- * depend on the other rows.  Any H from 1 to MOE_NORM_MAX_H and any element
+ * float32 [M], for the backward call (rounded where it is subnormal, an infinity
+ * where it passes float32's range; y is right there too).  Sums are float32.  A
+ * row's bits do not depend on the other rows.  Any H from 1 to MOE_NORM_MAX_H and any element
  * alignment; fastest with 16-byte aligned rows.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (M < 0, H, ldx, eps negative or not
  * finite, a type, residual_out without residual), MOE_ERR_LIMIT (H above the

@@ -102,31 +102,39 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
       for (int v = 0; v < NV; ++v) store8(zo, (v * TPR + j) * 8, H, z[v]);
     }
   }
-  float mean = square_sum<TPR>(z, red) / (float)H, eps = a.eps, unit = 1.f;
-  // Squares that leave float32's range (values past 2^63, or below 2^-50 with
-  // next to no eps) are summed once more in a unit that keeps them inside it;
-  // the whole row takes the same way.
+  float mean = square_sum<TPR>(z, red) / (float)H, eps = a.eps, unit = 1.f, pre = 1.f;
+  // Squares that leave float32's range (means past 2^100, or below 2^-100 with next to no
+  // eps) are summed once more in a unit
+  // that keeps them inside it: 2^-80 (32768 of the largest value make 2^111) or 2^96 (the
+  // smallest subnormal's square is 2^-106, and the sum stays below 2^107).  The whole row
+  // takes the same way.  y comes from z in a unit `pre` in which neither z nor rstd
+  // leaves the range: large rows in 2^-16, which makes a subnormal rstd (below 2^-126) a
+  // normal float and costs bits only of values whose y is 0; small rows in 2^96.
   const bool large = mean > kLargeMean, small = mean < kSmallMean && eps < kSmallEps;
   if (large || small) {
-    unit = large ? 0x1p-64f : 0x1p64f;
+    unit = large ? 0x1p-80f : 0x1p96f;
+    pre = large ? 0x1p-16f : unit;
     float t[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[v][i] = z[v][i] * unit;
+      for (int i = 0; i < 8; ++i) {
+        t[v][i] = z[v][i] * unit;
+        z[v][i] *= pre;
+      }
     if constexpr (TPR > 64) __syncthreads();  // red is read
     mean = square_sum<TPR>(t, red) / (float)H;
     eps = eps * unit * unit;
   }
-  const float rstd = unit / sqrtf(mean + eps);
+  const float rs = unit / pre / sqrtf(mean + eps);  // rstd for z in that unit
   if (!live) return;
-  if (a.rstd != nullptr && j == 0) a.rstd[m] = rstd;
+  if (a.rstd != nullptr && j == 0) a.rstd[m] = rs * pre;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = (v * TPR + j) * 8;
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = z[v][i] * rstd * w[v][i];
+    for (int i = 0; i < 8; ++i) y[i] = z[v][i] * rs * w[v][i];
     if constexpr (FP8) {
       // 16 neighbouring lanes hold one scale block (H is a multiple of 128, so a
       // block is wholly inside the row or wholly past it)
