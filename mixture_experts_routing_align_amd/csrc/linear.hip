@@ -688,8 +688,8 @@ __global__ __launch_bounds__(WQ* WP * 64, OCC) void linear_backward_w_kernel(Lin
   const int h = i % a.parts, e = i / a.parts;
   const int row0 = a.offsets != nullptr ? a.offsets[e] : 0;
   const int count = a.offsets != nullptr ? run_length(row0, a.counts[e], a.rows) : a.rows;
-  const int share = ((count + a.splits - 1) / a.splits + kD - 1) / kD * kD;
-  const int begin = min(count, split * share), rows = min(count, begin + share) - begin;
+  const RowRange range = split_rows(count, split, a.splits, kD);
+  const int begin = range.begin, rows = range.rows;
   const int q0 = tq * BQ, p0 = tp * BP;
   const int ldq = a.parts * a.N * 2, ldp = a.K * 2;
   const int64_t first = count > 0 ? (int64_t)row0 + begin : 0;
@@ -699,10 +699,10 @@ __global__ __launch_bounds__(WQ* WP * 64, OCC) void linear_backward_w_kernel(Lin
   PTile pt;
   qt.init(wave, lane, ldq, [&](int g) { return q0 + g * 8 < a.N ? (uint32_t)(g * 16) : kNoFetch; });
   pt.init(wave, lane, ldp, [&](int g) { return p0 + g * 8 < a.K ? (uint32_t)(g * 16) : kNoFetch; });
-  const int steps = (rows + kD - 1) / kD;
+  const int steps = ceil_div(rows, kD);
   auto issue = [&](int s, int stage) {
     char* b = smem + stage * kStage;
-    const int left = rows - s * kD;
+    const int left = rows_left(rows, s, kD);
     qt.load(resource(dz + (int64_t)s * kD * ldq), b, wave, 0, left);
     pt.load(resource(x + (int64_t)s * kD * ldp), b + QTile::kBytes, wave, 0, left);
   };
@@ -913,7 +913,7 @@ hipError_t run_few(const LinearArgs& a, hipStream_t s) {
 constexpr int kBQ = 128, kBP = 128;
 
 // Rows per expert on average; the runs themselves are known on the device only.
-int64_t mean_rows(const LinearArgs& a) { return (a.rows + a.E - 1) / a.E; }
+int64_t mean_rows(const LinearArgs& a) { return ceil_div(a.rows, a.E); }
 
 // Square tiles of `edge` that the rows and `cols` columns make.
 int64_t tiles(const LinearArgs& a, int64_t cols, int64_t edge) {

@@ -22,6 +22,7 @@
 
 #include "mma_common.h"
 #include "ops_internal.h"
+#include "row_runs.h"
 
 namespace moe {
 namespace tile {
@@ -58,12 +59,6 @@ struct Item {
   int tq, tp;  // tile indexes along the rows and along the columns
 };
 
-// The runs of one lane's experts, cut off at `rows`; a negative or far offset
-// leaves an empty run.
-__device__ __forceinline__ int run_length(int off, int cnt, int rows) {
-  return off < 0 || off >= rows ? 0 : max(0, min(cnt, rows - off));
-}
-
 // Item i of an expert with rt row tiles and cp column tiles: the 32 workgroups an XCD
 // runs at once then hold 8 row tiles by 4 column tiles, 12 operand tiles for 64 reads,
 // which its L2 serves (33 TB/s against 15 where the reads miss it).
@@ -83,7 +78,7 @@ __device__ __forceinline__ void tile_of(int i, int rt, int cp, Item& it) {
 __device__ __forceinline__ Item find_item(const LinearArgs& a, int b, int bq, int cp) {
   Item it{-1, 0, 0, 0, 0};
   if (a.offsets == nullptr) {
-    const int rt = (a.rows + bq - 1) / bq, total = rt * cp, chunk = (total + 7) / 8;
+    const int rt = ceil_div(a.rows, bq), total = rt * cp, chunk = (total + 7) / 8;
     const int i = (b & 7) * chunk + (b >> 3);
     if ((b >> 3) >= chunk || i >= total) return it;
     it.e = 0;
@@ -99,7 +94,7 @@ __device__ __forceinline__ Item find_item(const LinearArgs& a, int b, int bq, in
   int mine = 0;
   for (int j = 0; j < J; ++j) {
     const int e = lane * J + j;
-    if (e < a.E) mine = min(most, mine + (run_length(a.offsets[e], a.counts[e], a.rows) + bq - 1) / bq);
+    if (e < a.E) mine = min(most, mine + ceil_div(run_length(a.offsets[e], a.counts[e], a.rows), bq));
   }
   int incl = mine;
 #pragma unroll
@@ -117,7 +112,7 @@ __device__ __forceinline__ Item find_item(const LinearArgs& a, int b, int bq, in
   for (int j = 0; j < J; ++j) {
     const int c = lane * J + j;
     if (c >= a.E) break;
-    const int o = a.offsets[c], n = run_length(o, a.counts[c], a.rows), r = (n + bq - 1) / bq;
+    const int o = a.offsets[c], n = run_length(o, a.counts[c], a.rows), r = ceil_div(n, bq);
     e = c;
     off = o;
     cnt = n;
