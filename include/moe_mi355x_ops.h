@@ -146,7 +146,7 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_SWI
  * that holds every row, i.e. a dense projection.
  * Shapes: bf16 needs K and N multiples of 8, e4m3fn multiples of 128; 8-bit y
  * needs N a multiple of 128.  x, w, y, residual and preact 16-byte aligned.
- * y may be residual's buffer.
+ * A bf16 y may be residual's buffer; an 8-bit y that overlaps it is refused.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_LIMIT (E > MOE_MAX_EXPERTS, rows
  * >= 2^31, a matrix of one expert or 256 rows of x or y past 2^31 bytes),
  * MOE_ERR_HIP. */

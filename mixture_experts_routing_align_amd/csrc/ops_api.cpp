@@ -246,6 +246,13 @@ int moe_grouped_linear(const moe_linear_desc* d, hipStream_t stream) {
               {"residual", d->residual}, {"y", d->y}, {"preact", d->preact}};
   for (const auto& p : ptrs)
     if (int rc = check_aligned16(fn, p.name, p.p)) return rc;
+  // bf16 rows replace the residual's element by element; a row of codes would lie over
+  // another row's residual
+  const char* y0 = static_cast<const char*>(d->y);
+  const char* r0 = static_cast<const char*>(d->residual);
+  const int64_t cells = d->rows * d->N;
+  if (d->ydt == MOE_DT_E4M3 && r0 != nullptr && y0 < r0 + 2 * cells && r0 < y0 + cells)
+    return fail_status(MOE_ERR_SHAPE, "%s: 8-bit y overlaps residual", fn);
   moe::LinearArgs a{};
   a.offsets = d->expert_offsets;
   a.counts = d->expert_counts;

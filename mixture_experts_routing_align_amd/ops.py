@@ -317,9 +317,9 @@ def moe_grouped_linear(x: torch.Tensor, w, expert_offsets: Optional[torch.Tensor
     `x_scale`) or a bare bf16 tensor.  `act`: "none", "silu", "gelu" (tanh form)
     or "swiglu", silu(W x + bias) * (W_up x + up_bias) with `up`.  Returns ``(y,
     y_scale, preact)``: y bf16 [rows, N] (may be `residual` itself), or with
-    `fp8_out` (or an 8-bit `out`) 8-bit rows with their scales; preact, with
-    `save_preact` or given as a buffer, the bf16 pre-activations ([rows, 2N] for
-    swiglu) that moe_grouped_act_backward takes."""
+    `fp8_out` (or an 8-bit `out`) 8-bit rows with their scales, in buffers of their
+    own; preact, with `save_preact` or given as a buffer, the bf16 pre-activations
+    ([rows, 2N] for swiglu) that moe_grouped_act_backward takes."""
     _need(act in ACTIVATIONS, "act must be one of none, silu, gelu, swiglu")
     gated = act == "swiglu"
     dev = _device(x, "x")
