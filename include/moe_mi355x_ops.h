@@ -8,8 +8,12 @@
  *   moe_grouped_linear (gate+up, SwiGLU) -> moe_grouped_linear (down) ->
  *   moe_unpermute,
  * either in bf16 or with 8-bit rows and weights all along (the norm, the
- * permutation and the first product hand on e4m3fn rows with their scales);
- * the backward entry points run the same chain the other way.
+ * permutation and the first product hand on e4m3fn rows with their scales).
+ * The backward entry points run the same chain the other way, but for the
+ * router, which has none: moe_unpermute_backward gives the gradient of its
+ * weights, the caller takes that through the softmax over the chosen logits
+ * (dl = w (dw - sum over k of w dw)), and the dense products' gradients do the
+ * rest, whose dx is added to the experts'.
  *
  * The conventions of moe_mi355x.h hold: device memory owned by the caller,
  * nothing allocated, no synchronisation, no device data read on the host, every
