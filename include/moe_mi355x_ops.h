@@ -8,7 +8,10 @@
  *   moe_grouped_linear (gate+up, SwiGLU) -> moe_grouped_linear (down) ->
  *   moe_unpermute,
  * either in bf16 or with 8-bit rows and weights all along (the norm, the
- * permutation and the first product hand on e4m3fn rows with their scales).
+ * permutation and the first product hand on e4m3fn rows with their scales).  The
+ * router reads bf16 rows: a block in 8 bits calls the norm twice on the same x and
+ * residual, for bf16 rows and for 8-bit ones (both are roundings of the same y), and
+ * the second call may update the stream in place.
  * The backward entry points run the same chain the other way, but for the
  * router, which has none: moe_unpermute_backward gives the gradient of its
  * weights, the caller takes that through the softmax over the chosen logits
