@@ -31,8 +31,9 @@
  *     columns, [rows, C/128]; a value is code * scale.  The scale of a block is
  *     its absolute maximum over 448, at least 2^-126, and 1 for a block of
  *     zeros, and a code is the nearest (ties to even) to the float32 value over the
- *     scale, both quotients rounded to float32; a block with a NaN or an infinity
- *     gets a NaN scale, so all of it reads as NaN.
+ *     scale, both quotients rounded to float32 (where the exact quotient lies on the
+ *     border of two codes, the rounding of the float32 value decides); a block with a
+ *     NaN or an infinity gets a NaN scale, so all of it reads as NaN.
  *   - Sorted rows: expert e's rows are [expert_offsets[e], expert_offsets[e] +
  *     expert_counts[e]) of a [rows, C] matrix, as moe_align lays them out (the
  *     offsets padded to its block size).  Rows outside every expert's run
@@ -49,8 +50,8 @@
 extern "C" {
 #endif
 
-/* Version of this header (increases on any change; moe_abi_version() is that of
- * moe_mi355x.h). */
+/* Version of this header's declarations (increases when one changes;
+ * moe_abi_version() is that of moe_mi355x.h). */
 int32_t moe_ops_abi_version(void);
 
 typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_E4M3 = 2 } moe_dtype;
@@ -134,7 +135,8 @@ int moe_unpermute_backward(const void* dout_bf16, const void* y_bf16, const int3
 
 /* Activation of a product's epilogue: none, z*sigmoid(z), gelu (the tanh form:
  * z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))), and silu(z) * u with a second
- * product u (SwiGLU). */
+ * product u (SwiGLU).  A sigmoid below e^-87, where float32's normal range ends,
+ * counts as 0, in the gradients too. */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_SWIGLU = 3 } moe_act;
 
 /* One product over sorted rows, for row p of expert e:
@@ -152,7 +154,10 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_SWI
  * expert_offsets (E + 1 entries) and expert_counts (E) NULL: one expert (E == 1)
  * that holds every row, i.e. a dense projection.
  * Shapes: bf16 needs K and N multiples of 8, e4m3fn multiples of 128; 8-bit y
- * needs N a multiple of 128.  x, w, y, residual and preact 16-byte aligned.
+ * needs N a multiple of 128.  x, w, up, bias, up_bias, y, residual and preact
+ * 16-byte aligned.  The kernels' tiles are chosen by `rows` (over E, on average), in
+ * which the alignment's padding counts: fastest with its block size no larger than
+ * the experts' runs.
  * A bf16 y may be residual's buffer; an 8-bit y that overlaps it is refused.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_LIMIT (E > MOE_MAX_EXPERTS, rows
  * >= 2^31, a matrix of one expert or 256 rows of x or y past 2^31 bytes),

@@ -436,7 +436,11 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_kernel(LinearArgs a) {
 // straight into the matrix cores' registers (16 lanes x 256 contiguous bytes a
 // chunk).  All loads of a chunk are in flight at once; the WK sums meet in LDS in
 // wave order.  8-bit rows out need all 128 columns of a scale block: WC = 8.
-// Latency bounds it: 8 rows by 2048 x 2048 take 6.2 us, 8.4 MB of weights at 1.3 TB/s.
+// 8 dense rows by 2048 x 2048 take 6.2 us, 8.4 MB of weights at 1.3 TB/s: 128 workgroups
+// leave half of the compute units without one, and each walks one dependent memory trip
+// (16 waves of one chunk) and the join.  Over experts, 64 rows on 51 of 128, SwiGLU of
+// 2 x 768 x 2048: 117 us in bf16, 47 us in 8 bits with 8-bit rows out (2.7 and 3.4 TB/s of
+// the active weights).
 template <bool FP8, bool GATED, int WC, int WK>
 __global__ __launch_bounds__(WC* WK * 64) void linear_few_kernel(LinearArgs a) {
   constexpr int kParts = GATED ? 2 : 1, kCols = 16 * WC, kChunk = 128;
@@ -775,6 +779,8 @@ __global__ __launch_bounds__(WQ* WP * 64, OCC) void linear_backward_w_kernel(Lin
     return;
   }
   // float32: a lane's 16 bytes go out as they are, 64 bytes of each of 16 rows at a time
+  // (both gradients of 128 experts, 2 x 768 x 2048, 32768 rows: 1150 us, 810 with bf16
+  // results, which are half the bytes and leave as whole lines)
   float* out = (whole ? static_cast<float*>(a.dw[h]) : part + h * weight) + line0 * a.K;
 #pragma unroll
   for (int r = 0; r < kQ; ++r) {
@@ -815,7 +821,9 @@ __global__ __launch_bounds__(256) void join_splits_kernel(LinearArgs a) {
 
 // ---------------------------------------------------- activation gradient --
 
-// Element by element: dy, the pre-activations and dz pass once, so HBM bounds it.
+// Element by element: dy, the pre-activations and dz pass once.  32768 rows of 768 over 128
+// experts: 65 us for SwiGLU, 42 us for the others, 3.9 and 3.6 TB/s of those bytes, short of
+// what HBM gives the norm (6 TB/s): a workgroup searches its run before its first load.
 constexpr int kActRows = 16;  // rows a workgroup takes
 
 __global__ __launch_bounds__(256) void act_backward_kernel(LinearArgs a, const uint16_t* __restrict__ dy,
@@ -912,7 +920,11 @@ hipError_t run_few(const LinearArgs& a, hipStream_t s) {
 
 constexpr int kBQ = 128, kBP = 128;
 
-// Rows per expert on average; the runs themselves are known on the device only.
+// Rows per expert on average, of the matrix's height: the runs themselves are known on the
+// device only, so the alignment's padding counts, here and in tiles().  With a block
+// size far above the runs it weighs more than the rows do (64 rows over 128 experts, SwiGLU
+// of 2 x 768 x 2048, bf16: 117 us aligned to 16, 154 to 64, in the same form with more
+// empty workgroups; 512 rows: 253 and 164 us, in the depth-split form and in 128-wide tiles).
 int64_t mean_rows(const LinearArgs& a) { return ceil_div(a.rows, a.E); }
 
 // Square tiles of `edge` that the rows and `cols` columns make.
@@ -936,7 +948,8 @@ hipError_t forward_by_shape(const LinearArgs& a, hipStream_t s) {
   if (GATED && codes) {
     // a tile with 128 columns of SwiGLU takes 256 weight rows; 8-bit operands: 32 x 64
     // per wave, which leaves room for 4 waves per SIMD (291 us at 32768 rows; 64 x 64
-    // with 2: 322)
+    // with 2: 322).  There is no smaller tile for few rows (512 rows of 8 experts, 768 x
+    // 2048, 8-bit operands: 30 us, against 14.5 with bf16 rows out, which have one).
     if constexpr (FP8 && GATED) return run_forward<FP8, GATED, 64, 256, 2, 4, 2, 2>(a, s);
     if constexpr (!FP8 && GATED) return run_forward<FP8, GATED, 256, 256, 2, 4, 2, 3>(a, s);
   }
