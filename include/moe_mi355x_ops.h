@@ -73,8 +73,8 @@ typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_E4M3 = 2 } moe_dtype;
  * multiple of 128).  rstd (NULL: not wanted) gets (mean(z^2) + eps)^(-1/2),
  * float32 [M], for the backward call (rounded where it is subnormal, an infinity
  * where it passes float32's range; y is right there too).  Sums are float32.  A
- * row's bits do not depend on the other rows.  Any H from 1 to MOE_NORM_MAX_H and any element
- * alignment; fastest with 16-byte aligned rows.
+ * row's bits do not depend on the other rows or on their number.  Any H from 1 to
+ * MOE_NORM_MAX_H and any element alignment; fastest with 16-byte aligned rows.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (M < 0, H, ldx, eps negative or not
  * finite, a type, residual_out without residual), MOE_ERR_LIMIT (H above the
  * limit, M >= 2^31), MOE_ERR_HIP. */
@@ -160,8 +160,8 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_SWI
  * the experts' runs.
  * A bf16 y may be residual's buffer; an 8-bit y that overlaps it is refused.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_LIMIT (E > MOE_MAX_EXPERTS, rows
- * >= 2^31, a matrix of one expert or 256 rows of x or y past 2^31 bytes),
- * MOE_ERR_HIP. */
+ * >= 2^31, a matrix of one expert or 256 rows of x or y past 2^31 bytes, 2^31
+ * tiles of 16 x 16 or nearly so), MOE_ERR_HIP. */
 typedef struct {
   int64_t rows;
   int32_t E, N, K;

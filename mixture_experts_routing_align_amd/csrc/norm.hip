@@ -104,12 +104,12 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
   }
   float mean = square_sum<TPR>(z, red) / (float)H, eps = a.eps, unit = 1.f, pre = 1.f;
   // Squares that leave float32's range (means past 2^100, or below 2^-100 with next to no
-  // eps) are summed once more in a unit
-  // that keeps them inside it: 2^-80 (32768 of the largest value make 2^111) or 2^96 (the
-  // smallest subnormal's square is 2^-106, and the sum stays below 2^107).  The whole row
-  // takes the same way.  y comes from z in a unit `pre` in which neither z nor rstd
-  // leaves the range: large rows in 2^-16, which makes a subnormal rstd (below 2^-126) a
-  // normal float and costs bits only of values whose y is 0; small rows in 2^96.
+  // eps) are summed once more in a unit that keeps them inside it: 2^-80 (32768 of the
+  // largest value make 2^111) or 2^96 (the smallest subnormal's square is 2^-106, and the
+  // sum stays below 2^107).  The whole row takes the same way.  y comes from z in a unit
+  // `pre` in which neither z nor rstd leaves the range: large rows in 2^-16, which makes a
+  // subnormal rstd (below 2^-126) a normal float and costs bits only of values whose y is
+  // 0; small rows in 2^96.
   const bool large = mean > kLargeMean, small = mean < kSmallMean && eps < kSmallEps;
   if (large || small) {
     unit = large ? 0x1p-80f : 0x1p96f;
