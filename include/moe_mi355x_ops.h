@@ -34,6 +34,13 @@
  *     scale, both quotients rounded to float32 (where the exact quotient lies on the
  *     border of two codes, the rounding of the float32 value decides); a block with a
  *     NaN or an infinity gets a NaN scale, so all of it reads as NaN.
+ *   - MXFP4 rows are E2M1 codes [rows, C/2], two per byte, the even column in the
+ *     lower nibble, with one E8M0 byte per 32 columns, [rows, C/32], as the MXFP4
+ *     weights of moe_mi355x.h are; a value is code * 2^(byte - 127).  The byte of a
+ *     block made here is the exponent of its absolute maximum less 2, so that the
+ *     maximum over the scale lies in [4, 8), at least 2, and 127 for a block of zeros;
+ *     a code is the nearest (ties to even) to the value over the scale, at most 6.  A
+ *     block with a NaN or an infinity gets the byte 255, E8M0's NaN, and zero codes.
  *   - Sorted rows: expert e's rows are [expert_offsets[e], expert_offsets[e] +
  *     expert_counts[e]) of a [rows, C] matrix, as moe_align lays them out (the
  *     offsets padded to its block size).  Rows outside every expert's run
@@ -54,7 +61,7 @@ extern "C" {
  * moe_abi_version() is that of moe_mi355x.h). */
 int32_t moe_ops_abi_version(void);
 
-typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_E4M3 = 2 } moe_dtype;
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_E4M3 = 2, MOE_DT_MXFP4 = 3 } moe_dtype;
 
 /* ------------------------------------------------------------------ norm -- */
 
@@ -212,6 +219,101 @@ int moe_grouped_linear_backward_w(const void* dz_bf16, const void* x_bf16, int32
                                   const int32_t* expert_offsets, const int32_t* expert_counts, int64_t rows,
                                   int32_t E, int32_t N, int32_t K, moe_dtype wdt, void* dw, void* dup, float* db,
                                   float* dup_b, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* -------------------------------------------------------------- 4-bit rows -- */
+
+/* Rows of x ([M, H], bf16 or float32 by `xdt`, `ldx` >= H elements from row to row,
+ * H a multiple of 32) as MXFP4 rows.  With token_to_perm ([M * top_k]) the codes of
+ * token t go to row token_to_perm[t*top_k + k] for every slot whose position is in
+ * [0, rows), as moe_permute lays rows out: rows no slot maps to are not written, and
+ * positions in [0, rows) differ from slot to slot.  With token_to_perm NULL row t goes
+ * to row t (top_k 1, rows M).  Weights [E, N, K] are E * N rows of K, and the result
+ * is what MOE_W_MXFP4 stands for.  codes 16-byte aligned, x at its element's
+ * alignment, scales at any.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (a size, a type, an
+ * alignment), MOE_ERR_LIMIT (M*top_k or rows >= 2^31, H >= 2^29), MOE_ERR_HIP. */
+int moe_mxfp4_quantize(const void* x, moe_dtype xdt, int64_t ldx, const int32_t* token_to_perm, int64_t M,
+                       int32_t top_k, int32_t H, void* codes, uint8_t* scales, int64_t rows, hipStream_t stream);
+
+/* The values of MXFP4 rows ([rows, H], H a multiple of 32), bf16 or float32 (`odt`):
+ * exact for every scale byte that moe_mxfp4_quantize makes.  codes and out 16-byte
+ * aligned.  Errors as above. */
+int moe_mxfp4_dequantize(const void* codes, const uint8_t* scales, int64_t rows, int32_t H, void* out, moe_dtype odt,
+                         hipStream_t stream);
+
+/* moe_grouped_linear on row-major MXFP4 weights:
+ *   w, up       codes [E, N, K/2] with scale bytes [E, N, K/32]
+ *   x           [rows, K] by `xdt`: bf16 (x_scale NULL), or MXFP4 rows with x_scale
+ *   y           [rows, N] by `ydt`: bf16, or MXFP4 rows with y_scale
+ * and everything else as there.  Weights and MXFP4 rows enter the products as the
+ * values they stand for, sums are float32 (scale bytes 2 to 252 are exact; 255 makes
+ * NaN of its block's products; the others' results are not specified).
+ * Shapes: K a multiple of 32, N of 8, with MXFP4 y of 32.  x, w.w, up.w, bias,
+ * up_bias, y, residual and preact 16-byte aligned, scale bytes at any alignment.  A
+ * bf16 y may be residual's buffer; an MXFP4 y that overlaps it is refused.  Errors as
+ * for moe_grouped_linear. */
+typedef struct {
+  int64_t rows;
+  int32_t E, N, K;
+  moe_dtype xdt;
+  moe_act act;
+  moe_dtype ydt;
+  const int32_t* expert_offsets;
+  const int32_t* expert_counts;
+  const void* x;
+  const uint8_t* x_scale;
+  moe_weight w, up;
+  const void* bias;
+  const void* up_bias;
+  const void* residual;
+  void* y;
+  uint8_t* y_scale;
+  void* preact;
+} moe_linear_mxfp4_desc;
+
+int moe_grouped_linear_mxfp4(const moe_linear_mxfp4_desc* d, hipStream_t stream);
+
+/* moe_grouped_linear_backward_x on such weights (`up` NULL: one product): dz bf16
+ * [rows, N] (or [rows, 2N]), dx bf16 [rows, K].  The weights' own gradient does not
+ * depend on them: moe_grouped_linear_backward_w gives it, from bf16 rows. */
+int moe_grouped_linear_mxfp4_backward_x(const void* dz_bf16, const moe_weight* w, const moe_weight* up,
+                                        const int32_t* expert_offsets, const int32_t* expert_counts, int64_t rows,
+                                        int32_t E, int32_t N, int32_t K, void* dx_bf16, hipStream_t stream);
+
+/* ------------------------------------------------------- gradients, clipped -- */
+
+/* One of many gradients: `n` elements of type `dt` (bf16 or float32), contiguous, at
+ * their element's alignment (n may be 0).  `out` is where moe_grad_clip writes it: g
+ * itself or a buffer that overlaps no tensor of the list; the norm does not use it. */
+typedef struct {
+  const void* g;
+  void* out;
+  int64_t n;
+  moe_dtype dt;
+} moe_grad_tensor;
+
+/* Bytes of workspace (8-byte aligned device memory) for `count` tensors; 0 for a count
+ * the calls refuse. */
+size_t moe_grad_norm_workspace_bytes(int64_t count);
+
+/* norm[0] = (sum over the tensors' elements of g^2)^(1/2): summed in 64 bits in a
+ * fixed order, rounded to float32 (0 without an element, an infinity past its range).
+ * `list` is host memory and is read before the call returns.  Errors: MOE_ERR_NULL,
+ * MOE_ERR_SHAPE (a count or size negative, a type, an alignment), MOE_ERR_LIMIT (2^20
+ * tensors, 2^44 elements), MOE_ERR_WORKSPACE, MOE_ERR_HIP. */
+int moe_grad_norm(const moe_grad_tensor* list, int64_t count, float* norm, void* workspace, size_t workspace_bytes,
+                  hipStream_t stream);
+
+/* out = g * c for every tensor, rounded to its type, with c = max_norm / norm[0] where
+ * norm[0] is past max_norm (finite, not negative), else 1; also 1 where norm[0] is NaN or
+ * infinite, so gradients that cannot be scaled stay as they are and the norm tells.  norm
+ * is device memory and not an output.  A gradient that stays as it is and where it is is
+ * not written.  Errors as above, plus MOE_ERR_SHAPE for max_norm, and for an `out` that
+ * overlaps another tensor of the list or a part of its own. */
+int moe_grad_clip(const moe_grad_tensor* list, int64_t count, const float* norm, float max_norm, hipStream_t stream);
+
+/* moe_grad_norm, then moe_grad_clip with its result: the same bits in fewer launches. */
+int moe_clip_grad_norm(const moe_grad_tensor* list, int64_t count, float max_norm, float* norm, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -11,7 +11,8 @@ Entry points (same names as the C ABI): ``moe_align``,
 ``moe_layer_forward`` (via :class:`MoeLayer`), ``moe_layer_workspace_bytes``,
 ``moe_align_max_total``, ``moe_active_cap``, ``moe_tile_weights``,
 ``moe_tiled_weight_bytes``, ``moe_align_gate_up_silu``.  The operators around
-the layer (norm, rows by expert, expert products, gradients) are in
+the layer (norm, rows by expert, expert products, 4-bit rows and weights,
+gradients) are in
 :mod:`.ops` and importable from here under their C names.
 
 Weights are passed as ``(w, scale)`` pairs: ``w`` is ``[E, N, K]``
@@ -520,10 +521,17 @@ def moe_layer_forward(layer: MoeLayer, x, topk_ids, topk_weights, out=None, work
 from .ops import (  # noqa: E402,F401
     moe_add_rms_norm,
     moe_add_rms_norm_backward,
+    moe_clip_grad_norm,
+    moe_grad_clip,
+    moe_grad_norm,
     moe_grouped_act_backward,
     moe_grouped_linear,
     moe_grouped_linear_backward_w,
     moe_grouped_linear_backward_x,
+    moe_grouped_linear_mxfp4,
+    moe_grouped_linear_mxfp4_backward_x,
+    moe_mxfp4_dequantize,
+    moe_mxfp4_quantize,
     moe_permute,
     moe_unpermute,
     moe_unpermute_backward,

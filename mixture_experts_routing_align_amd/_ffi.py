@@ -110,6 +110,7 @@ SIGNATURES = {
 MOE_DT_BF16 = 0
 MOE_DT_F32 = 1
 MOE_DT_E4M3 = 2
+MOE_DT_MXFP4 = 3
 MOE_ACT_NONE = 0
 MOE_ACT_SILU = 1
 MOE_ACT_GELU = 2
@@ -126,6 +127,19 @@ class MoeLinearDesc(ctypes.Structure):
         ("x_scale", c_void_p), ("w", MoeWeight), ("up", MoeWeight), ("bias", c_void_p), ("up_bias", c_void_p),
         ("residual", c_void_p), ("y", c_void_p), ("y_scale", c_void_p), ("preact", c_void_p),
     ]
+
+
+class MoeLinearMxfp4Desc(ctypes.Structure):
+    _fields_ = [
+        ("rows", c_int64), ("E", c_int32), ("N", c_int32), ("K", c_int32), ("xdt", c_int), ("act", c_int),
+        ("ydt", c_int), ("expert_offsets", c_void_p), ("expert_counts", c_void_p), ("x", c_void_p),
+        ("x_scale", c_void_p), ("w", MoeWeight), ("up", MoeWeight), ("bias", c_void_p), ("up_bias", c_void_p),
+        ("residual", c_void_p), ("y", c_void_p), ("y_scale", c_void_p), ("preact", c_void_p),
+    ]
+
+
+class MoeGradTensor(ctypes.Structure):
+    _fields_ = [("g", c_void_p), ("out", c_void_p), ("n", c_int64), ("dt", c_int)]
 
 
 OPS_SIGNATURES = {
@@ -149,6 +163,17 @@ OPS_SIGNATURES = {
     "moe_grouped_linear_backward_w": (c_int, [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int32,
                                               c_int32, c_int32, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
                                               c_void_p, c_size_t, c_void_p]),
+    "moe_mxfp4_quantize": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_int64, c_int32, c_int32, c_void_p, c_void_p,
+                                   c_int64, c_void_p]),
+    "moe_mxfp4_dequantize": (c_int, [c_void_p, c_void_p, c_int64, c_int32, c_void_p, c_int, c_void_p]),
+    "moe_grouped_linear_mxfp4": (c_int, [P(MoeLinearMxfp4Desc), c_void_p]),
+    "moe_grouped_linear_mxfp4_backward_x": (c_int, [c_void_p, P(MoeWeight), P(MoeWeight), c_void_p, c_void_p, c_int64,
+                                                    c_int32, c_int32, c_int32, c_void_p, c_void_p]),
+    "moe_grad_norm_workspace_bytes": (c_size_t, [c_int64]),
+    # lists of gradients go by address: the binding packs them into one buffer
+    "moe_grad_norm": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_grad_clip": (c_int, [c_void_p, c_int64, c_void_p, c_float, c_void_p]),
+    "moe_clip_grad_norm": (c_int, [c_void_p, c_int64, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
 }
 
 _LIB = None

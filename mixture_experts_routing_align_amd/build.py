@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
 SOURCES = ["align.hip", "grouped.hip", "grouped_gu_fp8.hip", "grouped_gu_bf16.hip", "grouped_gu_fp4.hip",
            "grouped_down_fp8.hip", "grouped_down_bf16.hip", "grouped_down_fp4.hip", "layer_fused.hip", "narrow.hip", "wide.hip", "blend.hip", "probe.hip", "router.hip", "noalloc.hip", "api.cpp",
-           "norm.hip", "permute.hip", "linear.hip", "ops_api.cpp"]
+           "norm.hip", "permute.hip", "linear.hip", "linear_mx.hip", "mx.hip", "gradnorm.hip", "ops_api.cpp"]
 ARCH = "gfx950"
 
 # packed-fp32-ops stay off: the compiler emits no v_pk_{add,mul,fma}_f32.

@@ -108,4 +108,51 @@ int backward_w_splits(int64_t rows, int E, int N, int K, int parts);
 hipError_t launch_linear_backward_w(const LinearArgs& a, hipStream_t s);
 hipError_t launch_act_backward(const LinearArgs& a, const uint16_t* dy, const uint16_t* pre, uint16_t* dz, hipStream_t s);
 
+// ---- linear_mx.hip: the same products on MXFP4 weights
+struct MxLinearArgs : LinearArgs {
+  const uint8_t* xs;       // scale bytes of MXFP4 rows x, or nullptr: bf16 rows
+  const uint8_t* wsb[2];   // the weights' scale bytes
+  uint8_t* ysb;            // non-nullptr: y is MXFP4 rows
+};
+hipError_t launch_linear_mx(const MxLinearArgs& a, hipStream_t s);
+hipError_t launch_linear_mx_backward_x(const MxLinearArgs& a, hipStream_t s);
+
+// ---- mx.hip
+struct MxQuantizeArgs {
+  const void* x;        // bf16 or float32, ldx elements from row to row
+  int64_t ldx;
+  const int32_t* perm;  // [M * top_k] rows the tokens go to, or nullptr: row t to row t
+  int top_k;
+  int64_t M, rows;
+  int H;
+  uint8_t* codes;       // [rows, H / 2]
+  uint8_t* scales;      // [rows, H / 32]
+};
+hipError_t launch_mx_quantize(const MxQuantizeArgs& a, bool f32, hipStream_t s);
+
+struct MxDequantizeArgs {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  void* out;            // bf16 or float32
+  int64_t pieces;       // of 8 values
+};
+hipError_t launch_mx_dequantize(const MxDequantizeArgs& a, bool f32, hipStream_t s);
+
+// ---- gradnorm.hip
+struct GradTensor {
+  const void* g;
+  void* out;
+  int64_t n;            // elements
+  bool f32;             // float32, else bf16
+};
+size_t grad_norm_workspace(int64_t count);
+// Whether every launch's chunks can be counted in 32 bits.
+bool grad_sizes_ok(const GradTensor* list, int64_t count);
+// Sums of squares into `part`, *parts of them.
+hipError_t launch_grad_squares(const GradTensor* list, int64_t count, double* part, int* parts, hipStream_t s);
+hipError_t launch_grad_norm(const double* part, int parts, float* norm, hipStream_t s);
+// With `part` the norm is formed from the sums and written, else read.
+hipError_t launch_grad_clip(const GradTensor* list, int64_t count, const double* part, int parts, float* norm, float max_norm,
+                            bool in_place, hipStream_t s);
+
 }  // namespace moe

@@ -8,6 +8,8 @@ here, each backward pass is a call of its own.  All tensors must live on the
 current device.  Outputs not given are allocated, on the stream the call runs
 on; rows of an output that belong to no expert are left as they are.
 
+MXFP4 rows are ``torch.uint8`` codes ``[rows, C / 2]`` (two E2M1 codes per byte, lower
+nibble first) with ``torch.uint8`` E8M0 scales ``[rows, C / 32]``.
 8-bit rows are ``torch.float8_e4m3fn`` codes ``[rows, C]`` with float32 scales
 ``[rows, C / 128]``.  ``expert_offsets`` and ``expert_counts`` are those of
 :class:`AlignTables`; ``None`` for both means one expert that holds every row (a
@@ -17,7 +19,8 @@ dense projection with weights ``[1, N, K]`` or ``[N, K]``).
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from array import array
+from typing import List, Optional, Sequence, Tuple
 
 import torch
 
@@ -30,15 +33,18 @@ from ._ffi import (
     MOE_DT_BF16,
     MOE_DT_E4M3,
     MOE_DT_F32,
+    MOE_DT_MXFP4,
     MOE_W_BF16,
     MOE_W_FP8_E4M3,
     MoeLinearDesc,
+    MoeLinearMxfp4Desc,
     MoeWeight,
 )
 
 ACTIVATIONS = {"none": MOE_ACT_NONE, "silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU, "swiglu": MOE_ACT_SWIGLU}
 _STREAM_TYPES = {torch.bfloat16: MOE_DT_BF16, torch.float32: MOE_DT_F32}
 BLOCK = 128
+MX_BLOCK = 32
 
 
 def _need(cond: bool, msg: str) -> None:
@@ -119,6 +125,7 @@ def _out(t, shape, dtype, like, stream, what: str, dev: int) -> torch.Tensor:
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
+_U8 = (torch.uint8,)
 _E4M3 = torch.float8_e4m3fn
 _STREAM = (torch.bfloat16, torch.float32)
 _ROWS = (torch.bfloat16, _E4M3)
@@ -438,3 +445,219 @@ def moe_grouped_linear_backward_w(dz: torch.Tensor, x: torch.Tensor, expert_offs
         _STREAM_TYPES[dtype], dw[0].data_ptr(), _ptr(dw[1]), _ptr(db[0]), _ptr(db[1]), _ptr(ws), nbytes,
         _stream(stream, dev)))
     return dw[0], dw[1], db[0], db[1]
+
+
+# ------------------------------------------------------------- 4-bit rows --
+
+def moe_mxfp4_quantize(x: torch.Tensor, token_to_perm: Optional[torch.Tensor] = None, top_k: int = 1,
+                       rows: Optional[int] = None, codes: Optional[torch.Tensor] = None,
+                       scales: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """x (bf16 or float32) as MXFP4: ``(codes, scales)``, uint8 ``[..., C/2]`` and ``[..., C/32]``.
+
+    x is ``[M, C]`` (rows may be further than C apart) or, contiguous, a weight ``[E, N,
+    K]``, whose result is a weight pair of this package.  With `token_to_perm` the codes
+    of token t go to the rows of its slots, as in moe_permute: `rows` is the height of
+    the sorted matrix, and rows that no slot maps to are left as they are.  Straight
+    through the rounding the gradient of x is that of its values."""
+    _need(isinstance(x, torch.Tensor) and x.dtype in _STREAM_TYPES and x.dim() >= 2, "x must be bf16 or float32 [M, C]")
+    dev = _device(x, "x")
+    C = x.shape[-1]
+    _need(C > 0 and C % MX_BLOCK == 0, "MXFP4 rows need whole blocks of 32 columns")
+    if x.dim() == 2:
+        M = x.shape[0]
+        ldx = x.stride(0) if M > 1 else C
+        _need(x.stride(1) == 1 and ldx >= C, "x must have contiguous rows that do not overlap")
+    else:
+        _need(x.is_contiguous(), "x must be contiguous, or [M, C]")
+        M, ldx = x.numel() // C, C
+    lead = x.shape[:-1]
+    if token_to_perm is None:
+        _need(top_k == 1 and rows in (None, M), "top_k and rows go with token_to_perm")
+        rows = M
+    else:
+        _need(x.dim() == 2 and _slots(token_to_perm, top_k, dev) == M, "token_to_perm must hold M * top_k entries")
+        _need(rows is not None and rows >= 0, "token_to_perm needs the rows of the sorted matrix")
+        lead = (rows,)
+    codes = _out(codes, (*lead, C // 2), torch.uint8, x, stream, "codes", dev)
+    scales = _out(scales, (*lead, C // MX_BLOCK), torch.uint8, x, stream, "scales", dev)
+    _check(_ffi.load().moe_mxfp4_quantize(x.data_ptr(), _STREAM_TYPES[x.dtype], ldx, _ptr(token_to_perm), M, top_k, C,
+                                          codes.data_ptr(), scales.data_ptr(), rows, _stream(stream, dev)))
+    return codes, scales
+
+
+def moe_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values of MXFP4 codes ``[..., C/2]`` and scales ``[..., C/32]``, of `dtype`
+    (bfloat16 or float32), which holds them exactly."""
+    _need(dtype in _STREAM_TYPES, "dtype must be bfloat16 or float32")
+    dev = _device(codes, "codes")
+    _matrix(codes, "codes", _U8, None, dev)
+    _need(codes.dim() >= 1 and codes.shape[-1] > 0 and codes.shape[-1] % (MX_BLOCK // 2) == 0,
+          "MXFP4 rows need whole blocks of 32 columns")
+    C = 2 * codes.shape[-1]
+    _matrix(scales, "scales", _U8, (*codes.shape[:-1], C // MX_BLOCK), dev)
+    out = _out(out, (*codes.shape[:-1], C), dtype, codes, stream, "out", dev)
+    _check(_ffi.load().moe_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), codes.numel() * 2 // C, C, out.data_ptr(),
+                                            _STREAM_TYPES[dtype], _stream(stream, dev)))
+    return out
+
+
+def _mxfp4_weight(wt, what: str, dev: int):
+    """(codes, scales, E, N, K) of an MXFP4 weight pair."""
+    _need(isinstance(wt, tuple) and len(wt) == 2, what + " must be a pair of MXFP4 codes and scales")
+    w, s = wt
+    _matrix(w, what, _U8, None, dev)
+    _need(w.dim() in (2, 3), what + " must be [E, N, K/2] or [N, K/2]")
+    N, K = w.shape[-2], 2 * w.shape[-1]
+    _need(K > 0 and K % MX_BLOCK == 0, "MXFP4 weights come in whole blocks of 32 columns")
+    _matrix(s, what + " scales", _U8, (*w.shape[:-1], K // MX_BLOCK), dev)
+    return w, s, w.shape[0] if w.dim() == 3 else 1, N, K
+
+
+def moe_grouped_linear_mxfp4(x: torch.Tensor, w, expert_offsets: Optional[torch.Tensor] = None,
+                             expert_counts: Optional[torch.Tensor] = None, act: str = "none", up=None,
+                             bias: Optional[torch.Tensor] = None, up_bias: Optional[torch.Tensor] = None,
+                             residual: Optional[torch.Tensor] = None, x_scale: Optional[torch.Tensor] = None,
+                             mxfp4_out: bool = False, save_preact: bool = False, out: Optional[torch.Tensor] = None,
+                             out_scale: Optional[torch.Tensor] = None, preact: Optional[torch.Tensor] = None, stream=None):
+    """moe_grouped_linear on row-major MXFP4 weights: `w` (and `up`) are pairs of codes
+    ``[E, N, K/2]`` (or ``[N, K/2]``) and scales ``[E, N, K/32]``.
+
+    x is bf16 [rows, K], or with `x_scale` the codes of MXFP4 rows [rows, K/2].  Returns
+    ``(y, y_scale, preact)``: y bf16 [rows, N] (may be `residual` itself), or with
+    `mxfp4_out` (or a uint8 `out`) the codes and scales of MXFP4 rows; preact as there."""
+    _need(act in ACTIVATIONS, "act must be one of none, silu, gelu, swiglu")
+    gated = act == "swiglu"
+    dev = _device(x, "x")
+    wt, ws, E, N, K = _mxfp4_weight(w, "w", dev)
+    _runs(expert_offsets, expert_counts, E, dev)
+    _need(x.dim() == 2, "x must be [rows, K]")
+    rows = x.shape[0]
+    rows4 = x_scale is not None
+    if rows4:
+        _matrix(x, "x", _U8, (rows, K // 2), dev)
+        _matrix(x_scale, "x_scale", _U8, (rows, K // MX_BLOCK), dev)
+    else:
+        _matrix(x, "x", _BF16, (rows, K), dev)
+    _need(gated == (up is not None), "up goes with act='swiglu'")
+    ut = us = None
+    if gated:
+        ut, us, E2, N2, K2 = _mxfp4_weight(up, "up", dev)
+        _need((E2, N2, K2) == (E, N, K), "up must match w")
+    else:
+        _need(up_bias is None, "up_bias goes with act='swiglu'")
+    if bias is not None:
+        _matrix(bias, "bias", _BF16, None, dev)
+        _need(bias.numel() == E * N, "bias must be [E, N]")
+    if up_bias is not None:
+        _matrix(up_bias, "up_bias", _BF16, None, dev)
+        _need(up_bias.numel() == E * N, "up_bias must be [E, N]")
+    if residual is not None:
+        _matrix(residual, "residual", _BF16, (rows, N), dev)
+    mxfp4_out = mxfp4_out or (out is not None and out.dtype == torch.uint8)
+    if mxfp4_out:
+        _need(N % MX_BLOCK == 0, "MXFP4 rows need whole blocks of 32 columns")
+        out = _out(out, (rows, N // 2), torch.uint8, x, stream, "out", dev)
+        out_scale = _out(out_scale, (rows, N // MX_BLOCK), torch.uint8, x, stream, "out_scale", dev)
+    else:
+        _need(out_scale is None, "out_scale without MXFP4 output")
+        out = _out(out, (rows, N), torch.bfloat16, x, stream, "out", dev)
+    if save_preact or preact is not None:
+        preact = _out(preact, (rows, (2 if gated else 1) * N), torch.bfloat16, x, stream, "preact", dev)
+    d = MoeLinearMxfp4Desc(rows, E, N, K, MOE_DT_MXFP4 if rows4 else MOE_DT_BF16, ACTIVATIONS[act],
+                           MOE_DT_MXFP4 if mxfp4_out else MOE_DT_BF16, _ptr(expert_offsets), _ptr(expert_counts),
+                           x.data_ptr(), _ptr(x_scale), MoeWeight(wt.data_ptr(), ws.data_ptr()),
+                           MoeWeight(_ptr(ut), _ptr(us)), _ptr(bias), _ptr(up_bias), _ptr(residual), out.data_ptr(),
+                           _ptr(out_scale), _ptr(preact))
+    _check(_ffi.load().moe_grouped_linear_mxfp4(ctypes.byref(d), _stream(stream, dev)))
+    return out, out_scale, preact
+
+
+def moe_grouped_linear_mxfp4_backward_x(dz: torch.Tensor, w, expert_offsets: Optional[torch.Tensor] = None,
+                                        expert_counts: Optional[torch.Tensor] = None, up=None,
+                                        dx: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_grouped_linear_backward_x on MXFP4 weight pairs: dx[p] = W[e]^T dz[p], plus
+    W_up[e]^T of dz's second half with `up`; dz and dx bf16."""
+    dev = _device(dz, "dz")
+    wt, ws, E, N, K = _mxfp4_weight(w, "w", dev)
+    _runs(expert_offsets, expert_counts, E, dev)
+    second = None
+    if up is not None:
+        ut, us, E2, N2, K2 = _mxfp4_weight(up, "up", dev)
+        _need((E2, N2, K2) == (E, N, K), "up must match w")
+        second = ctypes.byref(MoeWeight(ut.data_ptr(), us.data_ptr()))
+    _need(dz.dim() == 2, "dz must be [rows, N]")
+    rows = dz.shape[0]
+    _matrix(dz, "dz", _BF16, (rows, N if up is None else 2 * N), dev)
+    dx = _out(dx, (rows, K), torch.bfloat16, dz, stream, "dx", dev)
+    _check(_ffi.load().moe_grouped_linear_mxfp4_backward_x(
+        dz.data_ptr(), ctypes.byref(MoeWeight(wt.data_ptr(), ws.data_ptr())), second, _ptr(expert_offsets),
+        _ptr(expert_counts), rows, E, N, K, dx.data_ptr(), _stream(stream, dev)))
+    return dx
+
+
+# ------------------------------------------------------ gradients, clipped --
+
+def _grad_list(grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]], dev: int):
+    """The gradients and their outputs as the C list, packed."""
+    packed = array("q")
+    for i, g in enumerate(grads):
+        if not (isinstance(g, torch.Tensor) and g.dtype in _STREAM_TYPES and g.is_contiguous() and g.get_device() == dev):
+            _matrix(g, f"gradient {i}", _STREAM, None, dev)
+        at = g.data_ptr()
+        to = at
+        if out is not None:
+            o = out[i]
+            _matrix(o, f"output {i}", (g.dtype,), g.shape, dev)
+            to = o.data_ptr()
+        packed.extend((at, to, g.numel(), _STREAM_TYPES[g.dtype]))
+    return packed
+
+
+def _grad_device(grads, out, what: str) -> int:
+    _need(isinstance(grads, (list, tuple)) and len(grads) > 0, what + " takes a list of at least one gradient")
+    _need(out is None or (isinstance(out, (list, tuple)) and len(out) == len(grads)), "out must match the gradients")
+    return _device(grads[0], "gradient 0")
+
+
+def moe_grad_norm(grads: Sequence[torch.Tensor], norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The 2-norm of all elements of all gradients together (bf16 or float32, contiguous,
+    any shapes), float32 [1] on the device; summed in 64 bits in a fixed order.  Where the
+    gradients are spread over GPUs, the norms' squares are what to add up before
+    moe_grad_clip."""
+    dev = _grad_device(grads, None, "moe_grad_norm")
+    packed = _grad_list(grads, None, dev)
+    norm = _out(norm, (1,), torch.float32, grads[0], stream, "norm", dev)
+    lib = _ffi.load()
+    nbytes = lib.moe_grad_norm_workspace_bytes(len(grads))
+    ws = _new((nbytes,), torch.uint8, grads[0], stream)
+    _check(lib.moe_grad_norm(packed.buffer_info()[0], len(grads), norm.data_ptr(), ws.data_ptr(), nbytes,
+                             _stream(stream, dev)))
+    return norm
+
+
+def moe_grad_clip(grads: Sequence[torch.Tensor], norm: torch.Tensor, max_norm: float,
+                  out: Optional[Sequence[torch.Tensor]] = None, stream=None) -> List[torch.Tensor]:
+    """The gradients times ``max_norm / norm`` where `norm` (float32 [1] on the device) is
+    past `max_norm`, else unchanged, as where the norm is NaN or infinite; in place, or
+    into `out`.  Returns the list written."""
+    dev = _grad_device(grads, out, "moe_grad_clip")
+    packed = _grad_list(grads, out, dev)
+    _matrix(norm, "norm", _F32, (1,), dev)
+    _check(_ffi.load().moe_grad_clip(packed.buffer_info()[0], len(grads), norm.data_ptr(), max_norm, _stream(stream, dev)))
+    return list(grads if out is None else out)
+
+
+def moe_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
+                       norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_grad_norm, then moe_grad_clip with its result, in fewer launches: the gradients
+    are scaled in place (or into `out`), their norm before that is returned."""
+    dev = _grad_device(grads, out, "moe_clip_grad_norm")
+    packed = _grad_list(grads, out, dev)
+    norm = _out(norm, (1,), torch.float32, grads[0], stream, "norm", dev)
+    lib = _ffi.load()
+    nbytes = lib.moe_grad_norm_workspace_bytes(len(grads))
+    ws = _new((nbytes,), torch.uint8, grads[0], stream)
+    _check(lib.moe_clip_grad_norm(packed.buffer_info()[0], len(grads), max_norm, norm.data_ptr(), ws.data_ptr(), nbytes,
+                                  _stream(stream, dev)))
+    return norm
