@@ -28,6 +28,302 @@ using namespace epilogue;
 
 extern __shared__ __attribute__((aligned(1024))) char smem[];
 
+// ---------------------------------------------------------------- forward --
+
+// Scale bytes of a stage's R operand rows, 8 a row (256 depth elements), staged by direct
+// 4-byte loads.  ALIGNED: a row's bytes begin at a multiple of 4, as they do where the
+// depth is a multiple of 128 and the array is 4-byte aligned; two loads a row then.  Else
+// the 8 bytes lie in up to three dwords: those from the one that holds the first are
+// loaded (none that holds no byte of the row), and the row's shift into them is added
+// when they are read.
+template <int R, int WAVES, bool ALIGNED>
+struct ScaleTile {
+  static constexpr int kWords = ALIGNED ? 2 : 4;  // dwords of LDS a row
+  static constexpr int kBytes = R * kWords * 4;
+  static constexpr int kPerWave = R * kWords / WAVES;
+  static constexpr int kLoads = (kPerWave + 63) / 64;
+  static_assert(R * kWords % WAVES == 0 && (kPerWave % 64 == 0 || kPerWave < 64), "equal loads for all waves");
+  uint32_t off[kLoads];  // byte offset of each of this lane's dwords in step 0, or kNoFetch
+  int end[kLoads];       // bytes from there to the end of its row
+  bool mine;             // a wave with fewer than 64 dwords leaves the other lanes out
+
+  // `lead`: bytes from the resource's (aligned) base to row 0; `row_of(r)`: the row of the
+  // array that operand row r is, or -1; `S` bytes a row.
+  template <typename F>
+  __device__ __forceinline__ void init(int wave, int lane, int lead, int S, F row_of) {
+    mine = kPerWave >= 64 || lane < kPerWave;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int d = wave * kPerWave + i * 64 + lane, r = row_of(d / kWords), w = d % kWords;
+      const int begin = lead + r * S;
+      off[i] = r < 0 ? kNoFetch : (uint32_t)((begin & ~3) + w * 4);
+      end[i] = begin + S - ((begin & ~3) + w * 4);
+      if (!ALIGNED && w == 3) off[i] = kNoFetch;
+    }
+  }
+  // Fills `lds` with the bytes of step s.
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* lds, int wave, int s) const {
+    if (!mine) return;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (wave * kPerWave + i * 64) * 4), 4,
+                                               s * 8 < end[i] ? off[i] : kNoFetch, s * 8, 0, 0);
+  }
+  // The bytes of blocks 2 q and 2 q + 1 (q = l / 16) for operand row r0 + l % 16, the first
+  // in the lowest byte; `left`: blocks from this step's first to the row's last, past which
+  // the codes are zeros and the byte must not be a NaN's.
+  __device__ static __forceinline__ uint32_t pair(const char* lds, int r0, int lead, int S, int lane, int left) {
+    const int r = r0 + (lane & 15), q = lane >> 4;
+    if constexpr (ALIGNED) {
+      return *reinterpret_cast<const uint16_t*>(lds + r * 8 + q * 2);
+    } else {
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(lds) + r * 16 + ((lead + r * S) & 3) + q * 2;
+      const uint32_t lo = p[0], hi = p[1];
+      return (2 * q < left ? lo : 0u) | (2 * q + 1 < left ? hi << 8 : 0u);
+    }
+  }
+};
+
+// The end of a tile: bias, activation and residual on the float32 sums, pre-activations,
+// bf16 or MXFP4 rows.  Lane l holds row l % 16 and 4 consecutive columns of each subtile,
+// acc[i][j] of a wave's row subtiles i and its columns' subtiles j (SwiGLU: kC of z, then kC
+// of u).  LDS is free.
+template <bool GATED, int BQ, int kCols, int WQ, int WP, int kQ, int kC>
+__device__ __forceinline__ void finish(const MxLinearArgs& a, int e, int64_t first, int live, int p0, int wq, int wp,
+                                       f32x4 (&acc)[kQ][GATED ? 2 * kC : kC]) {
+  constexpr int kParts = GATED ? 2 : 1, kThreads = WQ * WP * 64;
+  static_assert(kC % 2 == 0, "a wave holds whole scale blocks of its rows' columns");
+  const int lane = threadIdx.x & 63, quad = lane >> 4, row16 = lane & 15;
+  const int colw = wp * (kCols / WP) + quad * 4;  // this lane's first column of the tile
+  const int cols = min(kCols, a.N - p0);
+  using Rows = OutTile<BQ, kCols * 2, kThreads>;
+  auto columns = [&](auto f) {  // f(subtile row i, subtile column j, tile row, tile column)
+#pragma unroll
+    for (int i = 0; i < kQ; ++i)
+#pragma unroll
+      for (int j = 0; j < kC; ++j) f(i, j, q_row<WQ>(wq, i) + row16, colw + j * 16);
+  };
+  // act(z, u) + residual in place of z; the pre-activations, where they are kept,
+  // need the bias on both
+  columns([&](int i, int j, int m, int n) {
+    float z[4], u[4], y[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      z[c] = acc[i][j][c];
+      u[c] = acc[i][(GATED ? kC : 0) + j][c];
+    }
+    epilogue4<GATED>(a, e, first + m, p0 + n, m < live && n < cols, z, u, y);
+    if (a.preact != nullptr) {
+      Rows::put(smem, m, n * 2, pack4(z));
+      if (GATED) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][kC + j][c] = u[c];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[i][j][c] = y[c];
+  });
+  if (a.preact != nullptr) {
+    char* pre = reinterpret_cast<char*>(a.preact + first * kParts * a.N + p0);
+    __syncthreads();
+    Rows::flush(smem, pre, (int64_t)kParts * a.N * 2, live, cols * 2);
+    __syncthreads();
+    if constexpr (GATED) {
+      columns([&](int i, int j, int m, int n) {
+        const float u[4] = {acc[i][kC + j][0], acc[i][kC + j][1], acc[i][kC + j][2], acc[i][kC + j][3]};
+        Rows::put(smem, m, n * 2, pack4(u));
+      });
+      __syncthreads();
+      Rows::flush(smem, pre + (int64_t)a.N * 2, (int64_t)2 * a.N * 2, live, cols * 2);
+      __syncthreads();
+    }
+  }
+  if (a.ysb == nullptr) {
+    columns([&](int i, int j, int m, int n) {
+      const float y[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      Rows::put(smem, m, n * 2, pack4(y));
+    });
+    __syncthreads();
+    Rows::flush(smem, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + first * a.N + p0), (int64_t)a.N * 2, live, cols * 2);
+    return;
+  }
+  // a scale block is two subtiles over the four quads of one wave
+  using Codes = OutTile<BQ, kCols / 2, kThreads>;
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) {
+    const int m = q_row<WQ>(wq, i) + row16;
+#pragma unroll
+    for (int j = 0; j < kC; j += 2) {
+      uint32_t mx = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mx = max(mx, max(row::abs_bits(acc[i][j][c]), row::abs_bits(acc[i][j + 1][c])));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
+      const uint32_t byte = mx::scale_byte(mx);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        Codes::put(smem, m, (colw + (j + h) * 16) / 2,
+                   (uint16_t)mx::codes4(acc[i][j + h][0], acc[i][j + h][1], acc[i][j + h][2], acc[i][j + h][3], byte));
+      const int n = wp * (kCols / WP) + j * 16;
+      if (quad == 0 && m < live && n < cols) a.ysb[(first + m) * (a.N / mx::kBlock) + (p0 + n) / mx::kBlock] = (uint8_t)byte;
+    }
+  }
+  __syncthreads();
+  Codes::flush(smem, static_cast<char*>(a.y) + (first * a.N + p0) / 2, a.N / 2, live, cols / 2);
+}
+
+// MXFP4 rows: a workgroup's tile is BQ rows by BP weight rows (SwiGLU: BP / 2 of the gate
+// and the same BP / 2 of the up weight), WQ x WP waves, stages of 256 depth elements: 128
+// bytes of codes and 8 of scales a row.  Lane l takes blocks 2 (l / 16) and 2 (l / 16) + 1
+// of a stage, one for each of its two products.
+template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES>
+struct Rows4 {
+  static constexpr int kWaves = WQ * WP, kThreads = kWaves * 64;
+  static constexpr int kParts = GATED ? 2 : 1;
+  static constexpr int kCols = BP / kParts;
+  static constexpr int kQ = BQ / WQ / 16, kP = BP / WP / 16, kC = kP / kParts;
+  using QTile = RowTile<BQ, kWaves>;
+  using PTile = RowTile<kCols, kWaves>;
+  using QScale = ScaleTile<BQ, kWaves, ALIGNED>;
+  using PScale = ScaleTile<kCols, kWaves, ALIGNED>;
+  static constexpr int kPOff = QTile::kBytes, kQSOff = kPOff + kParts * PTile::kBytes, kPSOff = kQSOff + QScale::kBytes;
+  static constexpr int kStage = kPSOff + kParts * PScale::kBytes;
+  static constexpr int kLoads = QTile::kLoads + QScale::kLoads + kParts * (PTile::kLoads + PScale::kLoads);
+  static constexpr int kLds = STAGES * kStage;
+  static_assert(BQ * kCols * 2 <= kLds, "the output tile fits where the stages were");
+};
+
+template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES>
+__global__ __launch_bounds__(WQ* WP * 64, 2) void linear_rows4_kernel(MxLinearArgs a) {
+  using T = Rows4<GATED, ALIGNED, BQ, BP, WQ, WP, STAGES>;
+  constexpr int kQ = T::kQ, kP = T::kP, kC = T::kC, kParts = T::kParts, kCols = T::kCols;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wq = wave / WP, wp = wave % WP;
+  const Item it = find_item(a, row::block_index(), BQ, (a.N + kCols - 1) / kCols);
+  if (it.e < 0) return;
+  const int ld = a.K / 2, S = a.K / mx::kBlock;
+  const int q0 = it.tq * BQ, p0 = it.tp * kCols;
+  const int live = min(BQ, it.count - q0);  // rows of this tile
+  const int64_t first = (int64_t)it.row0 + q0, wfirst = (int64_t)it.e * a.N + p0;
+  const int wlive = min(kCols, a.N - p0);
+  const __amdgpu_buffer_rsrc_t rx = resource(static_cast<const char*>(a.x) + first * ld);
+  // the scales' resources begin at the aligned dword that holds the tile's first byte
+  const uint8_t* const xs = a.xs + first * S;
+  const int xlead = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(xs) & 3);
+  const __amdgpu_buffer_rsrc_t rxs = resource(xs - xlead);
+  __amdgpu_buffer_rsrc_t rw[kParts], rws[kParts];
+  int wlead[kParts];
+#pragma unroll
+  for (int h = 0; h < kParts; ++h) {
+    rw[h] = resource(static_cast<const char*>(a.w[h]) + wfirst * ld);
+    const uint8_t* const ws = a.wsb[h] + wfirst * S;
+    wlead[h] = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(ws) & 3);
+    rws[h] = resource(ws - wlead[h]);
+  }
+  typename T::QTile qt;
+  typename T::PTile pt;
+  typename T::QScale qs;
+  typename T::PScale ps[kParts];
+  qt.init(wave, lane, [&](int r) { return r < live ? (uint32_t)(r * ld) : kNoFetch; });
+  pt.init(wave, lane, [&](int r) { return r < wlive ? (uint32_t)(r * ld) : kNoFetch; });
+  qs.init(wave, lane, xlead, S, [&](int r) { return r < live ? r : -1; });
+#pragma unroll
+  for (int h = 0; h < kParts; ++h) ps[h].init(wave, lane, wlead[h], S, [&](int r) { return r < wlive ? r : -1; });
+  const int steps = (ld + kDB - 1) / kDB;
+  // past the last step nothing is left: the loads are issued and fetch nothing
+  auto issue = [&](int s, int stage) {
+    char* b = smem + stage * T::kStage;
+    qs.load(rxs, b + T::kQSOff, wave, s);
+    if constexpr (STAGES == 2)
+      qt.load_live(rx, b, wave, s * kDB, ld - s * kDB, live);
+    else  // the waits count on every load
+      qt.load(rx, b, wave, s * kDB, ld - s * kDB);
+#pragma unroll
+    for (int h = 0; h < kParts; ++h) {
+      ps[h].load(rws[h], b + T::kPSOff + h * T::PScale::kBytes, wave, s);
+      pt.load(rw[h], b + T::kPOff + h * T::PTile::kBytes, wave, s * kDB, ld - s * kDB);
+    }
+  };
+  f32x4 acc[kQ][kP];
+#pragma unroll
+  for (int i = 0; i < kQ; ++i)
+#pragma unroll
+    for (int j = 0; j < kP; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) issue(s, s);
+
+  auto p_row = [&](int j) { return wp * (kCols / WP) + (j % kC) * 16; };
+  auto multiply = [&](auto live_subtiles) {
+    constexpr int L = decltype(live_subtiles)::value;
+    constexpr int kNext = (STAGES - 2) * T::kLoads;
+    int stage = 0;
+    uint4 q[2][L], p[2][kP];
+    // scales of this step and of the next, those of two subtiles in a register
+    constexpr int kSq = (L + 1) / 2, kSp = (kP + 1) / 2;
+    uint32_t sq[kSq], sp[kSp], nq[kSq], np[kSp];
+    auto piece = [&](const char* b, int r0, int k) {
+      return *reinterpret_cast<const uint4*>(T::QTile::at(b, r0 + (lane & 15), 2 * (lane >> 4) + k));
+    };
+    auto read = [&](int k) {
+      const char* b = smem + stage * T::kStage;
+#pragma unroll
+      for (int i = 0; i < L; ++i) q[k][i] = piece(b, q_row<WQ>(wq, i), k);
+#pragma unroll
+      for (int j = 0; j < kP; ++j) p[k][j] = piece(b + T::kPOff + j / kC * T::PTile::kBytes, p_row(j), k);
+    };
+    auto read_scales = [&](int s) {
+      const char* b = smem + stage * T::kStage;
+      const int left = S - s * 8;
+      auto of_q = [&](int i) { return T::QScale::pair(b + T::kQSOff, q_row<WQ>(wq, i), xlead, S, lane, left); };
+      auto of_p = [&](int j) {
+        return T::PScale::pair(b + T::kPSOff + j / kC * T::PScale::kBytes, p_row(j), wlead[j / kC], S, lane, left);
+      };
+#pragma unroll
+      for (int i = 0; i < kSq; ++i) nq[i] = of_q(2 * i) | (2 * i + 1 < L ? of_q(2 * i + 1) << 16 : 0u);
+#pragma unroll
+      for (int j = 0; j < kSp; ++j) np[j] = of_p(2 * j) | (2 * j + 1 < kP ? of_p(2 * j + 1) << 16 : 0u);
+    };
+    auto products = [&](auto half) {
+      constexpr int H = decltype(half)::value;
+#pragma unroll
+      for (int j = 0; j < kP; ++j)
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          if (j % 2 == 0 && i % 2 == 0) acc[i][j] = mx::mfma<H, H>(p[H][j], sp[j / 2], q[H][i], sq[i / 2], acc[i][j]);
+          if (j % 2 == 0 && i % 2 == 1) acc[i][j] = mx::mfma<H, H + 2>(p[H][j], sp[j / 2], q[H][i], sq[i / 2], acc[i][j]);
+          if (j % 2 == 1 && i % 2 == 0) acc[i][j] = mx::mfma<H + 2, H>(p[H][j], sp[j / 2], q[H][i], sq[i / 2], acc[i][j]);
+          if (j % 2 == 1 && i % 2 == 1) acc[i][j] = mx::mfma<H + 2, H + 2>(p[H][j], sp[j / 2], q[H][i], sq[i / 2], acc[i][j]);
+        }
+    };
+    // loads behind the first stage's; with two stages those of rows depend on the rows, so
+    // they are not counted on
+    wait_and_meet<(STAGES - 1) * (T::kLoads - (STAGES == 2 ? T::QTile::kLoads : 0))>();
+    read(0);
+    read_scales(0);
+    for (int s = 0; s < steps; ++s) {
+#pragma unroll
+      for (int i = 0; i < kSq; ++i) sq[i] = nq[i];
+#pragma unroll
+      for (int j = 0; j < kSp; ++j) sp[j] = np[j];
+      read(1);
+      __builtin_amdgcn_sched_barrier(0);  // the reads are on their way before the products
+      products(Count<0>{});
+      __builtin_amdgcn_sched_barrier(0);
+      wait_and_meet<kNext>();  // this step's operands are in registers, the next stage has landed
+      issue(s + STAGES, stage);
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
+      read(0);  // of step s + 1; past the last one whatever lies there, unused
+      read_scales(s + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      products(Count<1>{});
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  by_live_subtiles<kQ>((live - wq * 16 + 16 * WQ - 1) / (16 * WQ), multiply);
+  wait_and_meet<0>();  // the loads past the last step have landed: LDS is free
+  finish<GATED, BQ, kCols, WQ, WP, kQ, kC>(a, it.e, first, live, p0, wq, wp, acc);
+}
+
 // --------------------------------------------------- forward, few rows --
 
 // Few rows per expert: the weights are read once and nothing is reused enough to stage it,
@@ -89,7 +385,7 @@ __global__ __launch_bounds__(WC* WK * 64) void linear_mx_few_kernel(MxLinearArgs
           xb = mx::kZeroByte;
         }
 #pragma unroll
-        for (int h = 0; h < kParts; ++h) acc[h] = mx::mfma<0>(wv[h], wb[h], xv, xb, acc[h]);
+        for (int h = 0; h < kParts; ++h) acc[h] = mx::mfma<0, 0>(wv[h], wb[h], xv, xb, acc[h]);
       } else {
         uint4 xv[4];
 #pragma unroll
@@ -277,6 +573,15 @@ MOE_MX_TILES(false, true)
 MOE_MX_TILES(true, false)
 MOE_MX_TILES(true, true)
 #undef MOE_MX_TILES
+#define MOE_MX_ROWS4(G, A)                                                    \
+  template __global__ void linear_rows4_kernel<G, A, 256, 256, 2, 4, 2>(MxLinearArgs); \
+  template __global__ void linear_rows4_kernel<G, A, 128, 128, 2, 2, 2>(MxLinearArgs); \
+  template __global__ void linear_rows4_kernel<G, A, 64, 64, G ? 4 : 2, G ? 1 : 2, 3>(MxLinearArgs);
+MOE_MX_ROWS4(false, false)
+MOE_MX_ROWS4(false, true)
+MOE_MX_ROWS4(true, false)
+MOE_MX_ROWS4(true, true)
+#undef MOE_MX_ROWS4
 template __global__ void linear_mx_backward_x_kernel<128, 128, 2, 2>(MxLinearArgs);
 
 template <typename K>
@@ -295,6 +600,38 @@ hipError_t run_few(const MxLinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES>
+hipError_t run_rows4(const MxLinearArgs& a, hipStream_t s) {
+  using T = Rows4<GATED, ALIGNED, BQ, BP, WQ, WP, STAGES>;
+  static std::atomic<size_t> allowed[kMaxCachedDevices];
+  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, BQ) * ((a.N + T::kCols - 1) / T::kCols);
+  void (*const kern)(MxLinearArgs) = &linear_rows4_kernel<GATED, ALIGNED, BQ, BP, WQ, WP, STAGES>;
+  return launch(kern, items, T::kThreads, T::kLds, a, s, allowed);
+}
+
+// Rows per expert on average, of the matrix's height, in which the alignment's padding
+// counts: the runs themselves are known on the device only.
+int64_t mean_rows(const MxLinearArgs& a) { return ceil_div(a.rows, a.E); }
+
+// Square tiles of `edge` that the rows and `cols` columns make.
+int64_t tiles(const MxLinearArgs& a, int64_t cols, int64_t edge) {
+  return (a.rows + edge - 1) / edge * ((cols + edge - 1) / edge);
+}
+
+bool wide_tiles(const MxLinearArgs& a, int64_t cols) { return tiles(a, cols, 256) >= 256 && mean_rows(a) >= 160; }
+
+// Rows per expert up to which the depth-split kernel is taken.
+constexpr int64_t kFewRows = 32;
+
+template <bool GATED, bool ALIGNED>
+hipError_t rows4_by_shape(const MxLinearArgs& a, hipStream_t s) {
+  if (mean_rows(a) <= kFewRows) return run_few<true, GATED, 2, 8>(a, s);
+  const int64_t cols = a.parts * (int64_t)a.N;
+  if (tiles(a, cols, 128) < 256) return run_rows4<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2, 3>(a, s);
+  if (wide_tiles(a, cols)) return run_rows4<GATED, ALIGNED, 256, 256, 2, 4, 2>(a, s);
+  return run_rows4<GATED, ALIGNED, 128, 128, 2, 2, 2>(a, s);
+}
+
 template <int BQ, int BP, int WQ, int WP>
 hipError_t run_backward_x(const MxLinearArgs& a, hipStream_t s) {
   static std::atomic<size_t> allowed[kMaxCachedDevices];
@@ -305,7 +642,11 @@ hipError_t run_backward_x(const MxLinearArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_linear_mx(const MxLinearArgs& a, hipStream_t s) {
-  if (a.xs != nullptr) return a.parts == 2 ? run_few<true, true, 2, 8>(a, s) : run_few<true, false, 2, 8>(a, s);
+  if (a.xs != nullptr) {
+    const uintptr_t lead = reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.wsb[0]) | reinterpret_cast<uintptr_t>(a.wsb[1]);
+    if (a.K % 128 == 0 && lead % 4 == 0) return a.parts == 2 ? rows4_by_shape<true, true>(a, s) : rows4_by_shape<false, true>(a, s);
+    return a.parts == 2 ? rows4_by_shape<true, false>(a, s) : rows4_by_shape<false, false>(a, s);
+  }
   return a.parts == 2 ? run_few<false, true, 2, 8>(a, s) : run_few<false, false, 2, 8>(a, s);
 }
 

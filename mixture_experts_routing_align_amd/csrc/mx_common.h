@@ -50,15 +50,15 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t byte) {
 }
 
 // One v_mfma_scale_f32_16x16x128_f8f6f4 on E2M1 codes: lane l feeds row l % 16 of either
-// operand with the 32 codes of one block (16 bytes) and that block's scale byte (byte OP of
-// a dword), and receives D[4 (l / 16) + i][l % 16].  On random codes the result is within
+// operand with the 32 codes of one block (16 bytes) and that block's scale byte (byte OPA or
+// OPB of a dword), and receives D[4 (l / 16) + i][l % 16].  On random codes the result is within
 // 6e-8 of the sum of absolute products, with scales 2^20 apart: float32 sums, unlike the
 // e4m3 form's.
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-template <int OP>
+template <int OPA, int OPB>
 __device__ __forceinline__ mma::f32x4 mfma(uint4 a, uint32_t sa, uint4 b, uint32_t sb, mma::f32x4 c) {
   const i32x8 av{(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0}, bv{(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, OP, (int)sa, OP, (int)sb);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, OPA, (int)sa, OPB, (int)sb);
 }
 
 }  // namespace mx
