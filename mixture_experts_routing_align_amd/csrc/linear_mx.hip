@@ -28,58 +28,72 @@ using namespace epilogue;
 
 extern __shared__ __attribute__((aligned(1024))) char smem[];
 
+__device__ __forceinline__ u32x4 as_vec(uint4 v) { return u32x4{v.x, v.y, v.z, v.w}; }
+
+// Calls f with 0, 1, ... N - 1, each a constant.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (I < N) {
+    f(Count<I>{});
+    each<N, I + 1>(f);
+  }
+}
+
 // ---------------------------------------------------------------- forward --
 
-// Scale bytes of a stage's R operand rows, 8 a row (256 depth elements), staged by direct
-// 4-byte loads.  ALIGNED: a row's bytes begin at a multiple of 4, as they do where the
-// depth is a multiple of 128 and the array is 4-byte aligned; two loads a row then.  Else
-// the 8 bytes lie in up to three dwords: those from the one that holds the first are
-// loaded (none that holds no byte of the row), and the row's shift into them is added
-// when they are read.
-template <int R, int WAVES, bool ALIGNED>
+// Scale bytes of R operand rows, staged by direct 4-byte loads in groups of G steps of 256
+// depth elements (8 bytes a step): every line that a load touches is a request to L2, as
+// dear as one for 64 bytes of codes, and 8 bytes a row and step were as many requests as
+// the codes' (16384 rows by 4096 x 7168 over 16 experts: 395 us, all of it the loads').
+// ALIGNED: a row's bytes begin at a multiple of 4, as they do where the depth is a multiple
+// of 128 and the array is 4-byte aligned.  Else they are loaded from the dword that holds
+// the first one on (none that holds no byte of the row), and the row's shift into it is
+// added when they are read.
+template <int R, int WAVES, int G, bool ALIGNED>
 struct ScaleTile {
-  static constexpr int kWords = ALIGNED ? 2 : 4;  // dwords of LDS a row
-  static constexpr int kBytes = R * kWords * 4;
+  static constexpr int kWords = 2 * G + (ALIGNED ? 0 : 1);  // dwords of LDS a row
+  static constexpr int kBytes = (R * kWords * 4 + 15) / 16 * 16;
   static constexpr int kPerWave = R * kWords / WAVES;
   static constexpr int kLoads = (kPerWave + 63) / 64;
-  static_assert(R * kWords % WAVES == 0 && (kPerWave % 64 == 0 || kPerWave < 64), "equal loads for all waves");
-  uint32_t off[kLoads];  // byte offset of each of this lane's dwords in step 0, or kNoFetch
+  static_assert(R * kWords % WAVES == 0, "equal loads for all waves");
+  uint32_t off[kLoads];  // byte offset of each of this lane's dwords in group 0, or kNoFetch
   int end[kLoads];       // bytes from there to the end of its row
-  bool mine;             // a wave with fewer than 64 dwords leaves the other lanes out
 
   // `lead`: bytes from the resource's (aligned) base to row 0; `row_of(r)`: the row of the
   // array that operand row r is, or -1; `S` bytes a row.
   template <typename F>
   __device__ __forceinline__ void init(int wave, int lane, int lead, int S, F row_of) {
-    mine = kPerWave >= 64 || lane < kPerWave;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int d = wave * kPerWave + i * 64 + lane, r = row_of(d / kWords), w = d % kWords;
-      const int begin = lead + r * S;
-      off[i] = r < 0 ? kNoFetch : (uint32_t)((begin & ~3) + w * 4);
-      end[i] = begin + S - ((begin & ~3) + w * 4);
-      if (!ALIGNED && w == 3) off[i] = kNoFetch;
+      const int begin = lead + r * S, at = (begin & ~3) + w * 4;
+      off[i] = r < 0 ? kNoFetch : (uint32_t)at;
+      end[i] = begin + S - at;
     }
   }
-  // Fills `lds` with the bytes of step s.
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* lds, int wave, int s) const {
-    if (!mine) return;
+  // Fills `lds` with the bytes of group g.
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* lds, int wave, int lane, int g) const {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (wave * kPerWave + i * 64) * 4), 4,
-                                               s * 8 < end[i] ? off[i] : kNoFetch, s * 8, 0, 0);
+      if (i * 64 + 64 <= kPerWave || i * 64 + lane < kPerWave)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (wave * kPerWave + i * 64) * 4), 4,
+                                                 g * G * 8 < end[i] ? off[i] : kNoFetch, g * G * 8, 0, 0);
   }
-  // The bytes of blocks 2 q and 2 q + 1 (q = l / 16) for operand row r0 + l % 16, the first
-  // in the lowest byte; `left`: blocks from this step's first to the row's last, past which
-  // the codes are zeros and the byte must not be a NaN's.
-  __device__ static __forceinline__ uint32_t pair(const char* lds, int r0, int lead, int S, int lane, int left) {
-    const int r = r0 + (lane & 15), q = lane >> 4;
+  // Where lane l finds the bytes of blocks 2 q and 2 q + 1 (q = l / 16) of operand row l % 16
+  // in step 0 of a group; the same for row r0 + l % 16, r0 a multiple of 16, r0 kRow on.
+  static constexpr int kRow = kWords * 4;
+  __device__ static __forceinline__ int lane_at(int lane, int lead, int S) {
+    const int r = lane & 15;
+    return r * kRow + (lane >> 4) * 2 + (ALIGNED ? 0 : (lead + r * S) & 3);
+  }
+  // The two bytes at p, the first in the lowest; `left`: blocks from there to the row's last,
+  // past which the codes are zeros and the byte must not be a NaN's.
+  __device__ static __forceinline__ uint32_t pair(const char* p, int left) {
     if constexpr (ALIGNED) {
-      return *reinterpret_cast<const uint16_t*>(lds + r * 8 + q * 2);
+      return *reinterpret_cast<const uint16_t*>(p);
     } else {
-      const uint8_t* p = reinterpret_cast<const uint8_t*>(lds) + r * 16 + ((lead + r * S) & 3) + q * 2;
-      const uint32_t lo = p[0], hi = p[1];
-      return (2 * q < left ? lo : 0u) | (2 * q + 1 < left ? hi << 8 : 0u);
+      const uint32_t lo = *reinterpret_cast<const uint8_t*>(p), hi = *reinterpret_cast<const uint8_t*>(p + 1);
+      return (0 < left ? lo : 0u) | (1 < left ? hi << 8 : 0u);
     }
   }
 };
@@ -173,10 +187,10 @@ __device__ __forceinline__ void finish(const MxLinearArgs& a, int e, int64_t fir
 }
 
 // MXFP4 rows: a workgroup's tile is BQ rows by BP weight rows (SwiGLU: BP / 2 of the gate
-// and the same BP / 2 of the up weight), WQ x WP waves, stages of 256 depth elements: 128
-// bytes of codes and 8 of scales a row.  Lane l takes blocks 2 (l / 16) and 2 (l / 16) + 1
-// of a stage, one for each of its two products.
-template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES>
+// and the same BP / 2 of the up weight), WQ x WP waves, STAGES stages of 256 depth elements,
+// 128 bytes of codes a row, and two groups of G steps' scale bytes.  Lane l takes blocks
+// 2 (l / 16) and 2 (l / 16) + 1 of a stage, one for each of its two halves.
+template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES, int G>
 struct Rows4 {
   static constexpr int kWaves = WQ * WP, kThreads = kWaves * 64;
   static constexpr int kParts = GATED ? 2 : 1;
@@ -184,18 +198,19 @@ struct Rows4 {
   static constexpr int kQ = BQ / WQ / 16, kP = BP / WP / 16, kC = kP / kParts;
   using QTile = RowTile<BQ, kWaves>;
   using PTile = RowTile<kCols, kWaves>;
-  using QScale = ScaleTile<BQ, kWaves, ALIGNED>;
-  using PScale = ScaleTile<kCols, kWaves, ALIGNED>;
-  static constexpr int kPOff = QTile::kBytes, kQSOff = kPOff + kParts * PTile::kBytes, kPSOff = kQSOff + QScale::kBytes;
-  static constexpr int kStage = kPSOff + kParts * PScale::kBytes;
-  static constexpr int kLoads = QTile::kLoads + QScale::kLoads + kParts * (PTile::kLoads + PScale::kLoads);
-  static constexpr int kLds = STAGES * kStage;
+  using QScale = ScaleTile<BQ, kWaves, G, ALIGNED>;
+  using PScale = ScaleTile<kCols, kWaves, G, ALIGNED>;
+  static constexpr int kStage = QTile::kBytes + kParts * PTile::kBytes;
+  static constexpr int kGroup = QScale::kBytes + kParts * PScale::kBytes;
+  static constexpr int kLoads = QTile::kLoads + kParts * PTile::kLoads;  // of codes
+  static constexpr int kLds = STAGES * kStage + 2 * kGroup;
   static_assert(BQ * kCols * 2 <= kLds, "the output tile fits where the stages were");
+  static_assert(G >= 2, "a group's loads are waited for at a meeting before it is read");
 };
 
-template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES>
+template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES, int G>
 __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_rows4_kernel(MxLinearArgs a) {
-  using T = Rows4<GATED, ALIGNED, BQ, BP, WQ, WP, STAGES>;
+  using T = Rows4<GATED, ALIGNED, BQ, BP, WQ, WP, STAGES, G>;
   constexpr int kQ = T::kQ, kP = T::kP, kC = T::kC, kParts = T::kParts, kCols = T::kCols;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wq = wave / WP, wp = wave % WP;
@@ -230,93 +245,111 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_rows4_kernel(MxLinearAr
 #pragma unroll
   for (int h = 0; h < kParts; ++h) ps[h].init(wave, lane, wlead[h], S, [&](int r) { return r < wlive ? r : -1; });
   const int steps = (ld + kDB - 1) / kDB;
+  char* const groups = smem + STAGES * T::kStage;
   // past the last step nothing is left: the loads are issued and fetch nothing
+  auto issue_scales = [&](int g) {
+    char* b = groups + (g & 1) * T::kGroup;
+    qs.load(rxs, b, wave, lane, g);
+#pragma unroll
+    for (int h = 0; h < kParts; ++h) ps[h].load(rws[h], b + T::QScale::kBytes + h * T::PScale::kBytes, wave, lane, g);
+  };
   auto issue = [&](int s, int stage) {
     char* b = smem + stage * T::kStage;
-    qs.load(rxs, b + T::kQSOff, wave, s);
-    if constexpr (STAGES == 2)
-      qt.load_live(rx, b, wave, s * kDB, ld - s * kDB, live);
-    else  // the waits count on every load
-      qt.load(rx, b, wave, s * kDB, ld - s * kDB);
+    qt.load(rx, b, wave, s * kDB, ld - s * kDB);
 #pragma unroll
-    for (int h = 0; h < kParts; ++h) {
-      ps[h].load(rws[h], b + T::kPSOff + h * T::PScale::kBytes, wave, s);
-      pt.load(rw[h], b + T::kPOff + h * T::PTile::kBytes, wave, s * kDB, ld - s * kDB);
-    }
+    for (int h = 0; h < kParts; ++h)
+      pt.load(rw[h], b + T::QTile::kBytes + h * T::PTile::kBytes, wave, s * kDB, ld - s * kDB);
   };
   f32x4 acc[kQ][kP];
 #pragma unroll
   for (int i = 0; i < kQ; ++i)
 #pragma unroll
     for (int j = 0; j < kP; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  issue_scales(0);
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) issue(s, s);
 
-  auto p_row = [&](int j) { return wp * (kCols / WP) + (j % kC) * 16; };
+  // A step is 2 L units: row subtile u % L times all column subtiles, first of the stage's
+  // lower halves, then of the upper ones.  A unit's rows are read kAhead units before it,
+  // into a ring of as many and one, the columns' other half beside the first unit; once the
+  // last rows are read the waves meet, the stage is filled again, and the rest of the units
+  // run beside the first reads of the next stage.
   auto multiply = [&](auto live_subtiles) {
-    constexpr int L = decltype(live_subtiles)::value;
-    constexpr int kNext = (STAGES - 2) * T::kLoads;
+    constexpr int L = decltype(live_subtiles)::value, kUnits = 2 * L;
+    constexpr int kRing = L >= 4 ? 4 : L == 3 ? 3 : 2, kAhead = kRing - 1, kMeet = kUnits - kAhead;
+    static_assert(kUnits % kRing == 0 && kMeet >= L, "units keep their places; the lower halves are done at the meeting");
     int stage = 0;
-    uint4 q[2][L], p[2][kP];
+    u32x4 q[kRing], p[2][kP];
     // scales of this step and of the next, those of two subtiles in a register
     constexpr int kSq = (L + 1) / 2, kSp = (kP + 1) / 2;
     uint32_t sq[kSq], sp[kSp], nq[kSq], np[kSp];
-    auto piece = [&](const char* b, int r0, int k) {
-      return *reinterpret_cast<const uint4*>(T::QTile::at(b, r0 + (lane & 15), 2 * (lane >> 4) + k));
+    // Lane l reads the pieces 2 (l / 16) + k of line l % 16 of a subtile; a line's swizzle
+    // repeats every 16 lines, so one offset a half serves all subtiles.  (As a vector, not a
+    // uint4: of a struct the compiler loses the type, takes the read to depend on every
+    // direct load and waits for the one just issued.)
+    int at[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) at[k] = (lane & 15) * kDB + ((2 * (lane >> 4) + k) ^ T::QTile::swz(lane & 15)) * 16;
+    const int sx_at = T::QScale::lane_at(lane, xlead, S) + wq * 16 * T::QScale::kRow;
+    int sw_at[kParts];
+#pragma unroll
+    for (int h = 0; h < kParts; ++h)
+      sw_at[h] = T::PScale::lane_at(lane, wlead[h], S) + wp * (kCols / WP) * T::PScale::kRow + T::QScale::kBytes + h * T::PScale::kBytes;
+    auto read_q = [&](int u) {
+      const char* b = smem + stage * T::kStage + wq * 16 * kDB + at[u / L];
+      q[u % kRing] = *reinterpret_cast<const u32x4*>(b + u % L * WQ * 16 * kDB);
     };
-    auto read = [&](int k) {
-      const char* b = smem + stage * T::kStage;
+    auto read_p = [&](int k) {
+      const char* b = smem + stage * T::kStage + T::QTile::kBytes + wp * (kCols / WP) * kDB + at[k];
 #pragma unroll
-      for (int i = 0; i < L; ++i) q[k][i] = piece(b, q_row<WQ>(wq, i), k);
-#pragma unroll
-      for (int j = 0; j < kP; ++j) p[k][j] = piece(b + T::kPOff + j / kC * T::PTile::kBytes, p_row(j), k);
+      for (int j = 0; j < kP; ++j) p[k][j] = *reinterpret_cast<const u32x4*>(b + j / kC * T::PTile::kBytes + j % kC * 16 * kDB);
     };
     auto read_scales = [&](int s) {
-      const char* b = smem + stage * T::kStage;
-      const int left = S - s * 8;
-      auto of_q = [&](int i) { return T::QScale::pair(b + T::kQSOff, q_row<WQ>(wq, i), xlead, S, lane, left); };
-      auto of_p = [&](int j) {
-        return T::PScale::pair(b + T::kPSOff + j / kC * T::PScale::kBytes, p_row(j), wlead[j / kC], S, lane, left);
-      };
+      const char* b = groups + (s / G & 1) * T::kGroup + s % G * 8;
+      const int left = S - s * 8 - 2 * (lane >> 4);
+      auto of_q = [&](int i) { return T::QScale::pair(b + sx_at + i * WQ * 16 * T::QScale::kRow, left); };
+      auto of_p = [&](int j) { return T::PScale::pair(b + sw_at[j / kC] + j % kC * 16 * T::PScale::kRow, left); };
 #pragma unroll
       for (int i = 0; i < kSq; ++i) nq[i] = of_q(2 * i) | (2 * i + 1 < L ? of_q(2 * i + 1) << 16 : 0u);
 #pragma unroll
       for (int j = 0; j < kSp; ++j) np[j] = of_p(2 * j) | (2 * j + 1 < kP ? of_p(2 * j + 1) << 16 : 0u);
     };
-    auto products = [&](auto half) {
-      constexpr int H = decltype(half)::value;
+    auto unit = [&](auto index) {
+      constexpr int u = decltype(index)::value, i = u % L, H = u / L, O = H + 2 * (i & 1);
 #pragma unroll
       for (int j = 0; j < kP; ++j)
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-          if (j % 2 == 0 && i % 2 == 0) acc[i][j] = mx::mfma<H, H>(p[H][j], sp[j / 2], q[H][i], sq[i / 2], acc[i][j]);
-          if (j % 2 == 0 && i % 2 == 1) acc[i][j] = mx::mfma<H, H + 2>(p[H][j], sp[j / 2], q[H][i], sq[i / 2], acc[i][j]);
-          if (j % 2 == 1 && i % 2 == 0) acc[i][j] = mx::mfma<H + 2, H>(p[H][j], sp[j / 2], q[H][i], sq[i / 2], acc[i][j]);
-          if (j % 2 == 1 && i % 2 == 1) acc[i][j] = mx::mfma<H + 2, H + 2>(p[H][j], sp[j / 2], q[H][i], sq[i / 2], acc[i][j]);
-        }
+        acc[i][j] = j & 1 ? mx::mfma<H + 2, O>(p[H][j], sp[j / 2], q[u % kRing], sq[i / 2], acc[i][j])
+                          : mx::mfma<H, O>(p[H][j], sp[j / 2], q[u % kRing], sq[i / 2], acc[i][j]);
     };
-    // loads behind the first stage's; with two stages those of rows depend on the rows, so
-    // they are not counted on
-    wait_and_meet<(STAGES - 1) * (T::kLoads - (STAGES == 2 ? T::QTile::kLoads : 0))>();
-    read(0);
+    wait_and_meet<(STAGES - 1) * T::kLoads>();
+    read_p(0);
     read_scales(0);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) read_q(u);
     for (int s = 0; s < steps; ++s) {
+      // the next group: the last bytes of the one before this, whose place it takes, were
+      // read before the meeting of step s - 1 (a branch behind the meeting would draw the
+      // products in front of it into its far side)
+      if (s % G == 0) issue_scales(s / G + 1);
 #pragma unroll
       for (int i = 0; i < kSq; ++i) sq[i] = nq[i];
 #pragma unroll
       for (int j = 0; j < kSp; ++j) sp[j] = np[j];
-      read(1);
-      __builtin_amdgcn_sched_barrier(0);  // the reads are on their way before the products
-      products(Count<0>{});
-      __builtin_amdgcn_sched_barrier(0);
-      wait_and_meet<kNext>();  // this step's operands are in registers, the next stage has landed
-      issue(s + STAGES, stage);
-      stage = stage == STAGES - 1 ? 0 : stage + 1;
-      read(0);  // of step s + 1; past the last one whatever lies there, unused
-      read_scales(s + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      products(Count<1>{});
-      __builtin_amdgcn_sched_barrier(0);
+      each<kUnits>([&](auto index) {
+        constexpr int u = decltype(index)::value;
+        if constexpr (u == kMeet) {
+          wait_and_meet<(STAGES - 2) * T::kLoads>();  // this step's operands are in registers, the next stage has landed
+          issue(s + STAGES, stage);
+          stage = stage == STAGES - 1 ? 0 : stage + 1;
+          read_p(0);  // of step s + 1; past the last one whatever lies there, unused
+          read_scales(s + 1);
+        }
+        read_q(u < kMeet ? u + kAhead : u - kMeet);
+        if constexpr (u == 0) read_p(1);
+        __builtin_amdgcn_sched_barrier(0);  // the reads are on their way before the products
+        unit(index);
+        __builtin_amdgcn_sched_barrier(0);
+      });
     }
   };
   by_live_subtiles<kQ>((live - wq * 16 + 16 * WQ - 1) / (16 * WQ), multiply);
@@ -385,7 +418,7 @@ __global__ __launch_bounds__(WC* WK * 64) void linear_mx_few_kernel(MxLinearArgs
           xb = mx::kZeroByte;
         }
 #pragma unroll
-        for (int h = 0; h < kParts; ++h) acc[h] = mx::mfma<0, 0>(wv[h], wb[h], xv, xb, acc[h]);
+        for (int h = 0; h < kParts; ++h) acc[h] = mx::mfma<0, 0>(as_vec(wv[h]), wb[h], as_vec(xv), xb, acc[h]);
       } else {
         uint4 xv[4];
 #pragma unroll
@@ -574,9 +607,9 @@ MOE_MX_TILES(true, false)
 MOE_MX_TILES(true, true)
 #undef MOE_MX_TILES
 #define MOE_MX_ROWS4(G, A)                                                    \
-  template __global__ void linear_rows4_kernel<G, A, 256, 256, 2, 4, 2>(MxLinearArgs); \
-  template __global__ void linear_rows4_kernel<G, A, 128, 128, 2, 2, 2>(MxLinearArgs); \
-  template __global__ void linear_rows4_kernel<G, A, 64, 64, G ? 4 : 2, G ? 1 : 2, 3>(MxLinearArgs);
+  template __global__ void linear_rows4_kernel<G, A, 256, 256, 2, 4, 2, 2>(MxLinearArgs); \
+  template __global__ void linear_rows4_kernel<G, A, 128, 128, 2, 2, 2, 4>(MxLinearArgs); \
+  template __global__ void linear_rows4_kernel<G, A, 64, 64, G ? 4 : 2, G ? 1 : 2, 3, 4>(MxLinearArgs);
 MOE_MX_ROWS4(false, false)
 MOE_MX_ROWS4(false, true)
 MOE_MX_ROWS4(true, false)
@@ -600,12 +633,12 @@ hipError_t run_few(const MxLinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES>
+template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES, int G>
 hipError_t run_rows4(const MxLinearArgs& a, hipStream_t s) {
-  using T = Rows4<GATED, ALIGNED, BQ, BP, WQ, WP, STAGES>;
+  using T = Rows4<GATED, ALIGNED, BQ, BP, WQ, WP, STAGES, G>;
   static std::atomic<size_t> allowed[kMaxCachedDevices];
   const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, BQ) * ((a.N + T::kCols - 1) / T::kCols);
-  void (*const kern)(MxLinearArgs) = &linear_rows4_kernel<GATED, ALIGNED, BQ, BP, WQ, WP, STAGES>;
+  void (*const kern)(MxLinearArgs) = &linear_rows4_kernel<GATED, ALIGNED, BQ, BP, WQ, WP, STAGES, G>;
   return launch(kern, items, T::kThreads, T::kLds, a, s, allowed);
 }
 
@@ -627,9 +660,9 @@ template <bool GATED, bool ALIGNED>
 hipError_t rows4_by_shape(const MxLinearArgs& a, hipStream_t s) {
   if (mean_rows(a) <= kFewRows) return run_few<true, GATED, 2, 8>(a, s);
   const int64_t cols = a.parts * (int64_t)a.N;
-  if (tiles(a, cols, 128) < 256) return run_rows4<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2, 3>(a, s);
-  if (wide_tiles(a, cols)) return run_rows4<GATED, ALIGNED, 256, 256, 2, 4, 2>(a, s);
-  return run_rows4<GATED, ALIGNED, 128, 128, 2, 2, 2>(a, s);
+  if (tiles(a, cols, 128) < 256) return run_rows4<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2, 3, 4>(a, s);
+  if (wide_tiles(a, cols)) return run_rows4<GATED, ALIGNED, 256, 256, 2, 4, 2, 2>(a, s);
+  return run_rows4<GATED, ALIGNED, 128, 128, 2, 2, 2, 4>(a, s);
 }
 
 template <int BQ, int BP, int WQ, int WP>

@@ -55,9 +55,10 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t byte) {
 // 6e-8 of the sum of absolute products, with scales 2^20 apart: float32 sums, unlike the
 // e4m3 form's.
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <int OPA, int OPB>
-__device__ __forceinline__ mma::f32x4 mfma(uint4 a, uint32_t sa, uint4 b, uint32_t sb, mma::f32x4 c) {
-  const i32x8 av{(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0}, bv{(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+__device__ __forceinline__ mma::f32x4 mfma(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, mma::f32x4 c) {
+  const i32x8 av{(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0}, bv{(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, OPA, (int)sa, OPB, (int)sb);
 }
 
