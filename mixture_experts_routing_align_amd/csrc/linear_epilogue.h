@@ -27,10 +27,8 @@ __device__ __forceinline__ float sigmoid(float x) {
 // The same for any x: past 87 on either side (and at the infinities) the correction
 // would meet an infinity, and float32's normal range has only 0 and 1 there.
 __device__ __forceinline__ float sigmoid_all(float x) { return x > 87.0f ? 1.0f : x < -87.0f ? 0.0f : sigmoid(x); }
-__device__ __forceinline__ float silu(float z) { return z * sigmoid_all(z); }
 // the tanh form of gelu: z/2 (1 + tanh(a)) = z sigmoid(2 a), a = sqrt(2/pi) (z + 0.044715 z^3)
 __device__ __forceinline__ float gelu_2a(float z) { return 1.5957691216057308f * fmaf(0.044715f * z * z, z, z); }
-__device__ __forceinline__ float gelu(float z) { return z * sigmoid_all(gelu_2a(z)); }
 
 __device__ __forceinline__ void unpack4(uint2 v, float (&f)[4]) {
   f[0] = row::bf16_lo(v.x);
@@ -40,43 +38,54 @@ __device__ __forceinline__ void unpack4(uint2 v, float (&f)[4]) {
 }
 __device__ __forceinline__ uint2 pack4(const float (&f)[4]) { return make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])); }
 
+// 1 / (1 + exp(-x)) without the remainder of x log2(e), whose rounding costs |x| 2^-24 of the
+// result where the exponential dominates: for epilogues that round to 8 bits or fewer and are
+// bound by their arithmetic.  The infinities need no care: the exponential is 0 or an
+// infinity there, as it is past 89.
+__device__ __forceinline__ float sigmoid_short(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
+}
+
+// act(z[, u]) of 4 elements.
+template <bool GATED, bool SHORT = false>
+__device__ __forceinline__ void act4(int act, const float (&z)[4], const float (&u)[4], float (&y)[4]) {
+  auto gate = [](float x) { return SHORT ? sigmoid_short(x) : sigmoid_all(x); };
+  if constexpr (GATED) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = z[c] * gate(z[c]) * u[c];
+  } else {
+    if (act == MOE_ACT_SILU) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c] = z[c] * gate(z[c]);
+    } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c] = z[c] * gate(gelu_2a(z[c]));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c] = z[c];
+    }
+  }
+}
+
+// v += 4 packed bf16 values.
+__device__ __forceinline__ void add4(float (&v)[4], uint2 packed) {
+  float f[4];
+  unpack4(packed, f);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v[c] += f[c];
+}
+
 // 4 consecutive columns n ... n + 3 of row r of expert e: bias, activation and
 // residual on float32 sums; z and u come back as the pre-activations.  `in`: the
 // columns and the row exist.
 template <bool GATED>
 __device__ __forceinline__ void epilogue4(const LinearArgs& a, int e, int64_t r, int n, bool in, float (&z)[4], float (&u)[4],
                                           float (&y)[4]) {
-  float f[4];
-  if (a.bias[0] != nullptr && in) {
-    unpack4(*reinterpret_cast<const uint2*>(a.bias[0] + (int64_t)e * a.N + n), f);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) z[c] += f[c];
-  }
-  if constexpr (GATED) {
-    if (a.bias[1] != nullptr && in) {
-      unpack4(*reinterpret_cast<const uint2*>(a.bias[1] + (int64_t)e * a.N + n), f);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) u[c] += f[c];
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = silu(z[c]) * u[c];
-  } else {
-    if (a.act == MOE_ACT_SILU) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) y[c] = silu(z[c]);
-    } else if (a.act == MOE_ACT_GELU) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) y[c] = gelu(z[c]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) y[c] = z[c];
-    }
-  }
-  if (a.residual != nullptr && in) {
-    unpack4(*reinterpret_cast<const uint2*>(a.residual + r * a.N + n), f);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] += f[c];
-  }
+  if (a.bias[0] != nullptr && in) add4(z, *reinterpret_cast<const uint2*>(a.bias[0] + (int64_t)e * a.N + n));
+  if constexpr (GATED)
+    if (a.bias[1] != nullptr && in) add4(u, *reinterpret_cast<const uint2*>(a.bias[1] + (int64_t)e * a.N + n));
+  act4<GATED>(a.act, z, u, y);
+  if (a.residual != nullptr && in) add4(y, *reinterpret_cast<const uint2*>(a.residual + r * a.N + n));
 }
 
 // Calls f with the smallest of kQ / 4, kQ / 2, 3 kQ / 4 and kQ subtiles that covers `live`.

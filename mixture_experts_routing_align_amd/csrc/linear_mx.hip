@@ -28,6 +28,8 @@ using namespace epilogue;
 
 extern __shared__ __attribute__((aligned(1024))) char smem[];
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 __device__ __forceinline__ u32x4 as_vec(uint4 v) { return u32x4{v.x, v.y, v.z, v.w}; }
 
 // Calls f with 0, 1, ... N - 1, each a constant.
@@ -49,13 +51,16 @@ __device__ __forceinline__ void each(F f) {
 // of 128 and the array is 4-byte aligned.  Else they are loaded from the dword that holds
 // the first one on (none that holds no byte of the row), and the row's shift into it is
 // added when they are read.
+//
+// The dwords are dealt to the waves 64 at a time; no lane is left out of a load, since a load
+// behind a branch that lanes take differently may be merged with another one's, whose place
+// in LDS is then taken for both.
 template <int R, int WAVES, int G, bool ALIGNED>
 struct ScaleTile {
   static constexpr int kWords = 2 * G + (ALIGNED ? 0 : 1);  // dwords of LDS a row
-  static constexpr int kBytes = (R * kWords * 4 + 15) / 16 * 16;
-  static constexpr int kPerWave = R * kWords / WAVES;
-  static constexpr int kLoads = (kPerWave + 63) / 64;
-  static_assert(R * kWords % WAVES == 0, "equal loads for all waves");
+  static constexpr int kPieces = (R * kWords + 63) / 64;    // loads of a wave in all
+  static constexpr int kBytes = kPieces * 256;
+  static constexpr int kLoads = (kPieces + WAVES - 1) / WAVES;
   uint32_t off[kLoads];  // byte offset of each of this lane's dwords in group 0, or kNoFetch
   int end[kLoads];       // bytes from there to the end of its row
 
@@ -65,26 +70,28 @@ struct ScaleTile {
   __device__ __forceinline__ void init(int wave, int lane, int lead, int S, F row_of) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int d = wave * kPerWave + i * 64 + lane, r = row_of(d / kWords), w = d % kWords;
+      const int d = (i * WAVES + wave) * 64 + lane, r = d < R * kWords ? row_of(d / kWords) : -1, w = d % kWords;
       const int begin = lead + r * S, at = (begin & ~3) + w * 4;
       off[i] = r < 0 ? kNoFetch : (uint32_t)at;
       end[i] = begin + S - at;
     }
   }
   // Fills `lds` with the bytes of group g.
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* lds, int wave, int lane, int g) const {
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* lds, int wave, int g) const {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      if (i * 64 + 64 <= kPerWave || i * 64 + lane < kPerWave)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (wave * kPerWave + i * 64) * 4), 4,
+      if ((i + 1) * WAVES <= kPieces || i * WAVES + wave < kPieces)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (i * WAVES + wave) * 256), 4,
                                                  g * G * 8 < end[i] ? off[i] : kNoFetch, g * G * 8, 0, 0);
   }
   // Where lane l finds the bytes of blocks 2 q and 2 q + 1 (q = l / 16) of operand row l % 16
   // in step 0 of a group; the same for row r0 + l % 16, r0 a multiple of 16, r0 kRow on.
   static constexpr int kRow = kWords * 4;
-  __device__ static __forceinline__ int lane_at(int lane, int lead, int S) {
+  __device__ static __forceinline__ int lane_at(int lane, int lead, int S) { return row_at(lane, lead, S) + (lane >> 4) * 2; }
+  // And the row's first byte.
+  __device__ static __forceinline__ int row_at(int lane, int lead, int S) {
     const int r = lane & 15;
-    return r * kRow + (lane >> 4) * 2 + (ALIGNED ? 0 : (lead + r * S) & 3);
+    return r * kRow + (ALIGNED ? 0 : (lead + r * S) & 3);
   }
   // The two bytes at p, the first in the lowest; `left`: blocks from there to the row's last,
   // past which the codes are zeros and the byte must not be a NaN's.
@@ -98,217 +105,264 @@ struct ScaleTile {
   }
 };
 
+// What a tile of the forward products is made of: BQ rows by BP weight rows (SwiGLU: BP / 2
+// of the gate and the same BP / 2 of the up weight, so that a lane holds z and u of its
+// elements), WQ x WP waves.
+template <bool GATED, int BQ_, int BP, int WQ_, int WP_>
+struct Shape {
+  static constexpr bool kGated = GATED;
+  static constexpr int BQ = BQ_, WQ = WQ_, WP = WP_;
+  static constexpr int kWaves = WQ * WP, kThreads = kWaves * 64;
+  static constexpr int kParts = GATED ? 2 : 1;
+  static constexpr int kCols = BP / kParts;                // output columns of a tile
+  static constexpr int kWaveCols = kCols / WP;             // and of a wave
+  static constexpr int kQ = BQ / WQ / 16, kP = BP / WP / 16, kC = kP / kParts;
+  static_assert(kC % 2 == 0, "a wave holds whole scale blocks of its rows' columns");
+};
+
+// Rows below `live` of the 16 rows of BYTES that a wave has gathered at `lds`, their first
+// `valid` bytes (a multiple of 16), to dst; ld bytes from row to row.
+template <int BYTES>
+__device__ __forceinline__ void flush16(const char* lds, char* dst, int64_t ld, int live, int valid) {
+  using Rows = OutTile<16, BYTES, 64>;
+  const int lane = threadIdx.x & 63;
+  asm volatile("" ::: "memory");  // a wave's LDS operations are done in order
+#pragma unroll
+  for (int i = 0; i < 16 * Rows::kPieces; i += 64) {
+    const int r = (i + lane) / Rows::kPieces, g = (i + lane) % Rows::kPieces;
+    if (r < min(live, 16) && g * 16 < valid)
+      *reinterpret_cast<u32x4*>(dst + r * ld + g * 16) = *reinterpret_cast<const u32x4*>(lds + r * BYTES + ((g ^ (r & Rows::kMask)) << 4));
+  }
+  asm volatile("" ::: "memory");
+}
+
 // The end of a tile: bias, activation and residual on the float32 sums, pre-activations,
 // bf16 or MXFP4 rows.  Lane l holds row l % 16 and 4 consecutive columns of each subtile,
 // acc[i][j] of a wave's row subtiles i and its columns' subtiles j (SwiGLU: kC of z, then kC
-// of u).  LDS is free.
-template <bool GATED, int BQ, int kCols, int WQ, int WP, int kQ, int kC>
-__device__ __forceinline__ void finish(const MxLinearArgs& a, int e, int64_t first, int live, int p0, int wq, int wp,
-                                       f32x4 (&acc)[kQ][GATED ? 2 * kC : kC]) {
-  constexpr int kParts = GATED ? 2 : 1, kThreads = WQ * WP * 64;
-  static_assert(kC % 2 == 0, "a wave holds whole scale blocks of its rows' columns");
-  const int lane = threadIdx.x & 63, quad = lane >> 4, row16 = lane & 15;
-  const int colw = wp * (kCols / WP) + quad * 4;  // this lane's first column of the tile
-  const int cols = min(kCols, a.N - p0);
-  using Rows = OutTile<BQ, kCols * 2, kThreads>;
-  auto columns = [&](auto f) {  // f(subtile row i, subtile column j, tile row, tile column)
-#pragma unroll
-    for (int i = 0; i < kQ; ++i)
-#pragma unroll
-      for (int j = 0; j < kC; ++j) f(i, j, q_row<WQ>(wq, i) + row16, colw + j * 16);
-  };
-  // act(z, u) + residual in place of z; the pre-activations, where they are kept,
-  // need the bias on both
-  columns([&](int i, int j, int m, int n) {
-    float z[4], u[4], y[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      z[c] = acc[i][j][c];
-      u[c] = acc[i][(GATED ? kC : 0) + j][c];
-    }
-    epilogue4<GATED>(a, e, first + m, p0 + n, m < live && n < cols, z, u, y);
-    if (a.preact != nullptr) {
-      Rows::put(smem, m, n * 2, pack4(z));
-      if (GATED) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][kC + j][c] = u[c];
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[i][j][c] = y[c];
-  });
-  if (a.preact != nullptr) {
-    char* pre = reinterpret_cast<char*>(a.preact + first * kParts * a.N + p0);
-    __syncthreads();
-    Rows::flush(smem, pre, (int64_t)kParts * a.N * 2, live, cols * 2);
-    __syncthreads();
-    if constexpr (GATED) {
-      columns([&](int i, int j, int m, int n) {
-        const float u[4] = {acc[i][kC + j][0], acc[i][kC + j][1], acc[i][kC + j][2], acc[i][kC + j][3]};
-        Rows::put(smem, m, n * 2, pack4(u));
-      });
-      __syncthreads();
-      Rows::flush(smem, pre + (int64_t)a.N * 2, (int64_t)2 * a.N * 2, live, cols * 2);
-      __syncthreads();
-    }
-  }
-  if (a.ysb == nullptr) {
-    columns([&](int i, int j, int m, int n) {
-      const float y[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      Rows::put(smem, m, n * 2, pack4(y));
-    });
-    __syncthreads();
-    Rows::flush(smem, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + first * a.N + p0), (int64_t)a.N * 2, live, cols * 2);
-    return;
-  }
-  // a scale block is two subtiles over the four quads of one wave
-  using Codes = OutTile<BQ, kCols / 2, kThreads>;
-#pragma unroll
-  for (int i = 0; i < kQ; ++i) {
-    const int m = q_row<WQ>(wq, i) + row16;
-#pragma unroll
-    for (int j = 0; j < kC; j += 2) {
-      uint32_t mx = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) mx = max(mx, max(row::abs_bits(acc[i][j][c]), row::abs_bits(acc[i][j + 1][c])));
-      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16));
-      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
-      const uint32_t byte = mx::scale_byte(mx);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        Codes::put(smem, m, (colw + (j + h) * 16) / 2,
-                   (uint16_t)mx::codes4(acc[i][j + h][0], acc[i][j + h][1], acc[i][j + h][2], acc[i][j + h][3], byte));
-      const int n = wp * (kCols / WP) + j * 16;
-      if (quad == 0 && m < live && n < cols) a.ysb[(first + m) * (a.N / mx::kBlock) + (p0 + n) / mx::kBlock] = (uint8_t)byte;
-    }
-  }
-  __syncthreads();
-  Codes::flush(smem, static_cast<char*>(a.y) + (first * a.N + p0) / 2, a.N / 2, live, cols / 2);
-}
+// of u).  Every wave turns its own 16 rows at a time into lines in LDS of its own, so that
+// no wave waits for another here and the next tile's operands may be on their way.  The
+// bias and the first rows' residual are loaded in front of those (loads come back in
+// order), the other rows' ahead of the rows before them.
+template <class T>
+struct Finish {
+  int e, live, p0;
+  int64_t first;
+  uint2 bias[T::kParts][T::kC], residual[2][T::kC];
 
-// MXFP4 rows: a workgroup's tile is BQ rows by BP weight rows (SwiGLU: BP / 2 of the gate
-// and the same BP / 2 of the up weight), WQ x WP waves, STAGES stages of 256 depth elements,
-// 128 bytes of codes a row, and two groups of G steps' scale bytes.  Lane l takes blocks
-// 2 (l / 16) and 2 (l / 16) + 1 of a stage, one for each of its two halves.
-template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES, int G>
-struct Rows4 {
-  static constexpr int kWaves = WQ * WP, kThreads = kWaves * 64;
-  static constexpr int kParts = GATED ? 2 : 1;
-  static constexpr int kCols = BP / kParts;
-  static constexpr int kQ = BQ / WQ / 16, kP = BP / WP / 16, kC = kP / kParts;
-  using QTile = RowTile<BQ, kWaves>;
-  using PTile = RowTile<kCols, kWaves>;
-  using QScale = ScaleTile<BQ, kWaves, G, ALIGNED>;
-  using PScale = ScaleTile<kCols, kWaves, G, ALIGNED>;
-  static constexpr int kStage = QTile::kBytes + kParts * PTile::kBytes;
-  static constexpr int kGroup = QScale::kBytes + kParts * PScale::kBytes;
-  static constexpr int kLoads = QTile::kLoads + kParts * PTile::kLoads;  // of codes
-  static constexpr int kLds = STAGES * kStage + 2 * kGroup;
-  static_assert(BQ * kCols * 2 <= kLds, "the output tile fits where the stages were");
-  static_assert(G >= 2, "a group's loads are waited for at a meeting before it is read");
+  // Column subtile j's first column of this lane.
+  __device__ __forceinline__ int column(int wave, int j) const {
+    return p0 + wave % T::WP * T::kWaveCols + j * 16 + (int)(threadIdx.x & 63) / 16 * 4;
+  }
+  __device__ __forceinline__ void load_residual(const MxLinearArgs& a, int wave, int i) {
+    const int m = q_row<T::WQ>(wave / T::WP, i) + (int)(threadIdx.x & 15);
+#pragma unroll
+    for (int j = 0; j < T::kC; ++j) {
+      const int n = column(wave, j);
+      residual[i & 1][j] = make_uint2(0, 0);
+      if (m < live && n < a.N) residual[i & 1][j] = *reinterpret_cast<const uint2*>(a.residual + (first + m) * a.N + n);
+    }
+  }
+  __device__ __forceinline__ void load(const MxLinearArgs& a, int wave) {
+#pragma unroll
+    for (int h = 0; h < T::kParts; ++h)
+#pragma unroll
+      for (int j = 0; j < T::kC; ++j) {
+        const int n = column(wave, j);
+        bias[h][j] = make_uint2(0, 0);
+        if (a.bias[h] != nullptr && n < a.N) bias[h][j] = *reinterpret_cast<const uint2*>(a.bias[h] + (int64_t)e * a.N + n);
+      }
+    if (a.residual != nullptr) load_residual(a, wave, 0);
+  }
+  __device__ __forceinline__ void store(const MxLinearArgs& a, int wave, char* lds, f32x4 (&acc)[T::kQ][T::kP]);
 };
 
-template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES, int G>
-__global__ __launch_bounds__(WQ* WP * 64, 2) void linear_rows4_kernel(MxLinearArgs a) {
-  using T = Rows4<GATED, ALIGNED, BQ, BP, WQ, WP, STAGES, G>;
-  constexpr int kQ = T::kQ, kP = T::kP, kC = T::kC, kParts = T::kParts, kCols = T::kCols;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wq = wave / WP, wp = wave % WP;
-  const Item it = find_item(a, row::block_index(), BQ, (a.N + kCols - 1) / kCols);
-  if (it.e < 0) return;
-  const int ld = a.K / 2, S = a.K / mx::kBlock;
-  const int q0 = it.tq * BQ, p0 = it.tp * kCols;
-  const int live = min(BQ, it.count - q0);  // rows of this tile
-  const int64_t first = (int64_t)it.row0 + q0, wfirst = (int64_t)it.e * a.N + p0;
-  const int wlive = min(kCols, a.N - p0);
-  const __amdgpu_buffer_rsrc_t rx = resource(static_cast<const char*>(a.x) + first * ld);
-  // the scales' resources begin at the aligned dword that holds the tile's first byte
-  const uint8_t* const xs = a.xs + first * S;
-  const int xlead = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(xs) & 3);
-  const __amdgpu_buffer_rsrc_t rxs = resource(xs - xlead);
-  __amdgpu_buffer_rsrc_t rw[kParts], rws[kParts];
-  int wlead[kParts];
+template <class T>
+__device__ __forceinline__ void Finish<T>::store(const MxLinearArgs& a, int wave, char* lds, f32x4 (&acc)[T::kQ][T::kP]) {
+  constexpr int kC = T::kC;
+  const int wq = wave / T::WP, wp = wave % T::WP;
+  const int lane = threadIdx.x & 63, quad = lane >> 4, row16 = lane & 15;
+  constexpr int kO = T::kOutCols / 16;  // column subtiles gathered at a time
+  using Rows = OutTile<16, T::kOutCols * 2, 64>;
+  using Codes = OutTile<16, T::kOutCols / 2, 64>;
 #pragma unroll
-  for (int h = 0; h < kParts; ++h) {
-    rw[h] = resource(static_cast<const char*>(a.w[h]) + wfirst * ld);
-    const uint8_t* const ws = a.wsb[h] + wfirst * S;
-    wlead[h] = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(ws) & 3);
-    rws[h] = resource(ws - wlead[h]);
+  for (int i = 0; i < T::kQ; ++i) {
+    const int left = live - q_row<T::WQ>(wq, i);
+    if (left <= 0) break;
+    if (a.residual != nullptr && i + 1 < T::kQ) load_residual(a, wave, i + 1);
+    const int64_t r0 = first + q_row<T::WQ>(wq, i);
+#pragma unroll
+    for (int j0 = 0; j0 < kC; j0 += kO) {
+      const int n0 = p0 + wp * T::kWaveCols + j0 * 16, cols = min(T::kOutCols, a.N - n0);
+      if (cols <= 0) break;
+      float y[kO][4], u[kO][4];
+#pragma unroll
+      for (int j = 0; j < kO; ++j) {
+        const int n = j * 16 + quad * 4;
+        float z[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          z[c] = acc[i][j0 + j][c];
+          u[j][c] = acc[i][(T::kGated ? kC : 0) + j0 + j][c];
+        }
+        add4(z, bias[0][j0 + j]);
+        if constexpr (T::kGated) add4(u[j], bias[1][j0 + j]);
+        act4<T::kGated, true>(a.act, z, u[j], y[j]);
+        if (a.residual != nullptr) add4(y[j], residual[i & 1][j0 + j]);
+        if (a.preact != nullptr) Rows::put(lds, row16, n * 2, pack4(z));
+      }
+      if (a.preact != nullptr) {
+        char* pre = reinterpret_cast<char*>(a.preact + r0 * T::kParts * a.N + n0);
+        flush16<T::kOutCols * 2>(lds, pre, (int64_t)T::kParts * a.N * 2, left, cols * 2);
+        if constexpr (T::kGated) {
+#pragma unroll
+          for (int j = 0; j < kO; ++j) Rows::put(lds, row16, (j * 16 + quad * 4) * 2, pack4(u[j]));
+          flush16<T::kOutCols * 2>(lds, pre + (int64_t)a.N * 2, (int64_t)2 * a.N * 2, left, cols * 2);
+        }
+      }
+      if (a.ysb == nullptr) {
+#pragma unroll
+        for (int j = 0; j < kO; ++j) Rows::put(lds, row16, (j * 16 + quad * 4) * 2, pack4(y[j]));
+        flush16<T::kOutCols * 2>(lds, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + r0 * a.N + n0), (int64_t)a.N * 2, left,
+                                 cols * 2);
+        continue;
+      }
+      // a scale block is two subtiles over the four quads
+#pragma unroll
+      for (int j = 0; j < kO; j += 2) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx = max(mx, max(row::abs_bits(y[j][c]), row::abs_bits(y[j + 1][c])));
+        mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16));
+        mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
+        const uint32_t byte = mx::scale_byte(mx);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          Codes::put(lds, row16, ((j + h) * 16 + quad * 4) / 2, (uint16_t)mx::codes4(y[j + h][0], y[j + h][1], y[j + h][2], y[j + h][3], byte));
+        if (quad == 0 && row16 < left && j * 16 < cols)
+          a.ysb[(r0 + row16) * (a.N / mx::kBlock) + (n0 + j * 16) / mx::kBlock] = (uint8_t)byte;
+      }
+      flush16<T::kOutCols / 2>(lds, static_cast<char*>(a.y) + (r0 * a.N + n0) / 2, a.N / 2, left, cols / 2);
+    }
   }
-  typename T::QTile qt;
-  typename T::PTile pt;
-  typename T::QScale qs;
-  typename T::PScale ps[kParts];
-  qt.init(wave, lane, [&](int r) { return r < live ? (uint32_t)(r * ld) : kNoFetch; });
-  pt.init(wave, lane, [&](int r) { return r < wlive ? (uint32_t)(r * ld) : kNoFetch; });
-  qs.init(wave, lane, xlead, S, [&](int r) { return r < live ? r : -1; });
+}
+
+// Lane l's 16-byte piece 2 (l / 16) + k of line l % 16 of a subtile of RowTile lines, k = 0
+// and 1: a line's swizzle repeats every 16 lines, so the offset serves all subtiles.
+__device__ __forceinline__ int piece_at(int lane, int k) {
+  return (lane & 15) * kDB + ((2 * (lane >> 4) + k) ^ RowTile<16, 1>::swz(lane & 15)) * 16;
+}
+
+// How a wave's products of one step run: 2 L units, row subtile u % L times all its column
+// subtiles, with the lower half of the operands' depth first and then the upper one.  A
+// unit's rows are read kAhead units before it into a ring of one more; once the last rows
+// are read the waves meet, the step's stage is filled again, and the rest of the units run
+// beside the first reads of the next step.
+template <int L>
+struct Units {
+  static constexpr int kCount = 2 * L;
+  static constexpr int kRing = L >= 4 ? 4 : L == 3 ? 3 : 2, kAhead = kRing - 1, kMeet = kCount - kAhead;
+  static_assert(kCount % kRing == 0 && kMeet >= L, "units keep their places; the lower halves are done at the meeting");
+};
+
+// MXFP4 rows: STAGES stages of 256 depth elements, 128 bytes of codes a row, and two groups
+// of G steps' scale bytes.  Lane l takes blocks 2 (l / 16) and 2 (l / 16) + 1 of a stage, one
+// for each half of its products.
+template <class T, bool ALIGNED, int STAGES, int G>
+struct Rows4 : T {
+  // columns of its 16 rows a wave gathers in LDS at a time: all of them where there is room
+  static constexpr int kOutCols = ALIGNED ? T::kWaveCols : 32;
+  using T::kP;
+  using T::kParts;
+  using QTile = RowTile<T::BQ, T::kWaves>;
+  using PTile = RowTile<T::kCols, T::kWaves>;
+  using QScale = ScaleTile<T::BQ, T::kWaves, G, ALIGNED>;
+  using PScale = ScaleTile<T::kCols, T::kWaves, G, ALIGNED>;
+  static constexpr int kStage = QTile::kBytes + kParts * PTile::kBytes;
+  static constexpr int kGroup = QScale::kBytes + kParts * PScale::kBytes;
+  static constexpr int kLoads = QTile::kLoads + kParts * PTile::kLoads;  // of a stage's codes
+  static constexpr int kLds = STAGES * kStage + 2 * kGroup;
+  static_assert(G >= 2, "a group's loads are waited for at a meeting before it is read");
+
+  __amdgpu_buffer_rsrc_t rx, rxs, rw[kParts], rws[kParts];
+  int xlead, wlead[kParts], ld, S, steps;
+  QTile qt;
+  PTile pt;
+  QScale qs;
+  PScale ps[kParts];
+
+  // The tile with rows `first` ... + live - 1 and weight rows `wfirst` ... + wlive - 1.
+  __device__ __forceinline__ void setup(const MxLinearArgs& a, int64_t first, int live, int64_t wfirst, int wlive, int wave, int lane) {
+    ld = a.K / 2;
+    S = a.K / mx::kBlock;
+    steps = (ld + kDB - 1) / kDB;
+    rx = resource(static_cast<const char*>(a.x) + first * ld);
+    // the scales' resources begin at the aligned dword that holds the tile's first byte
+    const uint8_t* const xs = a.xs + first * S;
+    xlead = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(xs) & 3);
+    rxs = resource(xs - xlead);
+    auto row = [](int l) { return [l](int r) { return r < l ? r : -1; }; };
+    auto off = [this](int l) { return [l, this](int r) { return r < l ? (uint32_t)(r * ld) : kNoFetch; }; };
+    qt.init(wave, lane, off(live));
+    qs.init(wave, lane, xlead, S, row(live));
+    pt.init(wave, lane, off(wlive));
 #pragma unroll
-  for (int h = 0; h < kParts; ++h) ps[h].init(wave, lane, wlead[h], S, [&](int r) { return r < wlive ? r : -1; });
-  const int steps = (ld + kDB - 1) / kDB;
-  char* const groups = smem + STAGES * T::kStage;
+    for (int h = 0; h < kParts; ++h) {
+      rw[h] = resource(static_cast<const char*>(a.w[h]) + wfirst * ld);
+      const uint8_t* const ws = a.wsb[h] + wfirst * S;
+      wlead[h] = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(ws) & 3);
+      rws[h] = resource(ws - wlead[h]);
+      ps[h].init(wave, lane, wlead[h], S, row(wlive));
+    }
+  }
+  __device__ __forceinline__ char* group(int g) const { return smem + STAGES * kStage + (g & 1) * kGroup; }
+  __device__ __forceinline__ void issue_scales(int g, int wave) const {
+    qs.load(rxs, group(g), wave, g);
+#pragma unroll
+    for (int h = 0; h < kParts; ++h) ps[h].load(rws[h], group(g) + QScale::kBytes + h * PScale::kBytes, wave, g);
+  }
   // past the last step nothing is left: the loads are issued and fetch nothing
-  auto issue_scales = [&](int g) {
-    char* b = groups + (g & 1) * T::kGroup;
-    qs.load(rxs, b, wave, lane, g);
-#pragma unroll
-    for (int h = 0; h < kParts; ++h) ps[h].load(rws[h], b + T::QScale::kBytes + h * T::PScale::kBytes, wave, lane, g);
-  };
-  auto issue = [&](int s, int stage) {
-    char* b = smem + stage * T::kStage;
+  __device__ __forceinline__ void issue(int s, int stage, int wave) const {
+    char* b = smem + stage * kStage;
     qt.load(rx, b, wave, s * kDB, ld - s * kDB);
 #pragma unroll
-    for (int h = 0; h < kParts; ++h)
-      pt.load(rw[h], b + T::QTile::kBytes + h * T::PTile::kBytes, wave, s * kDB, ld - s * kDB);
-  };
-  f32x4 acc[kQ][kP];
+    for (int h = 0; h < kParts; ++h) pt.load(rw[h], b + QTile::kBytes + h * PTile::kBytes, wave, s * kDB, ld - s * kDB);
+  }
+  __device__ __forceinline__ void start(int wave) const {
+    issue_scales(0, wave);
 #pragma unroll
-  for (int i = 0; i < kQ; ++i)
-#pragma unroll
-    for (int j = 0; j < kP; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  issue_scales(0);
-#pragma unroll
-  for (int s = 0; s < STAGES; ++s) issue(s, s);
-
-  // A step is 2 L units: row subtile u % L times all column subtiles, first of the stage's
-  // lower halves, then of the upper ones.  A unit's rows are read kAhead units before it,
-  // into a ring of as many and one, the columns' other half beside the first unit; once the
-  // last rows are read the waves meet, the stage is filled again, and the rest of the units
-  // run beside the first reads of the next stage.
-  auto multiply = [&](auto live_subtiles) {
-    constexpr int L = decltype(live_subtiles)::value, kUnits = 2 * L;
-    constexpr int kRing = L >= 4 ? 4 : L == 3 ? 3 : 2, kAhead = kRing - 1, kMeet = kUnits - kAhead;
-    static_assert(kUnits % kRing == 0 && kMeet >= L, "units keep their places; the lower halves are done at the meeting");
+    for (int s = 0; s < STAGES; ++s) issue(s, s, wave);
+  }
+  // The tile's products, the first L row subtiles of a wave's.
+  template <int L>
+  __device__ __forceinline__ void multiply(int wave, int lane, f32x4 (&acc)[T::kQ][kP]) const {
+    using U = Units<L>;
+    constexpr int kC = T::kC, kSq = (L + 1) / 2, kSp = (kP + 1) / 2;
+    const int wq = wave / T::WP, wp = wave % T::WP;
     int stage = 0;
-    u32x4 q[kRing], p[2][kP];
-    // scales of this step and of the next, those of two subtiles in a register
-    constexpr int kSq = (L + 1) / 2, kSp = (kP + 1) / 2;
-    uint32_t sq[kSq], sp[kSp], nq[kSq], np[kSp];
-    // Lane l reads the pieces 2 (l / 16) + k of line l % 16 of a subtile; a line's swizzle
-    // repeats every 16 lines, so one offset a half serves all subtiles.  (As a vector, not a
-    // uint4: of a struct the compiler loses the type, takes the read to depend on every
-    // direct load and waits for the one just issued.)
-    int at[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) at[k] = (lane & 15) * kDB + ((2 * (lane >> 4) + k) ^ T::QTile::swz(lane & 15)) * 16;
-    const int sx_at = T::QScale::lane_at(lane, xlead, S) + wq * 16 * T::QScale::kRow;
+    u32x4 q[U::kRing], p[2][kP];
+    uint32_t sq[kSq], sp[kSp], nq[kSq], np[kSp];  // scales of this step and of the next, two subtiles' in a register
+    // (Reads are of a vector, not of a uint4: of a struct the compiler loses the type, takes
+    // the read to depend on every direct load and waits for the one just issued.)
+    const int at[2] = {piece_at(lane, 0), piece_at(lane, 1)};
+    const int sx_at = QScale::lane_at(lane, xlead, S) + wq * 16 * QScale::kRow;
     int sw_at[kParts];
 #pragma unroll
     for (int h = 0; h < kParts; ++h)
-      sw_at[h] = T::PScale::lane_at(lane, wlead[h], S) + wp * (kCols / WP) * T::PScale::kRow + T::QScale::kBytes + h * T::PScale::kBytes;
+      sw_at[h] = PScale::lane_at(lane, wlead[h], S) + wp * T::kWaveCols * PScale::kRow + QScale::kBytes + h * PScale::kBytes;
     auto read_q = [&](int u) {
-      const char* b = smem + stage * T::kStage + wq * 16 * kDB + at[u / L];
-      q[u % kRing] = *reinterpret_cast<const u32x4*>(b + u % L * WQ * 16 * kDB);
+      const char* b = smem + stage * kStage + wq * 16 * kDB + at[u / L];
+      q[u % U::kRing] = *reinterpret_cast<const u32x4*>(b + u % L * T::WQ * 16 * kDB);
     };
     auto read_p = [&](int k) {
-      const char* b = smem + stage * T::kStage + T::QTile::kBytes + wp * (kCols / WP) * kDB + at[k];
+      const char* b = smem + stage * kStage + QTile::kBytes + wp * T::kWaveCols * kDB + at[k];
 #pragma unroll
-      for (int j = 0; j < kP; ++j) p[k][j] = *reinterpret_cast<const u32x4*>(b + j / kC * T::PTile::kBytes + j % kC * 16 * kDB);
+      for (int j = 0; j < kP; ++j) p[k][j] = *reinterpret_cast<const u32x4*>(b + j / kC * PTile::kBytes + j % kC * 16 * kDB);
     };
     auto read_scales = [&](int s) {
-      const char* b = groups + (s / G & 1) * T::kGroup + s % G * 8;
+      const char* b = group(s / G) + s % G * 8;
       const int left = S - s * 8 - 2 * (lane >> 4);
-      auto of_q = [&](int i) { return T::QScale::pair(b + sx_at + i * WQ * 16 * T::QScale::kRow, left); };
-      auto of_p = [&](int j) { return T::PScale::pair(b + sw_at[j / kC] + j % kC * 16 * T::PScale::kRow, left); };
+      auto of_q = [&](int i) { return QScale::pair(b + sx_at + i * T::WQ * 16 * QScale::kRow, left); };
+      auto of_p = [&](int j) { return PScale::pair(b + sw_at[j / kC] + j % kC * 16 * PScale::kRow, left); };
 #pragma unroll
       for (int i = 0; i < kSq; ++i) nq[i] = of_q(2 * i) | (2 * i + 1 < L ? of_q(2 * i + 1) << 16 : 0u);
 #pragma unroll
@@ -318,43 +372,217 @@ __global__ __launch_bounds__(WQ* WP * 64, 2) void linear_rows4_kernel(MxLinearAr
       constexpr int u = decltype(index)::value, i = u % L, H = u / L, O = H + 2 * (i & 1);
 #pragma unroll
       for (int j = 0; j < kP; ++j)
-        acc[i][j] = j & 1 ? mx::mfma<H + 2, O>(p[H][j], sp[j / 2], q[u % kRing], sq[i / 2], acc[i][j])
-                          : mx::mfma<H, O>(p[H][j], sp[j / 2], q[u % kRing], sq[i / 2], acc[i][j]);
+        acc[i][j] = j & 1 ? mx::mfma<H + 2, O>(p[H][j], sp[j / 2], q[u % U::kRing], sq[i / 2], acc[i][j])
+                          : mx::mfma<H, O>(p[H][j], sp[j / 2], q[u % U::kRing], sq[i / 2], acc[i][j]);
     };
-    wait_and_meet<(STAGES - 1) * T::kLoads>();
+    wait_and_meet<(STAGES - 1) * kLoads>();
     read_p(0);
     read_scales(0);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) read_q(u);
+    for (int u = 0; u < U::kAhead; ++u) read_q(u);
     for (int s = 0; s < steps; ++s) {
       // the next group: the last bytes of the one before this, whose place it takes, were
       // read before the meeting of step s - 1 (a branch behind the meeting would draw the
       // products in front of it into its far side)
-      if (s % G == 0) issue_scales(s / G + 1);
+      if (s % G == 0) issue_scales(s / G + 1, wave);
 #pragma unroll
       for (int i = 0; i < kSq; ++i) sq[i] = nq[i];
 #pragma unroll
       for (int j = 0; j < kSp; ++j) sp[j] = np[j];
-      each<kUnits>([&](auto index) {
+      each<U::kCount>([&](auto index) {
         constexpr int u = decltype(index)::value;
-        if constexpr (u == kMeet) {
-          wait_and_meet<(STAGES - 2) * T::kLoads>();  // this step's operands are in registers, the next stage has landed
-          issue(s + STAGES, stage);
+        if constexpr (u == U::kMeet) {
+          wait_and_meet<(STAGES - 2) * kLoads>();  // this step's operands are in registers, the next stage has landed
+          issue(s + STAGES, stage, wave);
           stage = stage == STAGES - 1 ? 0 : stage + 1;
           read_p(0);  // of step s + 1; past the last one whatever lies there, unused
           read_scales(s + 1);
         }
-        read_q(u < kMeet ? u + kAhead : u - kMeet);
+        read_q(u < U::kMeet ? u + U::kAhead : u - U::kMeet);
         if constexpr (u == 0) read_p(1);
         __builtin_amdgcn_sched_barrier(0);  // the reads are on their way before the products
         unit(index);
         __builtin_amdgcn_sched_barrier(0);
       });
     }
+  }
+};
+
+// bf16 rows: two stages of 64 depth elements, 128 bytes a row, beside two stages of 256 of
+// the weights, 128 bytes of codes and 8 of scales a row, each for four steps.  Lane l takes
+// the elements 16 (l / 16) ... + 15 of a step, which lie in one scale block, the first 8 in
+// the lower half of its products; it reads their codes as 8 bytes and widens them with the
+// scale as it goes, a half beside the products of the other.
+template <class T, bool ALIGNED>
+struct Rows16 : T {
+  using T::kP;
+  using T::kParts;
+  using QTile = RowTile<T::BQ, T::kWaves>;
+  using PTile = RowTile<T::kCols, T::kWaves>;
+  using PScale = ScaleTile<T::kCols, T::kWaves, 1, ALIGNED>;
+  static constexpr int kOutCols = T::kWaveCols;
+  static constexpr int kPStage = kParts * (PTile::kBytes + PScale::kBytes);
+  static constexpr int kPLoads = kParts * PTile::kLoads;  // of a stage's codes
+  static constexpr int kLds = 2 * QTile::kBytes + 2 * kPStage;
+
+  __amdgpu_buffer_rsrc_t rx, rw[kParts], rws[kParts];
+  int wlead[kParts], K, S, steps;
+  QTile qt;
+  PTile pt;
+  PScale ps[kParts];
+
+  __device__ __forceinline__ void setup(const MxLinearArgs& a, int64_t first, int live, int64_t wfirst, int wlive, int wave, int lane) {
+    K = a.K;
+    S = K / mx::kBlock;
+    steps = (K * 2 + kDB - 1) / kDB;
+    rx = resource(static_cast<const char*>(a.x) + first * K * 2);
+    qt.init(wave, lane, [&](int r) { return r < live ? (uint32_t)(r * K * 2) : kNoFetch; });
+    pt.init(wave, lane, [&](int r) { return r < wlive ? (uint32_t)(r * (K / 2)) : kNoFetch; });
+#pragma unroll
+    for (int h = 0; h < kParts; ++h) {
+      rw[h] = resource(static_cast<const char*>(a.w[h]) + wfirst * (K / 2));
+      const uint8_t* const ws = a.wsb[h] + wfirst * S;
+      wlead[h] = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(ws) & 3);
+      rws[h] = resource(ws - wlead[h]);
+      ps[h].init(wave, lane, wlead[h], S, [&](int r) { return r < wlive ? r : -1; });
+    }
+  }
+  __device__ __forceinline__ char* weights(int m) const { return smem + 2 * QTile::kBytes + (m & 1) * kPStage; }
+  // past the last step nothing is left: the loads are issued and fetch nothing
+  __device__ __forceinline__ void issue_q(int s, int wave) const {
+    qt.load(rx, smem + (s & 1) * QTile::kBytes, wave, s * kDB, K * 2 - s * kDB);
+  }
+  __device__ __forceinline__ void issue_p(int m, int wave) const {
+    char* b = weights(m);
+#pragma unroll
+    for (int h = 0; h < kParts; ++h) {
+      ps[h].load(rws[h], b + kParts * PTile::kBytes + h * PScale::kBytes, wave, m);
+      pt.load(rw[h], b + h * PTile::kBytes, wave, m * kDB, K / 2 - m * kDB);
+    }
+  }
+  __device__ __forceinline__ void start(int wave) const {
+    issue_p(0, wave);
+    issue_q(0, wave);
+    issue_q(1, wave);
+  }
+  // The tile's products, the first L row subtiles of a wave's.
+  template <int L>
+  __device__ __forceinline__ void multiply(int wave, int lane, f32x4 (&acc)[T::kQ][kP]) const {
+    using U = Units<L>;
+    constexpr int kC = T::kC;
+    const int wq = wave / T::WP, wp = wave % T::WP, quad = lane >> 4;
+    bf16x8 q[U::kRing], p[2][kP];
+    u32x2 codes[kP];
+    float scale[kP];
+    const int at[2] = {piece_at(lane, 0), piece_at(lane, 1)};
+    // 8 bytes of piece l / 32 of a line, in step 0 of a stage; a step later two pieces on
+    const int code_at = (lane & 15) * kDB + ((quad >> 1) ^ PTile::swz(lane & 15)) * 16 + (quad & 1) * 8 + wp * T::kWaveCols * kDB;
+    int scale_at[kParts];
+#pragma unroll
+    for (int h = 0; h < kParts; ++h)
+      scale_at[h] = PScale::row_at(lane, wlead[h], S) + (quad >> 1) + wp * T::kWaveCols * PScale::kRow + kParts * PTile::kBytes + h * PScale::kBytes;
+    auto read_q = [&](int s, int u) {
+      const char* b = smem + (s & 1) * QTile::kBytes + wq * 16 * kDB + at[u / L];
+      q[u % U::kRing] = *reinterpret_cast<const bf16x8*>(b + u % L * T::WQ * 16 * kDB);
+    };
+    auto read_p = [&](int s) {
+      const char* b = weights(s >> 2);
+      const int c = code_at ^ (s & 3) << 5;
+      const bool in = ALIGNED || (s * 2 + (quad >> 1)) < S;  // past the depth the codes are zeros, and the byte must not be a NaN's
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        codes[j] = *reinterpret_cast<const u32x2*>(b + c + j / kC * PTile::kBytes + j % kC * 16 * kDB);
+        const uint32_t byte = *reinterpret_cast<const uint8_t*>(b + scale_at[j / kC] + (s & 3) * 2 + j % kC * 16 * PScale::kRow);
+        scale[j] = mx::scale_bits(in ? byte : 0u);
+      }
+    };
+    auto widen = [&](int k) {
+#pragma unroll
+      for (int j = 0; j < kP; ++j) p[k][j] = mma::fp4x8_to_bf16(codes[j][k], scale[j]);
+    };
+    wait_and_meet<QTile::kLoads>();
+    read_p(0);
+#pragma unroll
+    for (int u = 0; u < U::kAhead; ++u) read_q(0, u);
+    widen(0);
+    for (int s = 0; s < steps; ++s) {
+      // the next weights: those before this step's, whose place they take, were in registers
+      // at the last meeting
+      if ((s & 3) == 0) issue_p((s >> 2) + 1, wave);
+      each<U::kCount>([&](auto index) {
+        constexpr int u = decltype(index)::value;
+        if constexpr (u == U::kMeet) {
+          // this step's operands are in registers and the next one's have landed, behind which
+          // there may be those weights on their way
+          if ((s & 3) == 0)
+            wait_and_meet<kPLoads>();
+          else
+            wait_and_meet<0>();
+          issue_q(s + 2, wave);
+          read_p(s + 1);
+        }
+        read_q(u < U::kMeet ? s : s + 1, u < U::kMeet ? u + U::kAhead : u - U::kMeet);
+        __builtin_amdgcn_sched_barrier(0);  // the reads are on their way before the products
+#pragma unroll
+        for (int j = 0; j < kP; ++j) acc[u % L][j] = mma::mfma(p[u / L][j], q[u % U::kRing], acc[u % L][j]);
+        if constexpr (u == 0) widen(1);
+        if constexpr (u == U::kCount - 1) widen(0);  // of the next step
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    }
+  }
+};
+
+// Tiles one after another (SERIES): workgroup b takes tile b / 8 and every (grid / 8)-th one
+// after it of the run of tiles that XCD b % 8 is dealt.  A tile's first stages are loaded
+// while the results of the one before it leave; with a tile per workgroup the search for it,
+// the first loads' latency and the results' way out were half of the time where the depth
+// is short.  Else a workgroup takes tile b / 8 alone: stores and loads come back in one
+// order, so a tile's first stage waits for the results before it, which a workgroup that
+// has a compute unit to itself pays for (128 experts, 32768 rows by 2048 x 768, 256 x 256
+// tiles: 143 us in series, 118 alone; 128 x 128, two to a compute unit: 106 and 115).
+template <class C, bool SERIES>
+__global__ __launch_bounds__(C::kThreads, 2) void linear_mx_kernel(MxLinearArgs a) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Runs runs;
+  runs.scan(a, C::BQ, (a.N + C::kCols - 1) / C::kCols);
+  const int64_t b = row::block_index();
+  const int chunk = (runs.total + 7) / 8, base = (int)(b & 7) * chunk, stride = (int)gridDim.x >> 3;
+  int64_t at = b >> 3;
+  auto next = [&] { return at < chunk && base + at < runs.total ? runs.item(a, base + (int)at) : Item{-1, 0, 0, 0, 0}; };
+  Item it = next();
+  if (it.e < 0) return;
+  char* const out = smem + C::kLds + wave * (16 * C::kOutCols * 2);
+  C core;
+  int64_t first;
+  int live, p0;
+  auto begin = [&] {
+    first = (int64_t)it.row0 + it.tq * C::BQ;
+    live = min(C::BQ, it.count - it.tq * C::BQ);
+    p0 = it.tp * C::kCols;
+    core.setup(a, first, live, (int64_t)it.e * a.N + p0, min(C::kCols, a.N - p0), wave, lane);
+    core.start(wave);
   };
-  by_live_subtiles<kQ>((live - wq * 16 + 16 * WQ - 1) / (16 * WQ), multiply);
-  wait_and_meet<0>();  // the loads past the last step have landed: LDS is free
-  finish<GATED, BQ, kCols, WQ, WP, kQ, kC>(a, it.e, first, live, p0, wq, wp, acc);
+  begin();
+  while (true) {
+    f32x4 acc[C::kQ][C::kP];
+#pragma unroll
+    for (int i = 0; i < C::kQ; ++i)
+#pragma unroll
+      for (int j = 0; j < C::kP; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    by_live_subtiles<C::kQ>((live - wave / C::WP * 16 + 16 * C::WQ - 1) / (16 * C::WQ),
+                            [&](auto l) { core.template multiply<decltype(l)::value>(wave, lane, acc); });
+    wait_and_meet<0>();  // every wave is done with the stages, and the loads past the last step have landed
+    Finish<C> finish{it.e, live, p0, first};
+    finish.load(a, wave);
+    if constexpr (SERIES) {
+      at += stride;
+      it = next();
+      if (it.e >= 0) begin();
+    }
+    finish.store(a, wave, out, acc);
+    if (!SERIES || it.e < 0) break;
+  }
 }
 
 // --------------------------------------------------- forward, few rows --
@@ -606,15 +834,28 @@ MOE_MX_TILES(false, true)
 MOE_MX_TILES(true, false)
 MOE_MX_TILES(true, true)
 #undef MOE_MX_TILES
-#define MOE_MX_ROWS4(G, A)                                                    \
-  template __global__ void linear_rows4_kernel<G, A, 256, 256, 2, 4, 2, 2>(MxLinearArgs); \
-  template __global__ void linear_rows4_kernel<G, A, 128, 128, 2, 2, 2, 4>(MxLinearArgs); \
-  template __global__ void linear_rows4_kernel<G, A, 64, 64, G ? 4 : 2, G ? 1 : 2, 3, 4>(MxLinearArgs);
+template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES, int G>
+using R4 = Rows4<Shape<GATED, BQ, BP, WQ, WP>, ALIGNED, STAGES, G>;
+#define MOE_MX_ROWS4(G, A)                                                     \
+  template __global__ void linear_mx_kernel<R4<G, A, 256, 256, 2, 4, 2, 2>, false>(MxLinearArgs); \
+  template __global__ void linear_mx_kernel<R4<G, A, 128, 128, 2, 2, 2, 2>, true>(MxLinearArgs); \
+  template __global__ void linear_mx_kernel<R4<G, A, 64, 64, G ? 4 : 2, G ? 1 : 2, 3, 4>, false>(MxLinearArgs);
 MOE_MX_ROWS4(false, false)
 MOE_MX_ROWS4(false, true)
 MOE_MX_ROWS4(true, false)
 MOE_MX_ROWS4(true, true)
 #undef MOE_MX_ROWS4
+template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP>
+using R16 = Rows16<Shape<GATED, BQ, BP, WQ, WP>, ALIGNED>;
+#define MOE_MX_ROWS16(G, A)                                                    \
+  template __global__ void linear_mx_kernel<R16<G, A, 256, 256, 2, 4>, false>(MxLinearArgs); \
+  template __global__ void linear_mx_kernel<R16<G, A, 128, 128, 2, 2>, true>(MxLinearArgs); \
+  template __global__ void linear_mx_kernel<R16<G, A, 64, 64, G ? 4 : 2, G ? 1 : 2>, false>(MxLinearArgs);
+MOE_MX_ROWS16(false, false)
+MOE_MX_ROWS16(false, true)
+MOE_MX_ROWS16(true, false)
+MOE_MX_ROWS16(true, true)
+#undef MOE_MX_ROWS16
 template __global__ void linear_mx_backward_x_kernel<128, 128, 2, 2>(MxLinearArgs);
 
 template <typename K>
@@ -633,13 +874,17 @@ hipError_t run_few(const MxLinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool GATED, bool ALIGNED, int BQ, int BP, int WQ, int WP, int STAGES, int G>
-hipError_t run_rows4(const MxLinearArgs& a, hipStream_t s) {
-  using T = Rows4<GATED, ALIGNED, BQ, BP, WQ, WP, STAGES, G>;
+// A workgroup per tile, or in series as many as run at once: kCUs compute units, as many
+// workgroups on each as have room in LDS.
+constexpr int64_t kCUs = 256;
+template <class C, bool SERIES>
+hipError_t run_tiles(const MxLinearArgs& a, hipStream_t s) {
   static std::atomic<size_t> allowed[kMaxCachedDevices];
-  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, BQ) * ((a.N + T::kCols - 1) / T::kCols);
-  void (*const kern)(MxLinearArgs) = &linear_rows4_kernel<GATED, ALIGNED, BQ, BP, WQ, WP, STAGES, G>;
-  return launch(kern, items, T::kThreads, T::kLds, a, s, allowed);
+  constexpr int lds = C::kLds + C::kWaves * 16 * C::kOutCols * 2;
+  static_assert(lds <= 160 * 1024, "a compute unit's LDS");
+  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, C::BQ) * ((a.N + C::kCols - 1) / C::kCols);
+  void (*const kern)(MxLinearArgs) = &linear_mx_kernel<C, SERIES>;
+  return launch(kern, SERIES ? std::min(items, kCUs * (160 * 1024 / lds)) : items, C::kThreads, lds, a, s, allowed);
 }
 
 // Rows per expert on average, of the matrix's height, in which the alignment's padding
@@ -660,9 +905,18 @@ template <bool GATED, bool ALIGNED>
 hipError_t rows4_by_shape(const MxLinearArgs& a, hipStream_t s) {
   if (mean_rows(a) <= kFewRows) return run_few<true, GATED, 2, 8>(a, s);
   const int64_t cols = a.parts * (int64_t)a.N;
-  if (tiles(a, cols, 128) < 256) return run_rows4<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2, 3, 4>(a, s);
-  if (wide_tiles(a, cols)) return run_rows4<GATED, ALIGNED, 256, 256, 2, 4, 2, 2>(a, s);
-  return run_rows4<GATED, ALIGNED, 128, 128, 2, 2, 2, 4>(a, s);
+  if (tiles(a, cols, 128) < 256) return run_tiles<R4<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2, 3, 4>, false>(a, s);
+  if (wide_tiles(a, cols)) return run_tiles<R4<GATED, ALIGNED, 256, 256, 2, 4, 2, 2>, false>(a, s);
+  return run_tiles<R4<GATED, ALIGNED, 128, 128, 2, 2, 2, 2>, true>(a, s);
+}
+
+template <bool GATED, bool ALIGNED>
+hipError_t rows16_by_shape(const MxLinearArgs& a, hipStream_t s) {
+  if (mean_rows(a) <= kFewRows) return run_few<false, GATED, 2, 8>(a, s);
+  const int64_t cols = a.parts * (int64_t)a.N;
+  if (tiles(a, cols, 128) < 256) return run_tiles<R16<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2>, false>(a, s);
+  if (wide_tiles(a, cols)) return run_tiles<R16<GATED, ALIGNED, 256, 256, 2, 4>, false>(a, s);
+  return run_tiles<R16<GATED, ALIGNED, 128, 128, 2, 2>, true>(a, s);
 }
 
 template <int BQ, int BP, int WQ, int WP>
@@ -675,12 +929,14 @@ hipError_t run_backward_x(const MxLinearArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_linear_mx(const MxLinearArgs& a, hipStream_t s) {
+  const uintptr_t lead = reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.wsb[0]) | reinterpret_cast<uintptr_t>(a.wsb[1]);
+  const bool aligned = a.K % 128 == 0 && lead % 4 == 0, gated = a.parts == 2;
   if (a.xs != nullptr) {
-    const uintptr_t lead = reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.wsb[0]) | reinterpret_cast<uintptr_t>(a.wsb[1]);
-    if (a.K % 128 == 0 && lead % 4 == 0) return a.parts == 2 ? rows4_by_shape<true, true>(a, s) : rows4_by_shape<false, true>(a, s);
-    return a.parts == 2 ? rows4_by_shape<true, false>(a, s) : rows4_by_shape<false, false>(a, s);
+    if (aligned) return gated ? rows4_by_shape<true, true>(a, s) : rows4_by_shape<false, true>(a, s);
+    return gated ? rows4_by_shape<true, false>(a, s) : rows4_by_shape<false, false>(a, s);
   }
-  return a.parts == 2 ? run_few<false, true, 2, 8>(a, s) : run_few<false, false, 2, 8>(a, s);
+  if (aligned) return gated ? rows16_by_shape<true, true>(a, s) : rows16_by_shape<false, true>(a, s);
+  return gated ? rows16_by_shape<true, false>(a, s) : rows16_by_shape<false, false>(a, s);
 }
 
 hipError_t launch_linear_mx_backward_x(const MxLinearArgs& a, hipStream_t s) { return run_backward_x<128, 128, 2, 2>(a, s); }

@@ -68,65 +68,83 @@ __device__ __forceinline__ void tile_of(int i, int rt, int cp, Item& it) {
   it.tq = 8 * g + r - it.tp * rows;
 }
 
-// The tile of workgroup `b` out of those of all experts' runs, `bq` rows a tile
-// and `cp` column tiles.  Every wave finds it by itself: lane l sums the tiles of
-// experts l J ... l J + J - 1, a scan over the wave gives each lane's first tile,
-// and the lane that holds the item names the expert.  Tiles are numbered expert
-// by expert, within an expert 8 row tiles by 8 row tiles, there column tile by column
-// tile, and dealt to the 8 XCDs in 8 equal runs (workgroup b runs on XCD b mod 8), so an
-// expert's weights and rows stay in one XCD's L2.
-__device__ __forceinline__ Item find_item(const LinearArgs& a, int b, int bq, int cp) {
-  Item it{-1, 0, 0, 0, 0};
-  if (a.offsets == nullptr) {
-    const int rt = ceil_div(a.rows, bq), total = rt * cp, chunk = (total + 7) / 8;
-    const int i = (b & 7) * chunk + (b >> 3);
-    if ((b >> 3) >= chunk || i >= total) return it;
-    it.e = 0;
-    it.count = a.rows;
-    tile_of(i, rt, cp, it);
+// All experts' tiles, `bq` rows a tile and `cp` column tiles.  Every wave scans the tables
+// by itself: lane l sums the tiles of experts l J ... l J + J - 1, a scan over the wave gives
+// each lane's first tile, and the lane that holds an item names its expert.  Tiles are
+// numbered expert by expert, within an expert 8 row tiles by 8 row tiles, there column tile
+// by column tile.
+struct Runs {
+  int bq, cp, J;
+  int mine, incl;  // row tiles of this lane's experts, and with those of the lanes before it
+  int total;       // tiles
+
+  __device__ __forceinline__ void scan(const LinearArgs& a, int rows_per_tile, int column_tiles) {
+    bq = rows_per_tile;
+    cp = column_tiles;
+    mine = incl = J = 0;
+    if (a.offsets == nullptr) {
+      total = ceil_div(a.rows, bq) * cp;
+      return;
+    }
+    const int lane = threadIdx.x & 63;
+    J = (a.E + 63) >> 6;
+    // No sum passes what runs that do not overlap can make (row_tiles_bound), so tables
+    // that claim more cannot wrap the products below; their items past it are left out.
+    const int most = a.rows / bq + min(a.E, a.rows);
+    for (int j = 0; j < J; ++j) {
+      const int e = lane * J + j;
+      if (e < a.E) mine = min(most, mine + ceil_div(run_length(a.offsets[e], a.counts[e], a.rows), bq));
+    }
+    incl = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(incl, d);
+      if (lane >= d) incl = min(most, incl + v);
+    }
+    total = __builtin_amdgcn_readlane(incl, 63) * cp;
+  }
+
+  // Tile i < total.
+  __device__ __forceinline__ Item item(const LinearArgs& a, int i) const {
+    Item it{0, 0, a.rows, 0, 0};
+    if (a.offsets == nullptr) {
+      tile_of(i, ceil_div(a.rows, bq), cp, it);
+      return it;
+    }
+    // the lane whose experts hold item i, and the expert within it
+    const int lane = threadIdx.x & 63;
+    const uint64_t after = __ballot(i < incl * cp);
+    const int owner = __builtin_ctzll(after);
+    int rest = i - (incl - mine) * cp, e = lane * J, off = 0, cnt = 0, rt = 1;
+    for (int j = 0; j < J; ++j) {
+      const int c = lane * J + j;
+      if (c >= a.E) break;
+      const int o = a.offsets[c], n = run_length(o, a.counts[c], a.rows), r = ceil_div(n, bq);
+      e = c;
+      off = o;
+      cnt = n;
+      rt = r;
+      if (rest < r * cp) break;
+      rest -= r * cp;
+    }
+    it.e = __builtin_amdgcn_readlane(e, owner);
+    it.row0 = __builtin_amdgcn_readlane(off, owner);
+    it.count = __builtin_amdgcn_readlane(cnt, owner);
+    rt = __builtin_amdgcn_readlane(rt, owner);
+    rest = __builtin_amdgcn_readlane(rest, owner);
+    tile_of(rest, rt, cp, it);
     return it;
   }
-  const int lane = threadIdx.x & 63;
-  const int J = (a.E + 63) >> 6;
-  // No sum passes what runs that do not overlap can make (row_tiles_bound), so tables
-  // that claim more cannot wrap the products below; their items past it are left out.
-  const int most = a.rows / bq + min(a.E, a.rows);
-  int mine = 0;
-  for (int j = 0; j < J; ++j) {
-    const int e = lane * J + j;
-    if (e < a.E) mine = min(most, mine + ceil_div(run_length(a.offsets[e], a.counts[e], a.rows), bq));
-  }
-  int incl = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d);
-    if (lane >= d) incl = min(most, incl + v);
-  }
-  const int total = __builtin_amdgcn_readlane(incl, 63) * cp, chunk = (total + 7) / 8;
-  const int i = (b & 7) * chunk + (b >> 3);
-  if ((b >> 3) >= chunk || i >= total) return it;
-  // the lane whose experts hold item i, and the expert within it
-  const uint64_t after = __ballot(i < incl * cp);
-  const int owner = __builtin_ctzll(after);
-  int rest = i - (incl - mine) * cp, e = lane * J, off = 0, cnt = 0, rt = 1;
-  for (int j = 0; j < J; ++j) {
-    const int c = lane * J + j;
-    if (c >= a.E) break;
-    const int o = a.offsets[c], n = run_length(o, a.counts[c], a.rows), r = ceil_div(n, bq);
-    e = c;
-    off = o;
-    cnt = n;
-    rt = r;
-    if (rest < r * cp) break;
-    rest -= r * cp;
-  }
-  it.e = __builtin_amdgcn_readlane(e, owner);
-  it.row0 = __builtin_amdgcn_readlane(off, owner);
-  it.count = __builtin_amdgcn_readlane(cnt, owner);
-  rt = __builtin_amdgcn_readlane(rt, owner);
-  rest = __builtin_amdgcn_readlane(rest, owner);
-  tile_of(rest, rt, cp, it);
-  return it;
+};
+
+// The tile of workgroup `b`: tiles are dealt to the 8 XCDs in 8 equal runs (workgroup b runs
+// on XCD b mod 8), so an expert's weights and rows stay in one XCD's L2.
+__device__ __forceinline__ Item find_item(const LinearArgs& a, int b, int bq, int cp) {
+  Runs runs;
+  runs.scan(a, bq, cp);
+  const int chunk = (runs.total + 7) / 8, i = (b & 7) * chunk + (b >> 3);
+  if ((b >> 3) >= chunk || i >= runs.total) return Item{-1, 0, 0, 0, 0};
+  return runs.item(a, i);
 }
 
 // Row tiles all runs can need: one partly filled tile per expert on top of the full ones.
