@@ -118,6 +118,8 @@ struct Shape {
   static constexpr int kWaveCols = kCols / WP;             // and of a wave
   static constexpr int kQ = BQ / WQ / 16, kP = BP / WP / 16, kC = kP / kParts;
   static_assert(kC % 2 == 0, "a wave holds whole scale blocks of its rows' columns");
+  // Columns of the result.
+  __device__ static __forceinline__ int width(const MxLinearArgs& a) { return a.N; }
 };
 
 // Rows below `live` of the 16 rows of BYTES that a wave has gathered at `lds`, their first
@@ -159,7 +161,7 @@ struct Finish {
     for (int j = 0; j < T::kC; ++j) {
       const int n = column(wave, j);
       residual[i & 1][j] = make_uint2(0, 0);
-      if (m < live && n < a.N) residual[i & 1][j] = *reinterpret_cast<const uint2*>(a.residual + (first + m) * a.N + n);
+      if (m < live && n < T::width(a)) residual[i & 1][j] = *reinterpret_cast<const uint2*>(a.residual + (first + m) * T::width(a) + n);
     }
   }
   __device__ __forceinline__ void load(const MxLinearArgs& a, int wave) {
@@ -179,6 +181,7 @@ struct Finish {
 template <class T>
 __device__ __forceinline__ void Finish<T>::store(const MxLinearArgs& a, int wave, char* lds, f32x4 (&acc)[T::kQ][T::kP]) {
   constexpr int kC = T::kC;
+  const int N = T::width(a);
   const int wq = wave / T::WP, wp = wave % T::WP;
   const int lane = threadIdx.x & 63, quad = lane >> 4, row16 = lane & 15;
   constexpr int kO = T::kOutCols / 16;  // column subtiles gathered at a time
@@ -192,7 +195,7 @@ __device__ __forceinline__ void Finish<T>::store(const MxLinearArgs& a, int wave
     const int64_t r0 = first + q_row<T::WQ>(wq, i);
 #pragma unroll
     for (int j0 = 0; j0 < kC; j0 += kO) {
-      const int n0 = p0 + wp * T::kWaveCols + j0 * 16, cols = min(T::kOutCols, a.N - n0);
+      const int n0 = p0 + wp * T::kWaveCols + j0 * 16, cols = min(T::kOutCols, N - n0);
       if (cols <= 0) break;
       float y[kO][4], u[kO][4];
 #pragma unroll
@@ -211,18 +214,18 @@ __device__ __forceinline__ void Finish<T>::store(const MxLinearArgs& a, int wave
         if (a.preact != nullptr) Rows::put(lds, row16, n * 2, pack4(z));
       }
       if (a.preact != nullptr) {
-        char* pre = reinterpret_cast<char*>(a.preact + r0 * T::kParts * a.N + n0);
-        flush16<T::kOutCols * 2>(lds, pre, (int64_t)T::kParts * a.N * 2, left, cols * 2);
+        char* pre = reinterpret_cast<char*>(a.preact + r0 * T::kParts * N + n0);
+        flush16<T::kOutCols * 2>(lds, pre, (int64_t)T::kParts * N * 2, left, cols * 2);
         if constexpr (T::kGated) {
 #pragma unroll
           for (int j = 0; j < kO; ++j) Rows::put(lds, row16, (j * 16 + quad * 4) * 2, pack4(u[j]));
-          flush16<T::kOutCols * 2>(lds, pre + (int64_t)a.N * 2, (int64_t)2 * a.N * 2, left, cols * 2);
+          flush16<T::kOutCols * 2>(lds, pre + (int64_t)N * 2, (int64_t)2 * N * 2, left, cols * 2);
         }
       }
       if (a.ysb == nullptr) {
 #pragma unroll
         for (int j = 0; j < kO; ++j) Rows::put(lds, row16, (j * 16 + quad * 4) * 2, pack4(y[j]));
-        flush16<T::kOutCols * 2>(lds, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + r0 * a.N + n0), (int64_t)a.N * 2, left,
+        flush16<T::kOutCols * 2>(lds, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + r0 * N + n0), (int64_t)N * 2, left,
                                  cols * 2);
         continue;
       }
@@ -239,9 +242,9 @@ __device__ __forceinline__ void Finish<T>::store(const MxLinearArgs& a, int wave
         for (int h = 0; h < 2; ++h)
           Codes::put(lds, row16, ((j + h) * 16 + quad * 4) / 2, (uint16_t)mx::codes4(y[j + h][0], y[j + h][1], y[j + h][2], y[j + h][3], byte));
         if (quad == 0 && row16 < left && j * 16 < cols)
-          a.ysb[(r0 + row16) * (a.N / mx::kBlock) + (n0 + j * 16) / mx::kBlock] = (uint8_t)byte;
+          a.ysb[(r0 + row16) * (N / mx::kBlock) + (n0 + j * 16) / mx::kBlock] = (uint8_t)byte;
       }
-      flush16<T::kOutCols / 2>(lds, static_cast<char*>(a.y) + (r0 * a.N + n0) / 2, a.N / 2, left, cols / 2);
+      flush16<T::kOutCols / 2>(lds, static_cast<char*>(a.y) + (r0 * N + n0) / 2, N / 2, left, cols / 2);
     }
   }
 }
@@ -290,8 +293,10 @@ struct Rows4 : T {
   QScale qs;
   PScale ps[kParts];
 
-  // The tile with rows `first` ... + live - 1 and weight rows `wfirst` ... + wlive - 1.
-  __device__ __forceinline__ void setup(const MxLinearArgs& a, int64_t first, int live, int64_t wfirst, int wlive, int wave, int lane) {
+  // The tile of expert e with rows `first` ... + live - 1 and the columns from p0 on.
+  __device__ __forceinline__ void setup(const MxLinearArgs& a, int e, int64_t first, int live, int p0, int wave, int lane) {
+    const int64_t wfirst = (int64_t)e * a.N + p0;
+    const int wlive = min(T::kCols, a.N - p0);
     ld = a.K / 2;
     S = a.K / mx::kBlock;
     steps = (ld + kDB - 1) / kDB;
@@ -431,7 +436,9 @@ struct Rows16 : T {
   PTile pt;
   PScale ps[kParts];
 
-  __device__ __forceinline__ void setup(const MxLinearArgs& a, int64_t first, int live, int64_t wfirst, int wlive, int wave, int lane) {
+  __device__ __forceinline__ void setup(const MxLinearArgs& a, int e, int64_t first, int live, int p0, int wave, int lane) {
+    const int64_t wfirst = (int64_t)e * a.N + p0;
+    const int wlive = min(T::kCols, a.N - p0);
     K = a.K;
     S = K / mx::kBlock;
     steps = (K * 2 + kDB - 1) / kDB;
@@ -533,6 +540,138 @@ struct Rows16 : T {
   }
 };
 
+// Rows' gradient: BQ rows by BP columns of dx; the depth is the weight rows, gate's then
+// up's, 64 a step, in two stages of either operand.  The weights lie across the depth, so
+// they are transposed on their way from LDS to the registers as bf16 weights are: a thread
+// takes the 16 bytes of one block of 32 columns of one weight row, a step ahead in
+// registers, widens them with their scale and leaves them in LDS as bf16.
+template <class T>
+struct Back16 : T {
+  using T::kP;
+  static constexpr int kD = 64, BP = T::kCols;
+  static constexpr int kOutCols = T::kWaveCols;
+  static constexpr int kLineBlocks = BP / mx::kBlock;
+  static constexpr int kPer = kD * kLineBlocks / T::kThreads;  // blocks of a stage a thread widens
+  static_assert(kD * kLineBlocks % T::kThreads == 0, "whole blocks per thread");
+  using QTile = RowTile<T::BQ, T::kWaves>;
+  using PTile = DepthTile<BP, kD, T::kWaves>;
+  static constexpr int kLds = 2 * QTile::kBytes + 2 * PTile::kBytes;
+  __device__ static __forceinline__ int width(const MxLinearArgs& a) { return a.K; }
+
+  __amdgpu_buffer_rsrc_t rq, rw[2], rws[2];
+  int N, S, per, steps, b;  // b: this thread's block of columns
+  QTile qt;
+  u32x4 codes[kPer];
+  uint32_t byte[kPer];
+
+  __device__ __forceinline__ static int line(int i) { return (i * T::kThreads + (int)threadIdx.x) / kLineBlocks; }
+  __device__ __forceinline__ static int block() { return (int)threadIdx.x % kLineBlocks; }
+
+  __device__ __forceinline__ void setup(const MxLinearArgs& a, int e, int64_t first, int live, int p0, int wave, int lane) {
+    const int ldq = a.parts * a.N * 2;
+    N = a.N;
+    S = a.K / mx::kBlock;
+    per = (N + kD - 1) / kD;
+    steps = per * a.parts;
+    rq = resource(static_cast<const char*>(a.dz) + first * ldq);
+    qt.init(wave, lane, [&](int r) { return r < live ? (uint32_t)(r * ldq) : kNoFetch; });
+    b = p0 / mx::kBlock + block();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      rw[h] = resource(static_cast<const char*>(a.w[h < a.parts ? h : 0]) + (int64_t)e * N * S * 16);
+      rws[h] = resource(a.wsb[h < a.parts ? h : 0] + (int64_t)e * N * S);
+    }
+  }
+  // past the last step nothing is left: the loads are issued and fetch nothing
+  __device__ __forceinline__ void issue_q(int s, int wave) const {
+    const int h = s >= per ? 1 : 0, k = s - h * per;
+    qt.load(rq, smem + (s & 1) * QTile::kBytes, wave, (h * N + k * kD) * 2, s < steps ? (N - k * kD) * 2 : 0);
+  }
+  static constexpr int kFetches = 2 * kPer;
+  __device__ __forceinline__ void fetch(int s) {
+    const int h = s >= per ? 1 : 0, k = s - h * per;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int n = k * kD + line(i);
+      const uint32_t at = s < steps && n < N && b < S ? (uint32_t)(n * S + b) : kNoFetch;
+      codes[i] = __builtin_amdgcn_raw_buffer_load_b128(h ? rw[1] : rw[0], at == kNoFetch ? kNoFetch : at * 16, 0, 0);
+      byte[i] = __builtin_amdgcn_raw_buffer_load_b8(h ? rws[1] : rws[0], at, 0, 0);
+    }
+  }
+  __device__ __forceinline__ char* weights(int s) const { return smem + 2 * QTile::kBytes + (s & 1) * PTile::kBytes; }
+  // A block is two 32-byte segments of its line; of 16 lanes that write side by side, half
+  // begin with the other 16 bytes of theirs, so that they reach all banks.
+  __device__ __forceinline__ void widen(int s) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int d = line(i), g = block();
+      const bool turn = kLineBlocks >= 8 ? g & 4 : d & 2;
+      const float f = mx::scale_bits(byte[i]);
+      char* const to = weights(s) + d * PTile::kLine;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<bf16x8*>(to + ((2 * g + k / 2) ^ PTile::swz(d)) * 32 + ((k ^ (turn ? 1 : 0)) & 1) * 16) =
+            mma::fp4x8_to_bf16(turn ? codes[i][k ^ 1] : codes[i][k], f);
+    }
+  }
+  __device__ __forceinline__ void start(int wave) {
+    fetch(0);
+    issue_q(0, wave);
+    widen(0);
+    fetch(1);
+  }
+  template <int L>
+  __device__ __forceinline__ void multiply(int wave, int lane, f32x4 (&acc)[T::kQ][kP]) {
+    using U = Units<L>;
+    const int wq = wave / T::WP, wp = wave % T::WP;
+    bf16x8 q[U::kRing], p[2][kP], upper[kP];
+    const int at[2] = {(lane & 15) * kDB + ((lane >> 4) ^ QTile::swz(lane & 15)) * 16,
+                       (lane & 15) * kDB + ((4 + (lane >> 4)) ^ QTile::swz(lane & 15)) * 16};
+    auto read_q = [&](int s, int u) {
+      const char* b = smem + (s & 1) * QTile::kBytes + wq * 16 * kDB + at[u / L];
+      q[u % U::kRing] = *reinterpret_cast<const bf16x8*>(b + u % L * T::WQ * 16 * kDB);
+    };
+    // A transposing read waits for every direct load before it, needed or not (the compiler
+    // takes it to depend on them), so both halves of a step's weights are read ahead of the
+    // next rows' loads, the upper one into registers of its own.
+    auto read_p = [&](int s) {
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        p[0][j] = PTile::frag(weights(s), wp * T::kWaveCols + j * 16, 0, lane);
+        upper[j] = PTile::frag(weights(s), wp * T::kWaveCols + j * 16, 1, lane);
+      }
+    };
+    wait_and_meet<0>();
+    read_p(0);
+    issue_q(1, wave);
+#pragma unroll
+    for (int u = 0; u < U::kAhead; ++u) read_q(0, u);
+    for (int s = 0; s < steps; ++s) {
+      // the next step's weights, in the place of the last one's, which were in registers at
+      // the last meeting; then those of the step after it
+      widen(s + 1);
+      fetch(s + 2);
+#pragma unroll
+      for (int j = 0; j < kP; ++j) p[1][j] = upper[j];
+      each<U::kCount>([&](auto index) {
+        constexpr int u = decltype(index)::value;
+        if constexpr (u == U::kMeet) {
+          // this step's operands are in registers and the next one's in LDS; behind its rows
+          // there are the weights just asked for
+          wait_and_meet<kFetches>();
+          read_p(s + 1);
+          issue_q(s + 2, wave);
+        }
+        read_q(u < U::kMeet ? s : s + 1, u < U::kMeet ? u + U::kAhead : u - U::kMeet);
+        __builtin_amdgcn_sched_barrier(0);  // the reads are on their way before the products
+#pragma unroll
+        for (int j = 0; j < kP; ++j) acc[u % L][j] = mma::mfma(p[u / L][j], q[u % U::kRing], acc[u % L][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    }
+  }
+};
+
 // Tiles one after another (SERIES): workgroup b takes tile b / 8 and every (grid / 8)-th one
 // after it of the run of tiles that XCD b % 8 is dealt.  A tile's first stages are loaded
 // while the results of the one before it leave; with a tile per workgroup the search for it,
@@ -545,7 +684,7 @@ template <class C, bool SERIES>
 __global__ __launch_bounds__(C::kThreads, 2) void linear_mx_kernel(MxLinearArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Runs runs;
-  runs.scan(a, C::BQ, (a.N + C::kCols - 1) / C::kCols);
+  runs.scan(a, C::BQ, (C::width(a) + C::kCols - 1) / C::kCols);
   const int64_t b = row::block_index();
   const int chunk = (runs.total + 7) / 8, base = (int)(b & 7) * chunk, stride = (int)gridDim.x >> 3;
   int64_t at = b >> 3;
@@ -560,7 +699,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void linear_mx_kernel(MxLinearArgs 
     first = (int64_t)it.row0 + it.tq * C::BQ;
     live = min(C::BQ, it.count - it.tq * C::BQ);
     p0 = it.tp * C::kCols;
-    core.setup(a, first, live, (int64_t)it.e * a.N + p0, min(C::kCols, a.N - p0), wave, lane);
+    core.setup(a, it.e, first, live, p0, wave, lane);
     core.start(wave);
   };
   begin();
@@ -708,121 +847,6 @@ __global__ __launch_bounds__(WC* WK * 64) void linear_mx_few_kernel(MxLinearArgs
   }
 }
 
-// ------------------------------------------------------------- backward x --
-
-// One workgroup: BQ rows by BP columns of dx; the depth is the weight rows, gate's then
-// up's.  A thread takes the 16 bytes of one block of 32 columns of one weight row, a step
-// ahead in registers, and leaves it in LDS as bf16 lines, from where it is transposed on
-// its way to the matrix cores as bf16 weights are.
-template <int BQ, int BP, int WQ, int WP>
-__global__ __launch_bounds__(WQ* WP * 64, 2) void linear_mx_backward_x_kernel(MxLinearArgs a) {
-  constexpr int kWaves = WQ * WP, kQ = BQ / WQ / 16, kP = BP / WP / 16, kD = 64;
-  constexpr int kPer = kD * BP / mx::kBlock / (kWaves * 64);  // blocks of a stage a thread widens
-  static_assert(kPer >= 1 && kD * BP / mx::kBlock % (kWaves * 64) == 0, "whole blocks per thread");
-  using QTile = RowTile<BQ, kWaves>;
-  using PTile = DepthTile<BP, kD, kWaves>;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wq = wave / WP, wp = wave % WP;
-  const Item it = find_item(a, row::block_index(), BQ, (a.K + BP - 1) / BP);
-  if (it.e < 0) return;
-  const int q0 = it.tq * BQ, p0 = it.tp * BP;
-  const int live = min(BQ, it.count - q0);
-  const int64_t first = (int64_t)it.row0 + q0;
-  const int ldq = a.parts * a.N * 2, S = a.K / mx::kBlock;
-  QTile qt;
-  qt.init(wave, lane, [&](int r) { return r < live ? (uint32_t)(r * ldq) : kNoFetch; });
-  // the depth runs over the N columns of dz's first part, then of its second
-  const int per = (a.N + kD - 1) / kD, steps = per * a.parts;
-  const __amdgpu_buffer_rsrc_t rq = resource(static_cast<const char*>(a.dz) + first * ldq);
-  // past the last step nothing is left: the loads are issued and fetch nothing
-  auto issue_q = [&](int s) {
-    const int h = s >= per ? 1 : 0, k = s - h * per;
-    qt.load(rq, smem + (s % 3) * QTile::kBytes, wave, (h * a.N + k * kD) * 2, s < steps ? (a.N - k * kD) * 2 : 0);
-  };
-  char* const weights = smem + 3 * QTile::kBytes;
-  // this thread's blocks: line d of the stage, block g of its BP / 32
-  constexpr int kLineBlocks = BP / mx::kBlock;
-  uint4 codes[kPer];
-  uint32_t byte[kPer];
-  auto fetch = [&](int s) {
-    const int h = s >= per ? 1 : 0, k = s - h * per;
-    const uint8_t* w = static_cast<const uint8_t*>(a.w[h]);
-    const uint8_t* ws = a.wsb[h];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int at = i * kWaves * 64 + (int)threadIdx.x, d = at / kLineBlocks, g = at % kLineBlocks;
-      const int n = k * kD + d, b = p0 / mx::kBlock + g;
-      codes[i] = make_uint4(0, 0, 0, 0);
-      byte[i] = mx::kZeroByte;
-      if (s < steps && n < a.N && b < S) {
-        const int64_t r = (int64_t)it.e * a.N + n;
-        codes[i] = *reinterpret_cast<const uint4*>(w + r * (a.K / 2) + b * 16);
-        byte[i] = ws[r * S + b];
-      }
-    }
-  };
-  auto widen = [&](int stage) {
-    char* base = weights + stage * PTile::kBytes;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int at = i * kWaves * 64 + (int)threadIdx.x, d = at / kLineBlocks, g = at % kLineBlocks;
-      const float f = mx::scale_bits(byte[i]);
-      const uint32_t c[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<bf16x8*>(base + d * PTile::kLine + (((2 * g + k / 2) ^ PTile::swz(d)) * 32) + (k & 1) * 16) =
-            mma::fp4x8_to_bf16(c[k], f);
-    }
-  };
-  f32x4 acc[kQ][kP];
-#pragma unroll
-  for (int i = 0; i < kQ; ++i)
-#pragma unroll
-    for (int j = 0; j < kP; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  fetch(0);
-  issue_q(0);
-  widen(0);
-  fetch(1);
-  issue_q(1);
-  auto multiply = [&](auto live_subtiles) {
-    constexpr int L = decltype(live_subtiles)::value;
-    for (int s = 0; s < steps; ++s) {
-      wait_and_meet<0>();
-      widen((s + 1) & 1);  // the other stage, whose readers have passed the barrier
-      fetch(s + 2);
-      issue_q(s + 2);
-      const char* b = smem + (s % 3) * QTile::kBytes;
-      const char* w = weights + (s & 1) * PTile::kBytes;
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        bf16x8 q[L], p[kP];
-#pragma unroll
-        for (int i = 0; i < L; ++i) q[i] = QTile::frag(b, q_row<WQ>(wq, i), kk, lane);
-#pragma unroll
-        for (int j = 0; j < kP; ++j) p[j] = PTile::frag(w, wp * (BP / WP) + j * 16, kk, lane);
-#pragma unroll
-        for (int j = 0; j < kP; ++j)
-#pragma unroll
-          for (int i = 0; i < L; ++i) acc[i][j] = mma::mfma(p[j], q[i], acc[i][j]);
-      }
-    }
-  };
-  by_live_subtiles<kQ>((live - wq * 16 + 16 * WQ - 1) / (16 * WQ), multiply);
-  wait_and_meet<0>();
-  using Rows = OutTile<BQ, BP * 2, kWaves * 64>;
-  static_assert(BQ * BP * 2 <= 3 * QTile::kBytes + 2 * PTile::kBytes, "the output tile fits where the stages were");
-#pragma unroll
-  for (int i = 0; i < kQ; ++i)
-#pragma unroll
-    for (int j = 0; j < kP; ++j) {
-      const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      Rows::put(smem, q_row<WQ>(wq, i) + (lane & 15), (wp * (BP / WP) + j * 16 + (lane >> 4) * 4) * 2, pack4(v));
-    }
-  __syncthreads();
-  Rows::flush(smem, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + first * a.K + p0), (int64_t)a.K * 2, live,
-              min(BP, a.K - p0) * 2);
-}
-
 // ---------------------------------------------------------------- launch --
 
 // Instantiated by name: the host pass of this compiler otherwise leaves out the
@@ -856,7 +880,12 @@ MOE_MX_ROWS16(false, true)
 MOE_MX_ROWS16(true, false)
 MOE_MX_ROWS16(true, true)
 #undef MOE_MX_ROWS16
-template __global__ void linear_mx_backward_x_kernel<128, 128, 2, 2>(MxLinearArgs);
+template <int BQ, int BP, int WQ, int WP>
+using B16 = Back16<Shape<false, BQ, BP, WQ, WP>>;
+template __global__ void linear_mx_kernel<B16<256, 256, 2, 4>, false>(MxLinearArgs);
+template __global__ void linear_mx_kernel<B16<128, 128, 2, 2>, true>(MxLinearArgs);
+template __global__ void linear_mx_kernel<B16<64, 128, 2, 2>, false>(MxLinearArgs);
+template __global__ void linear_mx_kernel<B16<32, 128, 2, 2>, false>(MxLinearArgs);
 
 template <typename K>
 hipError_t launch(K kern, int64_t items, int threads, int lds, const MxLinearArgs& a, hipStream_t s,
@@ -878,11 +907,11 @@ hipError_t run_few(const MxLinearArgs& a, hipStream_t s) {
 // workgroups on each as have room in LDS.
 constexpr int64_t kCUs = 256;
 template <class C, bool SERIES>
-hipError_t run_tiles(const MxLinearArgs& a, hipStream_t s) {
+hipError_t run_tiles(const MxLinearArgs& a, int cols, hipStream_t s) {
   static std::atomic<size_t> allowed[kMaxCachedDevices];
   constexpr int lds = C::kLds + C::kWaves * 16 * C::kOutCols * 2;
   static_assert(lds <= 160 * 1024, "a compute unit's LDS");
-  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, C::BQ) * ((a.N + C::kCols - 1) / C::kCols);
+  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, C::BQ) * ((cols + C::kCols - 1) / C::kCols);
   void (*const kern)(MxLinearArgs) = &linear_mx_kernel<C, SERIES>;
   return launch(kern, SERIES ? std::min(items, kCUs * (160 * 1024 / lds)) : items, C::kThreads, lds, a, s, allowed);
 }
@@ -905,25 +934,18 @@ template <bool GATED, bool ALIGNED>
 hipError_t rows4_by_shape(const MxLinearArgs& a, hipStream_t s) {
   if (mean_rows(a) <= kFewRows) return run_few<true, GATED, 2, 8>(a, s);
   const int64_t cols = a.parts * (int64_t)a.N;
-  if (tiles(a, cols, 128) < 256) return run_tiles<R4<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2, 3, 4>, false>(a, s);
-  if (wide_tiles(a, cols)) return run_tiles<R4<GATED, ALIGNED, 256, 256, 2, 4, 2, 2>, false>(a, s);
-  return run_tiles<R4<GATED, ALIGNED, 128, 128, 2, 2, 2, 2>, true>(a, s);
+  if (tiles(a, cols, 128) < 256) return run_tiles<R4<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2, 3, 4>, false>(a, a.N, s);
+  if (wide_tiles(a, cols)) return run_tiles<R4<GATED, ALIGNED, 256, 256, 2, 4, 2, 2>, false>(a, a.N, s);
+  return run_tiles<R4<GATED, ALIGNED, 128, 128, 2, 2, 2, 2>, true>(a, a.N, s);
 }
 
 template <bool GATED, bool ALIGNED>
 hipError_t rows16_by_shape(const MxLinearArgs& a, hipStream_t s) {
   if (mean_rows(a) <= kFewRows) return run_few<false, GATED, 2, 8>(a, s);
   const int64_t cols = a.parts * (int64_t)a.N;
-  if (tiles(a, cols, 128) < 256) return run_tiles<R16<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2>, false>(a, s);
-  if (wide_tiles(a, cols)) return run_tiles<R16<GATED, ALIGNED, 256, 256, 2, 4>, false>(a, s);
-  return run_tiles<R16<GATED, ALIGNED, 128, 128, 2, 2>, true>(a, s);
-}
-
-template <int BQ, int BP, int WQ, int WP>
-hipError_t run_backward_x(const MxLinearArgs& a, hipStream_t s) {
-  static std::atomic<size_t> allowed[kMaxCachedDevices];
-  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, BQ) * ((a.K + BP - 1) / BP);
-  return launch(&linear_mx_backward_x_kernel<BQ, BP, WQ, WP>, items, WQ * WP * 64, (3 * BQ + 2 * BP) * 128, a, s, allowed);
+  if (tiles(a, cols, 128) < 256) return run_tiles<R16<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2>, false>(a, a.N, s);
+  if (wide_tiles(a, cols)) return run_tiles<R16<GATED, ALIGNED, 256, 256, 2, 4>, false>(a, a.N, s);
+  return run_tiles<R16<GATED, ALIGNED, 128, 128, 2, 2>, true>(a, a.N, s);
 }
 
 }  // namespace
@@ -939,6 +961,11 @@ hipError_t launch_linear_mx(const MxLinearArgs& a, hipStream_t s) {
   return gated ? rows16_by_shape<true, false>(a, s) : rows16_by_shape<false, false>(a, s);
 }
 
-hipError_t launch_linear_mx_backward_x(const MxLinearArgs& a, hipStream_t s) { return run_backward_x<128, 128, 2, 2>(a, s); }
+hipError_t launch_linear_mx_backward_x(const MxLinearArgs& a, hipStream_t s) {
+  if (wide_tiles(a, a.K)) return run_tiles<B16<256, 256, 2, 4>, false>(a, a.K, s);
+  if (tiles(a, a.K, 128) < 256)
+    return mean_rows(a) <= 64 ? run_tiles<B16<32, 128, 2, 2>, false>(a, a.K, s) : run_tiles<B16<64, 128, 2, 2>, false>(a, a.K, s);
+  return run_tiles<B16<128, 128, 2, 2>, true>(a, a.K, s);
+}
 
 }  // namespace moe
