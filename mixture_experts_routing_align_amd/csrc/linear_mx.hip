@@ -30,8 +30,6 @@ extern __shared__ __attribute__((aligned(1024))) char smem[];
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ u32x4 as_vec(uint4 v) { return u32x4{v.x, v.y, v.z, v.w}; }
-
 // Calls f with 0, 1, ... N - 1, each a constant.
 template <int N, int I = 0, typename F>
 __device__ __forceinline__ void each(F f) {
@@ -760,45 +758,55 @@ __global__ __launch_bounds__(WC* WK * 64) void linear_mx_few_kernel(MxLinearArgs
   f32x4 acc[kParts];
 #pragma unroll
   for (int h = 0; h < kParts; ++h) acc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int c = wk; c * kBlocks < S; c += WK) {
+  // a chunk of weights on its way while the one before it is multiplied (rows come from L2)
+  struct Chunk {
+    u32x4 w[kParts][2];
+    uint32_t s[kParts][2];
+  };
+  auto fetch = [&](int c) {
+    Chunk t;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int b = c * kBlocks + quad * 2 + i;
-      const bool in = b < S;
-      const int at = in ? b : 0;
-      uint4 wv[kParts];
-      uint32_t wb[kParts];
+      const int b = c * kBlocks + quad * 2 + i, at = b < S ? b : 0;
 #pragma unroll
       for (int h = 0; h < kParts; ++h) {
-        wv[h] = *reinterpret_cast<const uint4*>(w[h] + at * 16);
-        wb[h] = sw[h][at];
-        if (!in) {
-          wv[h] = make_uint4(0, 0, 0, 0);
-          wb[h] = mx::kZeroByte;
-        }
+        t.w[h][i] = *reinterpret_cast<const u32x4*>(w[h] + at * 16);
+        t.s[h][i] = sw[h][at];
       }
-      if constexpr (ROWS4) {
-        uint4 xv = *reinterpret_cast<const uint4*>(x + at * 16);
-        uint32_t xb = sx[at];
-        if (!in) {
-          xv = make_uint4(0, 0, 0, 0);
-          xb = mx::kZeroByte;
-        }
+    }
+    return t;
+  };
+  Chunk next = fetch(wk);
+  for (int c = wk; c * kBlocks < S; c += WK) {
+    const Chunk now = next;
+    u32x4 xv[2][ROWS4 ? 1 : 4];
+    uint32_t xb[2];
 #pragma unroll
-        for (int h = 0; h < kParts; ++h) acc[h] = mx::mfma<0, 0>(as_vec(wv[h]), wb[h], as_vec(xv), xb, acc[h]);
-      } else {
-        uint4 xv[4];
+    for (int i = 0; i < 2; ++i) {
+      const int b = c * kBlocks + quad * 2 + i, at = b < S ? b : 0;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          xv[d] = *reinterpret_cast<const uint4*>(x + at * 64 + d * 16);
-          if (!in) xv[d] = make_uint4(0, 0, 0, 0);
-        }
+      for (int d = 0; d < (ROWS4 ? 1 : 4); ++d) xv[i][d] = *reinterpret_cast<const u32x4*>(x + at * (ROWS4 ? 16 : 64) + d * 16);
+      xb[i] = ROWS4 ? sx[at] : 0u;
+    }
+    next = fetch(c + WK);
 #pragma unroll
-        for (int h = 0; h < kParts; ++h) {
-          const float f = mx::scale_bits(wb[h]);
-          const uint32_t d[4] = {wv[h].x, wv[h].y, wv[h].z, wv[h].w};
+    for (int i = 0; i < 2; ++i) {
+      const bool in = c * kBlocks + quad * 2 + i < S;
+      const u32x4 zero{0u, 0u, 0u, 0u};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[h] = mma::mfma(mma::fp4x8_to_bf16(d[k], f), mma::as_bf16x8(xv[k]), acc[h]);
+      for (int d = 0; d < (ROWS4 ? 1 : 4); ++d)
+        if (!in) xv[i][d] = zero;
+#pragma unroll
+      for (int h = 0; h < kParts; ++h) {
+        const u32x4 wv = in ? now.w[h][i] : zero;
+        const uint32_t wb = in ? now.s[h][i] : (uint32_t)mx::kZeroByte;
+        if constexpr (ROWS4) {
+          acc[h] = mx::mfma<0, 0>(wv, wb, xv[i][0], in ? xb[i] : (uint32_t)mx::kZeroByte, acc[h]);
+        } else {
+          const float f = mx::scale_bits(wb);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            acc[h] = mma::mfma(mma::fp4x8_to_bf16(wv[k], f), __builtin_bit_cast(bf16x8, xv[i][k]), acc[h]);
         }
       }
     }
@@ -851,8 +859,10 @@ __global__ __launch_bounds__(WC* WK * 64) void linear_mx_few_kernel(MxLinearArgs
 
 // Instantiated by name: the host pass of this compiler otherwise leaves out the
 // launch stubs of some kernel templates that are only reached through pointers.
-#define MOE_MX_TILES(R, G)                                          \
-  template __global__ void linear_mx_few_kernel<R, G, 2, 8>(MxLinearArgs);
+#define MOE_MX_TILES(R, G)                                                     \
+  template __global__ void linear_mx_few_kernel<R, G, 1, 8>(MxLinearArgs);     \
+  template __global__ void linear_mx_few_kernel<R, G, 2, 8>(MxLinearArgs);     \
+  template __global__ void linear_mx_few_kernel<R, G, 2, 2>(MxLinearArgs);
 MOE_MX_TILES(false, false)
 MOE_MX_TILES(false, true)
 MOE_MX_TILES(true, false)
@@ -863,7 +873,8 @@ using R4 = Rows4<Shape<GATED, BQ, BP, WQ, WP>, ALIGNED, STAGES, G>;
 #define MOE_MX_ROWS4(G, A)                                                     \
   template __global__ void linear_mx_kernel<R4<G, A, 256, 256, 2, 4, 2, 2>, false>(MxLinearArgs); \
   template __global__ void linear_mx_kernel<R4<G, A, 128, 128, 2, 2, 2, 2>, true>(MxLinearArgs); \
-  template __global__ void linear_mx_kernel<R4<G, A, 64, 64, G ? 4 : 2, G ? 1 : 2, 3, 4>, false>(MxLinearArgs);
+  template __global__ void linear_mx_kernel<R4<G, A, 64, 128, 2, 2, 2, 2>, false>(MxLinearArgs);   \
+  template __global__ void linear_mx_kernel<R4<G, A, 32, 128, 2, 2, 2, 2>, true>(MxLinearArgs);
 MOE_MX_ROWS4(false, false)
 MOE_MX_ROWS4(false, true)
 MOE_MX_ROWS4(true, false)
@@ -874,7 +885,9 @@ using R16 = Rows16<Shape<GATED, BQ, BP, WQ, WP>, ALIGNED>;
 #define MOE_MX_ROWS16(G, A)                                                    \
   template __global__ void linear_mx_kernel<R16<G, A, 256, 256, 2, 4>, false>(MxLinearArgs); \
   template __global__ void linear_mx_kernel<R16<G, A, 128, 128, 2, 2>, true>(MxLinearArgs); \
-  template __global__ void linear_mx_kernel<R16<G, A, 64, 64, G ? 4 : 2, G ? 1 : 2>, false>(MxLinearArgs);
+  template __global__ void linear_mx_kernel<R16<G, A, 64, 64, G ? 4 : 2, G ? 1 : 2>, false>(MxLinearArgs); \
+  template __global__ void linear_mx_kernel<R16<G, A, 32, 64, 2, G ? 1 : 2>, false>(MxLinearArgs); \
+  template __global__ void linear_mx_kernel<R16<G, A, 32, 128, 2, 2>, true>(MxLinearArgs);
 MOE_MX_ROWS16(false, false)
 MOE_MX_ROWS16(false, true)
 MOE_MX_ROWS16(true, false)
@@ -884,8 +897,8 @@ template <int BQ, int BP, int WQ, int WP>
 using B16 = Back16<Shape<false, BQ, BP, WQ, WP>>;
 template __global__ void linear_mx_kernel<B16<256, 256, 2, 4>, false>(MxLinearArgs);
 template __global__ void linear_mx_kernel<B16<128, 128, 2, 2>, true>(MxLinearArgs);
-template __global__ void linear_mx_kernel<B16<64, 128, 2, 2>, false>(MxLinearArgs);
-template __global__ void linear_mx_kernel<B16<32, 128, 2, 2>, false>(MxLinearArgs);
+template __global__ void linear_mx_kernel<B16<64, 128, 2, 2>, true>(MxLinearArgs);
+template __global__ void linear_mx_kernel<B16<32, 128, 2, 2>, true>(MxLinearArgs);
 
 template <typename K>
 hipError_t launch(K kern, int64_t items, int threads, int lds, const MxLinearArgs& a, hipStream_t s,
@@ -925,26 +938,64 @@ int64_t tiles(const MxLinearArgs& a, int64_t cols, int64_t edge) {
   return (a.rows + edge - 1) / edge * ((cols + edge - 1) / edge);
 }
 
+// The depth-split form: few tiles in all (of 16 rows and 32 columns), which the staged forms
+// walk one memory trip after another.  Dense rows of bf16 by 2048 x 2048: 16 rows 8.6 us,
+// 12.9 in 32 x 64 tiles; 64 rows 9.1 and 13.1; 256 rows 24.5 and 14.9; 16 rows by 8192 x
+// 7168 25 and 44 (MXFP4 rows: 15 and 15).  Over many experts it is the slower one, 64 rows on
+// 51 of 128, SwiGLU of 2 x 768 x 2048: 33 us, 30 in 32 x 128 tiles (MXFP4 rows: 28 and 19).
+bool few_tiles(const MxLinearArgs& a) {
+  const int64_t mean = mean_rows(a);
+  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, 16) * ((a.N + 31) / 32);
+  return items <= (mean <= 32 ? 1024 : mean <= 64 ? 256 : 0);
+}
+
+// 8 waves along the depth while its tiles are fewer than 512, of half the columns where the
+// result allows it (8 dense rows, 2048 x 7168: 10 us, 16 on 32 columns); else 2 (16384
+// columns: 30 us, 31 with 8).
+template <bool ROWS4, bool GATED>
+hipError_t run_few_tiles(const MxLinearArgs& a, hipStream_t s) {
+  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, 16) * ((a.N + 31) / 32);
+  if (items >= 512) return run_few<ROWS4, GATED, 2, 2>(a, s);
+  return a.ysb != nullptr ? run_few<ROWS4, GATED, 2, 8>(a, s) : run_few<ROWS4, GATED, 1, 8>(a, s);
+}
+
+// 256-wide tiles read each operand byte half as often as 128-wide ones and are four times the
+// work: taken where they fill the GPU and the runs fill most of them (SwiGLU of 2 x 768 x
+// 2048: 32768 rows over 128 experts 115 us, 118 in 128-wide ones; 8192 rows 73 and 63.  4096
+// rows to 4 of 16 experts, 2 x 2048 x 7168: 305 and 367.  bf16 rows, the same three: 256 and
+// 260, 138 and 114, 809 and 942).
 bool wide_tiles(const MxLinearArgs& a, int64_t cols) { return tiles(a, cols, 256) >= 256 && mean_rows(a) >= 160; }
 
-// Rows per expert up to which the depth-split kernel is taken.
-constexpr int64_t kFewRows = 32;
+// Rows per expert on average up to which tiles have 32 rows: SwiGLU of 2 x 768 x 2048 over
+// 128 experts, MXFP4 rows, in 32 x 128 and 128 x 128 tiles: 8 rows an expert 42 and 50 us,
+// 24 52 and 56, 48 64 and 62 (bf16 rows: 61 and 82, 83 and 91, 111 and 110).
+constexpr int64_t kShortRuns = 40;
 
 template <bool GATED, bool ALIGNED>
 hipError_t rows4_by_shape(const MxLinearArgs& a, hipStream_t s) {
-  if (mean_rows(a) <= kFewRows) return run_few<true, GATED, 2, 8>(a, s);
+  if (few_tiles(a)) return run_few_tiles<true, GATED>(a, s);
   const int64_t cols = a.parts * (int64_t)a.N;
-  if (tiles(a, cols, 128) < 256) return run_tiles<R4<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2, 3, 4>, false>(a, a.N, s);
   if (wide_tiles(a, cols)) return run_tiles<R4<GATED, ALIGNED, 256, 256, 2, 4, 2, 2>, false>(a, a.N, s);
+  if (mean_rows(a) <= kShortRuns) return run_tiles<R4<GATED, ALIGNED, 32, 128, 2, 2, 2, 2>, true>(a, a.N, s);
+  // few 128-wide tiles: smaller ones (1024 dense rows by 4096 x 2048: 13.1 us, 14.8; 2048 x
+  // 2048: 12.8 and 14.7; in 64 x 64 16.7)
+  if (tiles(a, cols, 128) < 256) return run_tiles<R4<GATED, ALIGNED, 64, 128, 2, 2, 2, 2>, false>(a, a.N, s);
   return run_tiles<R4<GATED, ALIGNED, 128, 128, 2, 2, 2, 2>, true>(a, a.N, s);
 }
 
 template <bool GATED, bool ALIGNED>
 hipError_t rows16_by_shape(const MxLinearArgs& a, hipStream_t s) {
-  if (mean_rows(a) <= kFewRows) return run_few<false, GATED, 2, 8>(a, s);
+  if (few_tiles(a)) return run_few_tiles<false, GATED>(a, s);
   const int64_t cols = a.parts * (int64_t)a.N;
-  if (tiles(a, cols, 128) < 256) return run_tiles<R16<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2>, false>(a, a.N, s);
   if (wide_tiles(a, cols)) return run_tiles<R16<GATED, ALIGNED, 256, 256, 2, 4>, false>(a, a.N, s);
+  if (mean_rows(a) <= kShortRuns) return run_tiles<R16<GATED, ALIGNED, 32, 128, 2, 2>, true>(a, a.N, s);
+  // few tiles: smaller ones, of which more than one shares a compute unit (dense rows by 2048 x
+  // 2048, in 32 x 64, 64 x 64 and 128 x 128: 256 rows 14.9, 16.5 and 28.5 us; 512 15.9, 16.8 and
+  // 26; 2048 36, 26 and 28)
+  if (tiles(a, cols, 128) < 256) {
+    if (tiles(a, cols, 64) <= 256) return run_tiles<R16<GATED, ALIGNED, 32, 64, 2, GATED ? 1 : 2>, false>(a, a.N, s);
+    return run_tiles<R16<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2>, false>(a, a.N, s);
+  }
   return run_tiles<R16<GATED, ALIGNED, 128, 128, 2, 2>, true>(a, a.N, s);
 }
 
@@ -962,9 +1013,12 @@ hipError_t launch_linear_mx(const MxLinearArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_linear_mx_backward_x(const MxLinearArgs& a, hipStream_t s) {
+  // 4096 rows to 8 of 128 experts, 2 x 768 x 2048: 287 us, 309 in 128-wide tiles
   if (wide_tiles(a, a.K)) return run_tiles<B16<256, 256, 2, 4>, false>(a, a.K, s);
-  if (tiles(a, a.K, 128) < 256)
-    return mean_rows(a) <= 64 ? run_tiles<B16<32, 128, 2, 2>, false>(a, a.K, s) : run_tiles<B16<64, 128, 2, 2>, false>(a, a.K, s);
+  // the same weights, 16 rows an expert: 85 us, 109 in 128 x 128 tiles; 48 rows 130 and 128
+  if (mean_rows(a) <= kShortRuns) return run_tiles<B16<32, 128, 2, 2>, true>(a, a.K, s);
+  // few tiles: 64 rows on each of 8 experts 20 us, 25; 1024 dense rows by 2 x 2048 x 2048 43, 54
+  if (tiles(a, a.K, 128) < 256) return run_tiles<B16<64, 128, 2, 2>, true>(a, a.K, s);
   return run_tiles<B16<128, 128, 2, 2>, true>(a, a.K, s);
 }
 

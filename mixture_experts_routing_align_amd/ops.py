@@ -598,26 +598,31 @@ def moe_grouped_linear_mxfp4_backward_x(dz: torch.Tensor, w, expert_offsets: Opt
 
 # ------------------------------------------------------ gradients, clipped --
 
-def _grad_list(grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]], dev: int):
-    """The gradients and their outputs as the C list, packed."""
-    packed = array("q")
-    for i, g in enumerate(grads):
-        if not (isinstance(g, torch.Tensor) and g.dtype in _STREAM_TYPES and g.is_contiguous() and g.get_device() == dev):
-            _matrix(g, f"gradient {i}", _STREAM, None, dev)
-        at = g.data_ptr()
-        to = at
-        if out is not None:
-            o = out[i]
-            _matrix(o, f"output {i}", (g.dtype,), g.shape, dev)
-            to = o.data_ptr()
-        packed.extend((at, to, g.numel(), _STREAM_TYPES[g.dtype]))
-    return packed
-
-
-def _grad_device(grads, out, what: str) -> int:
+def _grads(grads, out, what: str):
+    """(device, the gradients and their outputs packed as the C list).  A step has hundreds
+    of them, so each is looked at in a few plain expressions that only a refusal repeats."""
     _need(isinstance(grads, (list, tuple)) and len(grads) > 0, what + " takes a list of at least one gradient")
     _need(out is None or (isinstance(out, (list, tuple)) and len(out) == len(grads)), "out must match the gradients")
-    return _device(grads[0], "gradient 0")
+    dev = _device(grads[0], "gradient 0")
+    try:
+        types = [_STREAM_TYPES[g.dtype] for g in grads]
+        fine = all([g.is_contiguous() and g.get_device() == dev for g in grads])
+        sizes = [g.numel() for g in grads]
+        if out is not None:
+            fine = fine and all([o.is_contiguous() and o.get_device() == dev for o in out])
+            fine = fine and sizes == [o.numel() for o in out] and types == [_STREAM_TYPES[o.dtype] for o in out]
+    except (KeyError, AttributeError):
+        fine = False
+    if not fine:
+        for i, g in enumerate(grads):
+            _matrix(g, f"gradient {i}", _STREAM, None, dev)
+            if out is not None:
+                _matrix(out[i], f"output {i}", (g.dtype,), None, dev)
+                _need(out[i].numel() == g.numel(), f"output {i} must have as many elements as its gradient")
+        raise ValueError(what + ": gradients that cannot be taken")
+    at = [g.data_ptr() for g in grads]
+    to = at if out is None else [o.data_ptr() for o in out]
+    return dev, array("q", [v for entry in zip(at, to, sizes, types) for v in entry])
 
 
 def moe_grad_norm(grads: Sequence[torch.Tensor], norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -625,8 +630,7 @@ def moe_grad_norm(grads: Sequence[torch.Tensor], norm: Optional[torch.Tensor] = 
     any shapes), float32 [1] on the device; summed in 64 bits in a fixed order.  Where the
     gradients are spread over GPUs, the norms' squares are what to add up before
     moe_grad_clip."""
-    dev = _grad_device(grads, None, "moe_grad_norm")
-    packed = _grad_list(grads, None, dev)
+    dev, packed = _grads(grads, None, "moe_grad_norm")
     norm = _out(norm, (1,), torch.float32, grads[0], stream, "norm", dev)
     lib = _ffi.load()
     nbytes = lib.moe_grad_norm_workspace_bytes(len(grads))
@@ -640,9 +644,8 @@ def moe_grad_clip(grads: Sequence[torch.Tensor], norm: torch.Tensor, max_norm: f
                   out: Optional[Sequence[torch.Tensor]] = None, stream=None) -> List[torch.Tensor]:
     """The gradients times ``max_norm / norm`` where `norm` (float32 [1] on the device) is
     past `max_norm`, else unchanged, as where the norm is NaN or infinite; in place, or
-    into `out`.  Returns the list written."""
-    dev = _grad_device(grads, out, "moe_grad_clip")
-    packed = _grad_list(grads, out, dev)
+    into `out` (tensors of the same types and numbers of elements).  Returns the list written."""
+    dev, packed = _grads(grads, out, "moe_grad_clip")
     _matrix(norm, "norm", _F32, (1,), dev)
     _check(_ffi.load().moe_grad_clip(packed.buffer_info()[0], len(grads), norm.data_ptr(), max_norm, _stream(stream, dev)))
     return list(grads if out is None else out)
@@ -652,8 +655,7 @@ def moe_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Opti
                        norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """moe_grad_norm, then moe_grad_clip with its result, in fewer launches: the gradients
     are scaled in place (or into `out`), their norm before that is returned."""
-    dev = _grad_device(grads, out, "moe_clip_grad_norm")
-    packed = _grad_list(grads, out, dev)
+    dev, packed = _grads(grads, out, "moe_clip_grad_norm")
     norm = _out(norm, (1,), torch.float32, grads[0], stream, "norm", dev)
     lib = _ffi.load()
     nbytes = lib.moe_grad_norm_workspace_bytes(len(grads))
