@@ -120,21 +120,31 @@ struct Shape {
   __device__ static __forceinline__ int width(const MxLinearArgs& a) { return a.N; }
 };
 
-// Rows below `live` of the 16 rows of BYTES that a wave has gathered at `lds`, their first
-// `valid` bytes (a multiple of 16), to dst; ld bytes from row to row.
+// 16 rows of BYTES that a wave gathers in LDS to store them as lines.  Pieces of 16 bytes
+// are swizzled by which 256 bytes of LDS (all banks) their row lies in, so that 16 rows'
+// same piece spreads over them.
 template <int BYTES>
-__device__ __forceinline__ void flush16(const char* lds, char* dst, int64_t ld, int live, int valid) {
-  using Rows = OutTile<16, BYTES, 64>;
-  const int lane = threadIdx.x & 63;
-  asm volatile("" ::: "memory");  // a wave's LDS operations are done in order
-#pragma unroll
-  for (int i = 0; i < 16 * Rows::kPieces; i += 64) {
-    const int r = (i + lane) / Rows::kPieces, g = (i + lane) % Rows::kPieces;
-    if (r < min(live, 16) && g * 16 < valid)
-      *reinterpret_cast<u32x4*>(dst + r * ld + g * 16) = *reinterpret_cast<const u32x4*>(lds + r * BYTES + ((g ^ (r & Rows::kMask)) << 4));
+struct WaveRows {
+  static constexpr int kPieces = BYTES / 16;
+  __device__ static __forceinline__ int swz(int r) { return (r * BYTES / 256) & (kPieces - 1); }
+  template <typename V>
+  __device__ static __forceinline__ void put(char* lds, int r, int byte, V v) {
+    *reinterpret_cast<V*>(lds + r * BYTES + (((byte >> 4) ^ swz(r)) << 4) + (byte & 15)) = v;
   }
-  asm volatile("" ::: "memory");
-}
+  // The rows below `live`, their first `valid` bytes (a multiple of 16), to dst; ld bytes from
+  // row to row.
+  __device__ static __forceinline__ void flush(const char* lds, char* dst, int64_t ld, int live, int valid) {
+    const int lane = threadIdx.x & 63;
+    asm volatile("" ::: "memory");  // a wave's LDS operations are done in order
+#pragma unroll
+    for (int i = 0; i < 16 * kPieces; i += 64) {
+      const int r = (i + lane) / kPieces, g = (i + lane) % kPieces;
+      if (r < min(live, 16) && g * 16 < valid)
+        *reinterpret_cast<u32x4*>(dst + r * ld + g * 16) = *reinterpret_cast<const u32x4*>(lds + r * BYTES + ((g ^ swz(r)) << 4));
+    }
+    asm volatile("" ::: "memory");
+  }
+};
 
 // The end of a tile: bias, activation and residual on the float32 sums, pre-activations,
 // bf16 or MXFP4 rows.  Lane l holds row l % 16 and 4 consecutive columns of each subtile,
@@ -183,8 +193,8 @@ __device__ __forceinline__ void Finish<T>::store(const MxLinearArgs& a, int wave
   const int wq = wave / T::WP, wp = wave % T::WP;
   const int lane = threadIdx.x & 63, quad = lane >> 4, row16 = lane & 15;
   constexpr int kO = T::kOutCols / 16;  // column subtiles gathered at a time
-  using Rows = OutTile<16, T::kOutCols * 2, 64>;
-  using Codes = OutTile<16, T::kOutCols / 2, 64>;
+  using Rows = WaveRows<T::kOutCols * 2>;
+  using Codes = WaveRows<T::kOutCols / 2>;
 #pragma unroll
   for (int i = 0; i < T::kQ; ++i) {
     const int left = live - q_row<T::WQ>(wq, i);
@@ -213,17 +223,17 @@ __device__ __forceinline__ void Finish<T>::store(const MxLinearArgs& a, int wave
       }
       if (a.preact != nullptr) {
         char* pre = reinterpret_cast<char*>(a.preact + r0 * T::kParts * N + n0);
-        flush16<T::kOutCols * 2>(lds, pre, (int64_t)T::kParts * N * 2, left, cols * 2);
+        Rows::flush(lds, pre, (int64_t)T::kParts * N * 2, left, cols * 2);
         if constexpr (T::kGated) {
 #pragma unroll
           for (int j = 0; j < kO; ++j) Rows::put(lds, row16, (j * 16 + quad * 4) * 2, pack4(u[j]));
-          flush16<T::kOutCols * 2>(lds, pre + (int64_t)N * 2, (int64_t)2 * N * 2, left, cols * 2);
+          Rows::flush(lds, pre + (int64_t)N * 2, (int64_t)2 * N * 2, left, cols * 2);
         }
       }
       if (a.ysb == nullptr) {
 #pragma unroll
         for (int j = 0; j < kO; ++j) Rows::put(lds, row16, (j * 16 + quad * 4) * 2, pack4(y[j]));
-        flush16<T::kOutCols * 2>(lds, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + r0 * N + n0), (int64_t)N * 2, left,
+        Rows::flush(lds, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + r0 * N + n0), (int64_t)N * 2, left,
                                  cols * 2);
         continue;
       }
@@ -242,7 +252,7 @@ __device__ __forceinline__ void Finish<T>::store(const MxLinearArgs& a, int wave
         if (quad == 0 && row16 < left && j * 16 < cols)
           a.ysb[(r0 + row16) * (N / mx::kBlock) + (n0 + j * 16) / mx::kBlock] = (uint8_t)byte;
       }
-      flush16<T::kOutCols / 2>(lds, static_cast<char*>(a.y) + (r0 * N + n0) / 2, N / 2, left, cols / 2);
+      Codes::flush(lds, static_cast<char*>(a.y) + (r0 * N + n0) / 2, N / 2, left, cols / 2);
     }
   }
 }
@@ -250,7 +260,7 @@ __device__ __forceinline__ void Finish<T>::store(const MxLinearArgs& a, int wave
 // Lane l's 16-byte piece 2 (l / 16) + k of line l % 16 of a subtile of RowTile lines, k = 0
 // and 1: a line's swizzle repeats every 16 lines, so the offset serves all subtiles.
 __device__ __forceinline__ int piece_at(int lane, int k) {
-  return (lane & 15) * kDB + ((2 * (lane >> 4) + k) ^ RowTile<16, 1>::swz(lane & 15)) * 16;
+  return (lane & 15) * kDB + ((2 * (lane >> 4) + k) ^ RowTile<16, 1, true>::swz(lane & 15)) * 16;
 }
 
 // How a wave's products of one step run: 2 L units, row subtile u % L times all its column
@@ -274,8 +284,8 @@ struct Rows4 : T {
   static constexpr int kOutCols = ALIGNED ? T::kWaveCols : 32;
   using T::kP;
   using T::kParts;
-  using QTile = RowTile<T::BQ, T::kWaves>;
-  using PTile = RowTile<T::kCols, T::kWaves>;
+  using QTile = RowTile<T::BQ, T::kWaves, true>;
+  using PTile = RowTile<T::kCols, T::kWaves, true>;
   using QScale = ScaleTile<T::BQ, T::kWaves, G, ALIGNED>;
   using PScale = ScaleTile<T::kCols, T::kWaves, G, ALIGNED>;
   static constexpr int kStage = QTile::kBytes + kParts * PTile::kBytes;
@@ -420,8 +430,8 @@ template <class T, bool ALIGNED>
 struct Rows16 : T {
   using T::kP;
   using T::kParts;
-  using QTile = RowTile<T::BQ, T::kWaves>;
-  using PTile = RowTile<T::kCols, T::kWaves>;
+  using QTile = RowTile<T::BQ, T::kWaves, true>;
+  using PTile = RowTile<T::kCols, T::kWaves, true>;
   using PScale = ScaleTile<T::kCols, T::kWaves, 1, ALIGNED>;
   static constexpr int kOutCols = T::kWaveCols;
   static constexpr int kPStage = kParts * (PTile::kBytes + PScale::kBytes);

@@ -160,8 +160,9 @@ inline int64_t row_tiles_bound(int64_t rows, int E, bool dense, int bq) {
 constexpr int kDB = 128;
 
 // A tile of R operand rows by kDB bytes of depth, staged by WAVES waves: each direct
-// load of a wave fills 1 KB = 8 lines.
-template <int R, int WAVES>
+// load of a wave fills 1 KB = 8 lines.  PAIRS: made for reads in which neighbouring quads
+// of lanes take pieces two apart (a quad has a pair of them), not neighbouring ones.
+template <int R, int WAVES, bool PAIRS = false>
 struct RowTile {
   static constexpr int kBytes = R * kDB;
   static constexpr int kLines = 1024 / kDB;  // lines one load of a wave fills
@@ -170,8 +171,14 @@ struct RowTile {
   static_assert(kBytes % (1024 * WAVES) == 0, "whole loads per wave");
   // Piece g of line r sits at g ^ swz(r): two lines make 256 bytes of LDS (all banks),
   // and the 16 lines that the lanes of a quad read at one piece land on 16 different
-  // pieces of them (measured: no bank conflicts).
-  __device__ static __forceinline__ int swz(int r) { return (r / 2) & (kPieces - 1); }
+  // pieces of them (measured: no bank conflicts).  The LDS serves 16 lanes at a time, some
+  // of one quad and the others of the next one, so what the rows of either add to the
+  // piece has to stay apart under the distance of their pieces: the lowest bit of r / 2
+  // does for a distance of 1, the second one, which PAIRS puts in its place, for 2.
+  __device__ static __forceinline__ int swz(int r) {
+    const int i = (r / 2) & (kPieces - 1);
+    return PAIRS ? (i & ~3) | (i & 1) << 1 | (i >> 1 & 1) : i;
+  }
 
   uint32_t off[kLoads];  // this lane's byte offset of each of its loads at depth 0, or kNoFetch
   int piece;             // and the depth byte its piece starts at
