@@ -12,6 +12,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "linear_epilogue.h"
 #include "linear_tile.h"
@@ -680,8 +681,124 @@ struct Back16 : T {
   }
 };
 
+// Orders of all experts' tiles, dealt to the XCDs (workgroup b runs on XCD b mod 8).
+// Expert by expert in 8 equal runs, as in find_item:
+struct ByExpert : Runs {
+  // Tile `at` of XCD x.
+  __device__ __forceinline__ Item item(const LinearArgs& a, int x, int64_t at) const {
+    const int chunk = (total + 7) / 8;
+    return at < chunk && x * chunk + at < total ? Runs::item(a, x * chunk + (int)at) : Item{-1, 0, 0, 0, 0};
+  }
+};
+
+// By what a tile costs: the full row tiles first, then the last ones of the runs that fill
+// three quarters of theirs, half and a quarter (rounded up, as the products are:
+// by_live_subtiles), each kind dealt to the XCDs in 8 equal parts.  Every XCD has the same
+// work then, and what its compute units begin last is short.  256 rows an expert on average,
+// 256 x 256 tiles, a third of them partly filled (128 experts, 2 x 768 x 2048, expert by expert and by cost):
+// bf16 rows 259 and 241 us, their gradient 287 and 271, MXFP4 rows 117 and 115.  It takes 1 us
+// longer to find a tile so: the tables of experts are read for every kind.
+// Within a kind tiles are in the order of Runs, whose scan this is; the three partial kinds
+// have at most a row tile per expert and are scanned as fields of one number.
+struct ByCost {
+  static constexpr int kKinds = 4, kField = 20;
+  static_assert(MOE_MAX_EXPERTS < 1 << kField, "a field holds every expert");
+  int bq, cp, J;
+  int full, full_incl;       // full row tiles of this lane's experts, and with those of the lanes before it
+  uint64_t part, part_incl;  // the same of the partial kinds, kind k in field k - 1
+  int total[kKinds];         // tiles
+
+  // Kind of the last `rest` rows of a run, 0 < rest < bq, or of a whole tile's.
+  __device__ __forceinline__ int kind(int rest) const { return kKinds - (int)((unsigned)rest * kKinds + bq - 1) / bq; }
+  // Row tiles of kind 0 of a run of n rows.
+  __device__ __forceinline__ int whole(int n) const { return n / bq + (n % bq > 0 && kind(n % bq) == 0 ? 1 : 0); }
+
+  __device__ __forceinline__ void scan(const LinearArgs& a, int rows_per_tile, int column_tiles) {
+    bq = rows_per_tile;
+    cp = column_tiles;
+    full = full_incl = J = 0;
+    part = part_incl = 0;
+#pragma unroll
+    for (int k = 0; k < kKinds; ++k) total[k] = 0;
+    if (a.offsets == nullptr) {
+      total[0] = ceil_div(a.rows, bq) * cp;
+      return;
+    }
+    const int lane = threadIdx.x & 63;
+    J = (a.E + 63) >> 6;
+    const int most = a.rows / bq + min(a.E, a.rows);  // as in Runs
+    for (int j = 0; j < J; ++j) {
+      const int e = lane * J + j;
+      if (e >= a.E) break;
+      const int n = run_length(a.offsets[e], a.counts[e], a.rows), rest = n % bq, k = rest > 0 ? kind(rest) : 0;
+      full = min(most, full + whole(n));
+      if (k > 0) part += (uint64_t)1 << (k - 1) * kField;
+    }
+    full_incl = full;
+    part_incl = part;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(full_incl, d);
+      const uint64_t w = __shfl_up((unsigned long long)part_incl, d);
+      if (lane >= d) {
+        full_incl = min(most, full_incl + v);
+        part_incl += w;
+      }
+    }
+    total[0] = __builtin_amdgcn_readlane(full_incl, 63) * cp;
+#pragma unroll
+    for (int k = 1; k < kKinds; ++k) total[k] = __builtin_amdgcn_readlane(field(part_incl, k), 63) * cp;
+  }
+  __device__ __forceinline__ static int field(uint64_t v, int k) { return (int)(v >> (k - 1) * kField) & ((1 << kField) - 1); }
+
+  // Tile `at` of XCD x, of any kind.
+  __device__ __forceinline__ Item item(const LinearArgs& a, int x, int64_t at) const {
+    int turn = 0;  // the XCD that gets the first tile left over of a kind
+#pragma unroll
+    for (int k = 0; k < kKinds; ++k) {
+      const int each = total[k] >> 3, over = total[k] & 7, r = (x - turn) & 7;
+      const int mine = each + (r < over ? 1 : 0);
+      if (at < mine) return of_kind(a, k, r * each + min(r, over) + (int)at);
+      at -= mine;
+      turn += over;
+    }
+    return Item{-1, 0, 0, 0, 0};
+  }
+  __device__ __forceinline__ Item of_kind(const LinearArgs& a, int k, int i) const {
+    Item it{0, 0, a.rows, 0, 0};
+    if (a.offsets == nullptr) {
+      tile_of(i, ceil_div(a.rows, bq), cp, it);
+      return it;
+    }
+    const int lane = threadIdx.x & 63;
+    const int mine = k == 0 ? full : field(part, k), incl = k == 0 ? full_incl : field(part_incl, k);
+    const int owner = __builtin_ctzll(__ballot(i < incl * cp));
+    int rest = i - (incl - mine) * cp, e = lane * J, off = 0, cnt = 0, rt = 1;
+    for (int j = 0; j < J; ++j) {
+      const int c = lane * J + j;
+      if (c >= a.E) break;
+      const int o = a.offsets[c], n = run_length(o, a.counts[c], a.rows);
+      const int r = k == 0 ? whole(n) : n % bq > 0 && kind(n % bq) == k ? 1 : 0;
+      e = c;
+      off = o;
+      cnt = n;
+      rt = r;
+      if (rest < r * cp) break;
+      rest -= r * cp;
+    }
+    it.e = __builtin_amdgcn_readlane(e, owner);
+    it.row0 = __builtin_amdgcn_readlane(off, owner);
+    it.count = __builtin_amdgcn_readlane(cnt, owner);
+    rt = __builtin_amdgcn_readlane(rt, owner);
+    rest = __builtin_amdgcn_readlane(rest, owner);
+    tile_of(rest, rt, cp, it);
+    if (k > 0) it.tq = it.count / bq;
+    return it;
+  }
+};
+
 // Tiles one after another (SERIES): workgroup b takes tile b / 8 and every (grid / 8)-th one
-// after it of the run of tiles that XCD b % 8 is dealt.  A tile's first stages are loaded
+// after it of those that XCD b % 8 is dealt.  A tile's first stages are loaded
 // while the results of the one before it leave; with a tile per workgroup the search for it,
 // the first loads' latency and the results' way out were half of the time where the depth
 // is short.  Else a workgroup takes tile b / 8 alone: stores and loads come back in one
@@ -691,12 +808,13 @@ struct Back16 : T {
 template <class C, bool SERIES>
 __global__ __launch_bounds__(C::kThreads, 2) void linear_mx_kernel(MxLinearArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  Runs runs;
-  runs.scan(a, C::BQ, (C::width(a) + C::kCols - 1) / C::kCols);
+  // large tiles alone in a compute unit by their cost; the search is dear for small ones
+  std::conditional_t<!SERIES && C::kQ % 4 == 0, ByCost, ByExpert> tiles;
+  tiles.scan(a, C::BQ, (C::width(a) + C::kCols - 1) / C::kCols);
   const int64_t b = row::block_index();
-  const int chunk = (runs.total + 7) / 8, base = (int)(b & 7) * chunk, stride = (int)gridDim.x >> 3;
+  const int stride = (int)gridDim.x >> 3;
   int64_t at = b >> 3;
-  auto next = [&] { return at < chunk && base + at < runs.total ? runs.item(a, base + (int)at) : Item{-1, 0, 0, 0, 0}; };
+  auto next = [&] { return tiles.item(a, (int)(b & 7), at); };
   Item it = next();
   if (it.e < 0) return;
   char* const out = smem + C::kLds + wave * (16 * C::kOutCols * 2);
