@@ -177,6 +177,21 @@ def test_forward_forms(moe, rows, N, K, act, bias, res, save, rows4, out4):
     forward_case(moe, rows, act, bias, res, save, rows4, out4, N, K)
 
 
+# 130 experts, three to a lane of a wave, with runs of every length: large tiles in the order of their cost
+MANY = (3200, 130, 8, 1, "skew", 0.1)
+
+
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("rows4,out4", [(False, False), (True, True)])
+def test_forward_many_experts(moe, act, rows4, out4):
+    forward_case(moe, MANY, act, False, True, False, rows4, out4, 544, 96)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_backward_x_many_experts(moe, gated):
+    backward_case(moe, MANY, gated, 72, 1056)
+
+
 @pytest.mark.parametrize("rows", [5, 200], ids=str)
 @pytest.mark.parametrize("rows4", [False, True])
 def test_nan_blocks_stay_in_their_rows(moe, rows, rows4):
