@@ -7,6 +7,22 @@
 // A weight is its E2M1 code times its block's scale.  With MXFP4 rows the products are the
 // matrix cores' own 4-bit ones (mx_common.h); with bf16 rows the codes are widened to bf16
 // with their scale, which is exact, so sums are float32 either way.
+//
+// Three kinds of products share one driver (linear_mx_kernel), in tiles staged in LDS by
+// direct loads: Rows4, Rows16 and Back16.  A few rows take linear_mx_few_kernel.  32768 rows
+// over 128 experts, 2 x 768 x 2048, SwiGLU, runs of uneven length, against the bytes at a
+// large copy's 4.9 TB/s or the operations at a large bf16 product's 1.43 PFLOP/s:
+//   bf16 rows, pre-activations kept     239 us, floor 144 (operations); matrix cores busy 44%
+//   MXFP4 rows                          115 us, floor  61 (bytes); 23%
+//   the gradient of the bf16 rows       268 us, floor 144 (operations); 36%
+// Equal runs with one expert's weights take 183, 73 and 194 us: the rest is partly filled
+// tiles and weights that come from HBM.  MXFP4 rows, dense, 8192 x 2048 x 7168: 80 us, 3.0
+// PFLOP/s; in copies without the loads of its loop 64, without its products 60, without the
+// loads and most LDS reads 57, so neither hides the other whole: a tile has its compute unit
+// alone, and its two stages leave one step's time for the next one's loads.  Three stages
+// need smaller tiles, which load more (256 x 128 and 128 x 256: 88 us), and lines touched
+// ahead of their loads cost what they hide (82 us).  8 tokens top-8 in 16-row runs, 51 of 128 experts: 30 us,
+// floor 17 (bytes), MXFP4 rows 19.
 
 #include <math.h>
 #include <stdint.h>
@@ -278,7 +294,8 @@ struct Units {
 
 // MXFP4 rows: STAGES stages of 256 depth elements, 128 bytes of codes a row, and two groups
 // of G steps' scale bytes.  Lane l takes blocks 2 (l / 16) and 2 (l / 16) + 1 of a stage, one
-// for each half of its products.
+// for each half of its products.  LDS cycles of 32768 rows (see the top): 10.7M, 17.7M before
+// the lines' swizzle was made for pairs of pieces.
 template <class T, bool ALIGNED, int STAGES, int G>
 struct Rows4 : T {
   // columns of its 16 rows a wave gathers in LDS at a time: all of them where there is room
@@ -426,7 +443,8 @@ struct Rows4 : T {
 // the weights, 128 bytes of codes and 8 of scales a row, each for four steps.  Lane l takes
 // the elements 16 (l / 16) ... + 15 of a step, which lie in one scale block, the first 8 in
 // the lower half of its products; it reads their codes as 8 bytes and widens them with the
-// scale as it goes, a half beside the products of the other.
+// scale as it goes, a half beside the products of the other.  LDS cycles of 32768 rows (see
+// the top): 29.7M, 46.2M with a swizzle for single pieces (254 and 257 us).
 template <class T, bool ALIGNED>
 struct Rows16 : T {
   using T::kP;
@@ -1088,11 +1106,14 @@ hipError_t run_few_tiles(const MxLinearArgs& a, hipStream_t s) {
 }
 
 // 256-wide tiles read each operand byte half as often as 128-wide ones and are four times the
-// work: taken where they fill the GPU and the runs fill most of them (SwiGLU of 2 x 768 x
-// 2048: 32768 rows over 128 experts 115 us, 118 in 128-wide ones; 8192 rows 73 and 63.  4096
-// rows to 4 of 16 experts, 2 x 2048 x 7168: 305 and 367.  bf16 rows, the same three: 256 and
-// 260, 138 and 114, 809 and 942).
-bool wide_tiles(const MxLinearArgs& a, int64_t cols) { return tiles(a, cols, 256) >= 256 && mean_rows(a) >= 160; }
+// work: taken where they fill the GPU and the runs fill most of them.  SwiGLU of 2 x 768 x
+// 2048 over 128 experts, rows an expert on average, 256- and 128-wide tiles, us:
+//                        96          128          256       16384 rows, 16 experts, 2 x 2048 x 7168
+//   MXFP4 rows        77   73      84   84     115   121       305   362
+//   bf16 rows        139  135     160  166     239   262       800   951
+//   their gradient   164  162     175  186     268   306       872  1160
+constexpr int kWideRuns = 120;
+bool wide_tiles(const MxLinearArgs& a, int64_t cols) { return tiles(a, cols, 256) >= 256 && mean_rows(a) >= kWideRuns; }
 
 // Rows per expert on average up to which tiles have 32 rows: SwiGLU of 2 x 768 x 2048 over
 // 128 experts, MXFP4 rows, in 32 x 128 and 128 x 128 tiles: 8 rows an expert 42 and 50 us,
@@ -1141,9 +1162,8 @@ hipError_t launch_linear_mx(const MxLinearArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_linear_mx_backward_x(const MxLinearArgs& a, hipStream_t s) {
-  // 4096 rows to 8 of 128 experts, 2 x 768 x 2048: 287 us, 309 in 128-wide tiles
   if (wide_tiles(a, a.K)) return run_tiles<B16<256, 256, 2, 4>, false>(a, a.K, s);
-  // the same weights, 16 rows an expert: 85 us, 109 in 128 x 128 tiles; 48 rows 130 and 128
+  // 2 x 768 x 2048, 16 rows an expert: 85 us, 109 in 128 x 128 tiles; 48 rows 130 and 128
   if (mean_rows(a) <= kShortRuns) return run_tiles<B16<32, 128, 2, 2>, true>(a, a.K, s);
   // few tiles: 64 rows on each of 8 experts 20 us, 25; 1024 dense rows by 2 x 2048 x 2048 43, 54
   if (tiles(a, a.K, 128) < 256) return run_tiles<B16<64, 128, 2, 2>, true>(a, a.K, s);
