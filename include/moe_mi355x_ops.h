@@ -1,7 +1,8 @@
 /*
  * moe_mi355x_ops.h - operators around the expert layer, forward and backward
  * (libmoe_mi355x.so): the RMS norm in front of the router, token rows laid out
- * by expert and brought back, and the experts' matrix products over such rows.
+ * by expert and brought back, the experts' matrix products over such rows, rows and
+ * weights in 4 bits, and the clipping of all gradients by their norm.
  *
  * One expert block at prefill or training width runs as
  *   moe_add_rms_norm -> moe_router_topk -> moe_align -> moe_permute ->
@@ -12,6 +13,10 @@
  * router reads bf16 rows: a block in 8 bits calls the norm twice on the same x and
  * residual, for bf16 rows and for 8-bit ones (both are roundings of the same y), and
  * the second call may update the stream in place.
+ * In 4 bits it runs as moe_add_rms_norm -> router, align -> moe_mxfp4_quantize (whose rows
+ * go to their sorted places) -> moe_grouped_linear_mxfp4 twice (the first one hands on MXFP4
+ * rows) -> moe_unpermute; with bf16 rows the same weights train, their gradient being
+ * that of the values they stand for.
  * The backward entry points run the same chain the other way, but for the
  * router, which has none: moe_unpermute_backward gives the gradient of its
  * weights, the caller takes that through the softmax over the chosen logits
@@ -235,8 +240,8 @@ int moe_mxfp4_quantize(const void* x, moe_dtype xdt, int64_t ldx, const int32_t*
                        int32_t top_k, int32_t H, void* codes, uint8_t* scales, int64_t rows, hipStream_t stream);
 
 /* The values of MXFP4 rows ([rows, H], H a multiple of 32), bf16 or float32 (`odt`):
- * exact for every scale byte that moe_mxfp4_quantize makes.  codes and out 16-byte
- * aligned.  Errors as above. */
+ * exact, an infinity where they pass the type's largest value, NaN with the byte 255.
+ * codes and out 16-byte aligned.  Errors as above. */
 int moe_mxfp4_dequantize(const void* codes, const uint8_t* scales, int64_t rows, int32_t H, void* out, moe_dtype odt,
                          hipStream_t stream);
 

@@ -488,7 +488,7 @@ def moe_mxfp4_quantize(x: torch.Tensor, token_to_perm: Optional[torch.Tensor] = 
 def moe_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of MXFP4 codes ``[..., C/2]`` and scales ``[..., C/32]``, of `dtype`
-    (bfloat16 or float32), which holds them exactly."""
+    (bfloat16 or float32): exact, an infinity where they pass its largest one."""
     _need(dtype in _STREAM_TYPES, "dtype must be bfloat16 or float32")
     dev = _device(codes, "codes")
     _matrix(codes, "codes", _U8, None, dev)

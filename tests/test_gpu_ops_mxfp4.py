@@ -57,6 +57,18 @@ def test_special_values(moe, dtype):
                           mx_values(codes, scales)[finite].cpu().numpy())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+def test_every_scale(moe, dtype):
+    """All 256 scale bytes with all 16 codes: 2^-128 is the smallest value, exact in either
+    type; what passes the largest one is an infinity."""
+    scales = torch.arange(256, dtype=torch.uint8, device="cuda")[:, None]
+    pair = torch.arange(16, dtype=torch.uint8, device="cuda")
+    codes = (pair | pair.flip(0) << 4).repeat(256, 1)
+    got = moe.moe_mxfp4_dequantize(codes, scales, dtype=dtype)
+    want = mx_values(codes, scales).to(dtype)
+    assert torch.equal(got[:255], want[:255]) and bool(got[255].isnan().all())
+
+
 @pytest.mark.parametrize("M,H", [(1, 32), (3, 64), (5, 96), (7, 544), (33, 2048), (2, 8224), (2100, 512), (1, 32768)])
 @pytest.mark.parametrize("dtype,pitch", [(torch.bfloat16, 0), (torch.bfloat16, 3), (torch.float32, 0), (torch.float32, 1)], ids=str)
 def test_quantize(moe, M, H, dtype, pitch):

@@ -4,6 +4,8 @@ float64 autograd, the serving chain in 4 bits stage by stage, graph replays, two
 and the layer kernels on the same weights."""
 
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -267,3 +269,32 @@ def test_binding_refuses_mismatches(moe):
         with pytest.raises((ValueError, moe.MoeError)):
             call()
             log(f"call {i} was not refused")
+
+
+def test_readme_block(moe):
+    """README's 4-bit block as it is printed: it runs, its two chains agree with the calls
+    on the values they stand for, and the gradients' norm is theirs."""
+    readme = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    blocks = [b for b in re.findall(r"```python\n(.*?)```", open(readme).read(), flags=re.S) if "moe_clip_grad_norm" in b]
+    assert len(blocks) == 1
+    M, H, I, E, k = 90, 128, 96, 6, 2
+    log("README 4-bit block")
+    b = Block(M, H, I, E, 5)
+    r = Routed(moe, M, E, k, 16, 5)
+    g = gen(6)
+    grads = {n: randn(g, E, I, H) for n in ("dgate", "dup")} | {"ddown": randn(g, E, H, I), "dnorm_w": randn(g, H)}
+    before = {n: t.clone() for n, t in grads.items()}
+    x_rows, _ = moe.moe_permute(b.x, r.perm, k, r.rows)
+    got = dict(grads, moe=moe, gate=b.gate, up=b.up, down=b.down, n=b.x, perm=r.perm, k=k, rows=r.rows, off=r.offsets, cnt=r.counts,
+               x_rows=x_rows, dz=randn(g, r.rows, 2 * I))
+    exec(blocks[0], got)
+    torch.cuda.synchronize()
+    kept = r.kept
+    assert torch.equal(got["xs"][kept], moe.moe_mxfp4_quantize(x_rows)[0][kept])
+    h, _, pre = moe.moe_grouped_linear_mxfp4(x_rows, got["gate4"], r.offsets, r.counts, act="swiglu", up=got["up4"], save_preact=True)
+    assert torch.equal(got["h"][kept], h[kept]) and torch.equal(got["pre"][kept], pre[kept])
+    assert got["y"].shape == (r.rows, H) and got["dx_rows"].shape == (r.rows, H) and bool(got["y"][kept].isfinite().all())
+    norm = sum(float(t.double().square().sum()) for t in before.values()) ** 0.5
+    assert abs(float(got["norm"]) - norm) <= norm * 2.0 ** -23
+    for n, t in grads.items():
+        assert_within(t, before[n].double() / norm, (STEP + 2.0 ** -22) * before[n].double().abs() / norm)
