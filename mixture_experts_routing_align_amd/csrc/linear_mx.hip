@@ -439,7 +439,7 @@ struct Rows4 : T {
   }
 };
 
-// bf16 rows: two stages of 64 depth elements, 128 bytes a row, beside two stages of 256 of
+// bf16 rows: two or four stages of 64 depth elements, 128 bytes a row, beside two stages of 256 of
 // the weights, 128 bytes of codes and 8 of scales a row, each for four steps.  Lane l takes
 // the elements 16 (l / 16) ... + 15 of a step, which lie in one scale block, the first 8 in
 // the lower half of its products; it reads their codes as 8 bytes and widens them with the
@@ -455,7 +455,14 @@ struct Rows16 : T {
   static constexpr int kOutCols = T::kWaveCols;
   static constexpr int kPStage = kParts * (PTile::kBytes + PScale::kBytes);
   static constexpr int kPLoads = kParts * PTile::kLoads;  // of a stage's codes
-  static constexpr int kLds = 2 * QTile::kBytes + 2 * kPStage;
+  // Loads come back in order, so weights asked for have to land before rows asked for later
+  // are used.  With four stages of rows that is as late as the weights are used themselves;
+  // with two it is a step after they were asked for, which tiles of many rows spend
+  // multiplying.  256 dense rows by 2048 x 2048 in 32 x 64 tiles: 13.8 us, 15.7 with two.
+  // In 32 x 128 tiles four leave two workgroups a compute unit for three: 8 tokens top-8 over
+  // 128 experts 34.8 us, 29.3 with two.
+  static constexpr int kQStages = T::BQ <= 32 && kParts * T::kCols <= 64 ? 4 : 2;
+  static constexpr int kLds = kQStages * QTile::kBytes + 2 * kPStage;
 
   __amdgpu_buffer_rsrc_t rx, rw[kParts], rws[kParts];
   int wlead[kParts], K, S, steps;
@@ -481,10 +488,10 @@ struct Rows16 : T {
       ps[h].init(wave, lane, wlead[h], S, [&](int r) { return r < wlive ? r : -1; });
     }
   }
-  __device__ __forceinline__ char* weights(int m) const { return smem + 2 * QTile::kBytes + (m & 1) * kPStage; }
+  __device__ __forceinline__ char* weights(int m) const { return smem + kQStages * QTile::kBytes + (m & 1) * kPStage; }
   // past the last step nothing is left: the loads are issued and fetch nothing
   __device__ __forceinline__ void issue_q(int s, int wave) const {
-    qt.load(rx, smem + (s & 1) * QTile::kBytes, wave, s * kDB, K * 2 - s * kDB);
+    qt.load(rx, smem + (s & (kQStages - 1)) * QTile::kBytes, wave, s * kDB, K * 2 - s * kDB);
   }
   __device__ __forceinline__ void issue_p(int m, int wave) const {
     char* b = weights(m);
@@ -496,8 +503,8 @@ struct Rows16 : T {
   }
   __device__ __forceinline__ void start(int wave) const {
     issue_p(0, wave);
-    issue_q(0, wave);
-    issue_q(1, wave);
+#pragma unroll
+    for (int s = 0; s < kQStages; ++s) issue_q(s, wave);
   }
   // The tile's products, the first L row subtiles of a wave's.
   template <int L>
@@ -516,7 +523,7 @@ struct Rows16 : T {
     for (int h = 0; h < kParts; ++h)
       scale_at[h] = PScale::row_at(lane, wlead[h], S) + (quad >> 1) + wp * T::kWaveCols * PScale::kRow + kParts * PTile::kBytes + h * PScale::kBytes;
     auto read_q = [&](int s, int u) {
-      const char* b = smem + (s & 1) * QTile::kBytes + wq * 16 * kDB + at[u / L];
+      const char* b = smem + (s & (kQStages - 1)) * QTile::kBytes + wq * 16 * kDB + at[u / L];
       q[u % U::kRing] = *reinterpret_cast<const bf16x8*>(b + u % L * T::WQ * 16 * kDB);
     };
     auto read_p = [&](int s) {
@@ -534,7 +541,7 @@ struct Rows16 : T {
 #pragma unroll
       for (int j = 0; j < kP; ++j) p[k][j] = mma::fp4x8_to_bf16(codes[j][k], scale[j]);
     };
-    wait_and_meet<QTile::kLoads>();
+    wait_and_meet<(kQStages - 1) * QTile::kLoads>();
     read_p(0);
 #pragma unroll
     for (int u = 0; u < U::kAhead; ++u) read_q(0, u);
@@ -547,12 +554,13 @@ struct Rows16 : T {
         constexpr int u = decltype(index)::value;
         if constexpr (u == U::kMeet) {
           // this step's operands are in registers and the next one's have landed, behind which
-          // there may be those weights on their way
-          if ((s & 3) == 0)
-            wait_and_meet<kPLoads>();
+          // there may be later rows and those weights on their way
+          constexpr int kLater = (kQStages - 2) * QTile::kLoads;
+          if ((s & 3) <= kQStages - 2)
+            wait_and_meet<kLater + kPLoads>();
           else
-            wait_and_meet<0>();
-          issue_q(s + 2, wave);
+            wait_and_meet<kLater>();
+          issue_q(s + kQStages, wave);
           read_p(s + 1);
         }
         read_q(u < U::kMeet ? s : s + 1, u < U::kMeet ? u + U::kAhead : u - U::kMeet);
@@ -1086,8 +1094,8 @@ int64_t tiles(const MxLinearArgs& a, int64_t cols, int64_t edge) {
 
 // The depth-split form: few tiles in all (of 16 rows and 32 columns), which the staged forms
 // walk one memory trip after another.  Dense rows of bf16 by 2048 x 2048: 16 rows 8.6 us,
-// 12.9 in 32 x 64 tiles; 64 rows 9.1 and 13.1; 256 rows 24.5 and 14.9; 16 rows by 8192 x
-// 7168 25 and 44 (MXFP4 rows: 15 and 15).  Over many experts it is the slower one, 64 rows on
+// 12.9 in 32 x 64 tiles; 64 rows 9.1 and 13.0; 256 rows 24.5 and 13.8; 16 rows by 8192 x
+// 7168 25 and 36 (MXFP4 rows: 15 and 15).  Over many experts it is the slower one, 64 rows on
 // 51 of 128, SwiGLU of 2 x 768 x 2048: 33 us, 30 in 32 x 128 tiles (MXFP4 rows: 28 and 19).
 bool few_tiles(const MxLinearArgs& a) {
   const int64_t mean = mean_rows(a);
@@ -1139,8 +1147,8 @@ hipError_t rows16_by_shape(const MxLinearArgs& a, hipStream_t s) {
   if (wide_tiles(a, cols)) return run_tiles<R16<GATED, ALIGNED, 256, 256, 2, 4>, false>(a, a.N, s);
   if (mean_rows(a) <= kShortRuns) return run_tiles<R16<GATED, ALIGNED, 32, 128, 2, 2>, true>(a, a.N, s);
   // few tiles: smaller ones, of which more than one shares a compute unit (dense rows by 2048 x
-  // 2048, in 32 x 64, 64 x 64 and 128 x 128: 256 rows 14.9, 16.5 and 28.5 us; 512 15.9, 16.8 and
-  // 26; 2048 36, 26 and 28)
+  // 2048, in 32 x 64, 64 x 64 and 128 x 128: 256 rows 13.8, 16.5 and 28.5 us; 512 15.2, 16.8 and
+  // 26; 2048 35, 26 and 28)
   if (tiles(a, cols, 128) < 256) {
     if (tiles(a, cols, 64) <= 256) return run_tiles<R16<GATED, ALIGNED, 32, 64, 2, GATED ? 1 : 2>, false>(a, a.N, s);
     return run_tiles<R16<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2>, false>(a, a.N, s);
