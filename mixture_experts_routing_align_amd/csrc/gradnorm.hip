@@ -18,6 +18,7 @@
 // and clipped copy 623 us (5.8 TB/s of 3.6 GB), nothing to clip in place 203.
 #include <hip/hip_runtime.h>
 
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -133,8 +134,9 @@ __device__ __forceinline__ void store_piece(float* out, int at, int n, const flo
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void scale_chunk(const T* g, T* out, int n, float c, bool past_cache) {
+// `F`: the factor's type, in which the products are made.
+template <typename F, typename T>
+__device__ __forceinline__ void scale_chunk(const T* g, T* out, int n, F c, bool past_cache) {
   constexpr int kSteps = kChunk / (kThreads * 8);
   Piece<T> p[kSteps];
 #pragma unroll
@@ -145,8 +147,23 @@ __device__ __forceinline__ void scale_chunk(const T* g, T* out, int n, float c, 
     if (at >= n) break;
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = p[i].get(e) * c;
+    for (int e = 0; e < 8; ++e) v[e] = (float)(p[i].get(e) * c);
     store_piece(out, at, n, v, past_cache);
+  }
+}
+
+// This workgroup's chunks times c.
+template <typename F>
+__device__ __forceinline__ void clip_chunks(const Tensors& t, F c, bool past_cache) {
+  for (uint32_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
+    const uint32_t id = t.chunks - 1 - k;
+    const int i = tensor_of(t, id);
+    const int64_t at = (int64_t)(id - t.first[i]) * kChunk;
+    const int n = (int)min((int64_t)kChunk, t.n[i] - at);
+    if (t.f32[i / 32] >> (i % 32) & 1)
+      scale_chunk(static_cast<const float*>(t.g[i]) + at, static_cast<float*>(t.out[i]) + at, n, c, past_cache);
+    else
+      scale_chunk(static_cast<const uint16_t*>(t.g[i]) + at, static_cast<uint16_t*>(t.out[i]) + at, n, c, past_cache);
   }
 }
 
@@ -163,16 +180,12 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(Tensors t, const double*
   // a norm that is NaN or infinite scales nothing
   const float c = v > max_norm && v < INFINITY ? max_norm / v : 1.0f;
   if (c == 1.0f && in_place) return;
-  for (uint32_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
-    const uint32_t id = t.chunks - 1 - k;
-    const int i = tensor_of(t, id);
-    const int64_t at = (int64_t)(id - t.first[i]) * kChunk;
-    const int n = (int)min((int64_t)kChunk, t.n[i] - at);
-    if (t.f32[i / 32] >> (i % 32) & 1)
-      scale_chunk(static_cast<const float*>(t.g[i]) + at, static_cast<float*>(t.out[i]) + at, n, c, past_cache);
-    else
-      scale_chunk(static_cast<const uint16_t*>(t.g[i]) + at, static_cast<uint16_t*>(t.out[i]) + at, n, c, past_cache);
-  }
+  // below float32's normal range the factor would have lost bits, so it and its products are
+  // in 64 bits there
+  if (c < FLT_MIN)
+    clip_chunks(t, (double)max_norm / v, past_cache);
+  else
+    clip_chunks(t, c, past_cache);
 }
 
 int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }

@@ -1,0 +1,71 @@
+"""Gradients clipped at the ends of float32's range: factors below its smallest normal
+number.
+
+A clipped value is g * max_norm / norm with the norm rounded to float32: one rounding of
+the norm (relative, half of float32's), one of the result to float32, and one to its type;
+below the smallest normal number a rounding is off by half of the smallest subnormal.  The
+steps in 64 bits between them add less than 2^-50."""
+
+import math
+
+import pytest
+import torch
+
+from moe_testlib import log
+from ops_testlib import assert_within, gen, half
+
+pytestmark = pytest.mark.gpu
+
+F32 = half(torch.float32)
+BF16, FP32 = torch.bfloat16, torch.float32
+SUBNORMAL = {FP32: 2.0 ** -150, BF16: 2.0 ** -134}  # half of the smallest one
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import mixture_experts_routing_align_amd as m
+
+    return m
+
+
+def norm64(grads):
+    return math.sqrt(sum(float(g.double().square().sum()) for g in grads))
+
+
+def randoms(scale, types, sizes=(9000, 5, 0, 20000)):
+    return [(torch.randn(n, generator=gen(n + 1), device="cuda") * scale).to(types[i % len(types)]) for i, n in enumerate(sizes)]
+
+
+def assert_scaled(out, before, factor):
+    for o, b in zip(out, before):
+        ref = b.double() * factor
+        bound = ref.abs() * (2 * F32 + 2.0 ** -50) + SUBNORMAL[FP32]
+        if b.dtype == BF16:
+            bound = bound + (ref.abs() + bound) * half(BF16) + SUBNORMAL[BF16]
+        assert_within(o, ref, bound)
+
+
+# norms of about 1.7e2, 1.7e38 and 1.7e-37, by factors down to 2^-146, below which nothing is left
+@pytest.mark.parametrize("types", [(FP32,), (BF16,), (FP32, BF16)], ids=str)
+@pytest.mark.parametrize("scale,max_norm", [(1e36, 1.0), (1e36, 1e-4), (1e36, 3e-7), (1.0, 1e-36), (1.0, 1e-41), (1e-39, 1e-42)])
+def test_small_factors(moe, types, scale, max_norm):
+    log(f"clip {types} scale={scale} max_norm={max_norm}")
+    grads = randoms(scale, types)
+    before = [g.clone() for g in grads]
+    norm = moe.moe_grad_norm(grads)
+    want = min(1.0, float(torch.tensor(max_norm)) / norm64(grads))
+    out = [torch.full_like(g, 7.0) for g in grads]
+    assert torch.equal(moe.moe_clip_grad_norm(grads, max_norm, out=out), norm)
+    assert_scaled(out, before, want)
+    two = [torch.empty_like(g) for g in grads]
+    moe.moe_grad_clip(grads, norm, max_norm, out=two)
+    assert all(torch.equal(a, b) for a, b in zip(out, two))
+    moe.moe_clip_grad_norm(grads, max_norm)  # in place
+    assert all(torch.equal(a, b) for a, b in zip(out, grads))
+
+
+def test_no_norm_at_all(moe):
+    """A largest norm of zero makes zeros of everything finite."""
+    grads = randoms(1e30, (FP32, BF16))
+    moe.moe_clip_grad_norm(grads, 0.0)
+    assert not any(bool(g.any()) for g in grads)
