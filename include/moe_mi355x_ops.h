@@ -310,13 +310,15 @@ int moe_grad_norm(const moe_grad_tensor* list, int64_t count, float* norm, void*
 
 /* out = g * c for every tensor, rounded to its type, with c = max_norm / norm[0] where
  * norm[0] is past max_norm (finite, not negative), else 1; also 1 where norm[0] is NaN or
- * infinite, so gradients that cannot be scaled stay as they are and the norm tells.  norm
+ * infinite: gradients that it cannot scale stay as they are, and the norm tells.  norm
  * is device memory and not an output.  A gradient that stays as it is and where it is is
  * not written.  Errors as above, plus MOE_ERR_SHAPE for max_norm, and for an `out` that
  * overlaps another tensor of the list or a part of its own. */
 int moe_grad_clip(const moe_grad_tensor* list, int64_t count, const float* norm, float max_norm, hipStream_t stream);
 
-/* moe_grad_norm, then moe_grad_clip with its result: the same bits in fewer launches. */
+/* moe_grad_norm, then moe_grad_clip with its result: the same bits in fewer launches,
+ * except that finite gradients whose norm passes float32's range (norm[0] is an infinity
+ * then) are scaled by the norm as it was summed, in 64 bits. */
 int moe_clip_grad_norm(const moe_grad_tensor* list, int64_t count, float max_norm, float* norm, void* workspace,
                        size_t workspace_bytes, hipStream_t stream);
 

@@ -108,14 +108,14 @@ __global__ __launch_bounds__(kThreads) void squares_kernel(Tensors t, double* pa
 }
 
 // The norm from the workgroups' sums, in a fixed order.
-__device__ __forceinline__ float norm_of(const double* part, int parts) {
+__device__ __forceinline__ double norm_of(const double* part, int parts) {
   double s = 0.0;
   for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
-  return (float)sqrt(block_sum64(s));
+  return sqrt(block_sum64(s));
 }
 
 __global__ __launch_bounds__(kThreads) void norm_kernel(const double* part, int parts, float* norm) {
-  const float v = norm_of(part, parts);
+  const float v = (float)norm_of(part, parts);
   if (threadIdx.x == 0) *norm = v;
 }
 
@@ -170,20 +170,26 @@ __device__ __forceinline__ void clip_chunks(const Tensors& t, F c, bool past_cac
 // `part`: the sums of the first pass, or nullptr: the norm is there already.
 __global__ __launch_bounds__(kThreads) void clip_kernel(Tensors t, const double* part, int parts, float* norm, float max_norm,
                                                         int write_norm, int in_place, int past_cache) {
+  double norm64;
   float v;
   if (part != nullptr) {
-    v = norm_of(part, parts);
+    norm64 = norm_of(part, parts);
+    v = (float)norm64;
     if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+    // the norm that is returned, so that a clip of its own gives the same bits, but where
+    // float32 cannot hold it
+    if (v < INFINITY) norm64 = v;
   } else {
-    v = *norm;
+    norm64 = v = *norm;
   }
   // a norm that is NaN or infinite scales nothing
-  const float c = v > max_norm && v < INFINITY ? max_norm / v : 1.0f;
+  const bool scaled = norm64 > max_norm && norm64 < (double)INFINITY;
+  const float c = scaled ? max_norm / v : 1.0f;
   if (c == 1.0f && in_place) return;
-  // below float32's normal range the factor would have lost bits, so it and its products are
-  // in 64 bits there
+  // the factor by such a norm, or below float32's normal range, where it would have lost
+  // bits, and its products are in 64 bits
   if (c < FLT_MIN)
-    clip_chunks(t, (double)max_norm / v, past_cache);
+    clip_chunks(t, (double)max_norm / norm64, past_cache);
   else
     clip_chunks(t, c, past_cache);
 }

@@ -654,7 +654,9 @@ def moe_grad_clip(grads: Sequence[torch.Tensor], norm: torch.Tensor, max_norm: f
 def moe_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
                        norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """moe_grad_norm, then moe_grad_clip with its result, in fewer launches: the gradients
-    are scaled in place (or into `out`), their norm before that is returned."""
+    are scaled in place (or into `out`), their norm before that is returned.  Finite
+    gradients whose norm passes float32's range are scaled by it too; an infinity is
+    returned then."""
     dev, packed = _grads(grads, out, "moe_clip_grad_norm")
     norm = _out(norm, (1,), torch.float32, grads[0], stream, "norm", dev)
     lib = _ffi.load()

@@ -1,5 +1,5 @@
 """Gradients clipped at the ends of float32's range: factors below its smallest normal
-number.
+number, and norms past its largest one.
 
 A clipped value is g * max_norm / norm with the norm rounded to float32: one rounding of
 the norm (relative, half of float32's), one of the result to float32, and one to its type;
@@ -69,3 +69,37 @@ def test_no_norm_at_all(moe):
     grads = randoms(1e30, (FP32, BF16))
     moe.moe_clip_grad_norm(grads, 0.0)
     assert not any(bool(g.any()) for g in grads)
+
+
+@pytest.mark.parametrize("types", [(FP32,), (BF16,), (FP32, BF16)], ids=str)
+@pytest.mark.parametrize("max_norm", [1.0, 1e30, 3e38, 1e-10])
+def test_norm_past_float32(moe, types, max_norm):
+    """Finite gradients whose norm (about 5e39) float32 cannot hold are clipped by it all the
+    same; the norm that is returned is an infinity, by which moe_grad_clip scales nothing."""
+    log(f"clip {types} past float32, max_norm={max_norm}")
+    grads = randoms(3e37, types)
+    before = [g.clone() for g in grads]
+    assert all(bool(g.isfinite().all()) for g in grads) and norm64(grads) > 3.5e38
+    want = float(torch.tensor(max_norm)) / norm64(grads)
+    out = [torch.full_like(g, 7.0) for g in grads]
+    norm = moe.moe_clip_grad_norm(grads, max_norm, out=out)
+    assert bool(norm.isinf())
+    assert_scaled(out, before, want)
+    apart = [torch.full_like(g, 7.0) for g in grads]
+    assert bool(moe.moe_grad_norm(grads).isinf())
+    moe.moe_grad_clip(grads, norm, max_norm, out=apart)
+    assert all(torch.equal(a, b) for a, b in zip(apart, before))
+    assert bool(moe.moe_clip_grad_norm(grads, max_norm).isinf())  # in place
+    assert all(torch.equal(a, b) for a, b in zip(out, grads))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_not_finite_beside_large_ones(moe, value):
+    """A gradient that is not finite still scales nothing, however large the others are."""
+    grads = randoms(3e37, (FP32,))
+    grads[0][17] = value
+    before = [g.clone() for g in grads]
+    norm = moe.moe_clip_grad_norm(grads, 1.0)
+    assert bool(norm.isnan() if value != value else norm == float("inf"))
+    for g, b in zip(grads, before):
+        assert torch.equal(g.nan_to_num(nan=-1.0), b.nan_to_num(nan=-1.0))
