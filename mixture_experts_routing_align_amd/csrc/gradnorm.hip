@@ -152,12 +152,13 @@ __device__ __forceinline__ void scale_chunk(const T* g, T* out, int n, F c, bool
   }
 }
 
-// This workgroup's chunks times c.
+// This workgroup's chunks times c.  What stays as it is and where it is is not written.
 template <typename F>
 __device__ __forceinline__ void clip_chunks(const Tensors& t, F c, bool past_cache) {
   for (uint32_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
     const uint32_t id = t.chunks - 1 - k;
     const int i = tensor_of(t, id);
+    if (c == 1 && t.out[i] == t.g[i]) continue;
     const int64_t at = (int64_t)(id - t.first[i]) * kChunk;
     const int n = (int)min((int64_t)kChunk, t.n[i] - at);
     if (t.f32[i / 32] >> (i % 32) & 1)

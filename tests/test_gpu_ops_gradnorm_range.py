@@ -103,3 +103,19 @@ def test_not_finite_beside_large_ones(moe, value):
     assert bool(norm.isnan() if value != value else norm == float("inf"))
     for g, b in zip(grads, before):
         assert torch.equal(g.nan_to_num(nan=-1.0), b.nan_to_num(nan=-1.0))
+
+
+def test_nothing_to_clip_writes_nothing_in_place(moe):
+    """Where nothing is scaled, a gradient that is clipped in place keeps its very bits,
+    beside others that are copied: a signalling NaN would come back as a quiet one."""
+    signalling = 0x7F81  # bf16
+    there = torch.full((9000,), signalling, dtype=torch.int16, device="cuda").view(BF16)
+    wide = torch.full((3000,), signalling << 16, dtype=torch.int32, device="cuda").view(FP32)
+    other = torch.ones(9000, device="cuda")
+    copy = torch.zeros_like(other)
+    for call in (lambda: moe.moe_clip_grad_norm([there, other, wide], 1.0, out=[there, copy, wide]),
+                 lambda: moe.moe_grad_clip([there, other, wide], torch.tensor([1.0], device="cuda"), 1.0, out=[there, copy, wide])):
+        copy.zero_()
+        call()
+        assert torch.equal(copy, other)
+        assert bool((there.view(torch.int16) == signalling).all()) and bool((wide.view(torch.int32) == signalling << 16).all())
