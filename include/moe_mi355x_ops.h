@@ -303,8 +303,9 @@ size_t moe_grad_norm_workspace_bytes(int64_t count);
 /* norm[0] = (sum over the tensors' elements of g^2)^(1/2): summed in 64 bits in a
  * fixed order, rounded to float32 (0 without an element, an infinity past its range).
  * `list` is host memory and is read before the call returns.  Errors: MOE_ERR_NULL,
- * MOE_ERR_SHAPE (a count or size negative, a type, an alignment), MOE_ERR_LIMIT (2^20
- * tensors, 2^44 elements), MOE_ERR_WORKSPACE, MOE_ERR_HIP. */
+ * MOE_ERR_SHAPE (a count or size negative, a type, an alignment, a workspace that lies
+ * over a gradient or the norm), MOE_ERR_LIMIT (2^20 tensors, 2^44 elements),
+ * MOE_ERR_WORKSPACE, MOE_ERR_HIP. */
 int moe_grad_norm(const moe_grad_tensor* list, int64_t count, float* norm, void* workspace, size_t workspace_bytes,
                   hipStream_t stream);
 
@@ -312,13 +313,15 @@ int moe_grad_norm(const moe_grad_tensor* list, int64_t count, float* norm, void*
  * norm[0] is past max_norm (finite, not negative), else 1; also 1 where norm[0] is NaN or
  * infinite: gradients that it cannot scale stay as they are, and the norm tells.  norm
  * is device memory and not an output.  A gradient that stays as it is and where it is is
- * not written.  Errors as above, plus MOE_ERR_SHAPE for max_norm, and for an `out` that
- * overlaps another tensor of the list or a part of its own. */
+ * not written.  Errors as above, plus MOE_ERR_SHAPE for max_norm, for an `out` that
+ * overlaps another tensor of the list or a part of its own, and for a norm that lies over
+ * an output. */
 int moe_grad_clip(const moe_grad_tensor* list, int64_t count, const float* norm, float max_norm, hipStream_t stream);
 
 /* moe_grad_norm, then moe_grad_clip with its result: the same bits in fewer launches,
  * except that finite gradients whose norm passes float32's range (norm[0] is an infinity
- * then) are scaled by the norm as it was summed, in 64 bits. */
+ * then) are scaled by the norm as it was summed, in 64 bits.  The norm is written while
+ * gradients are read, so it may not lie over one of them either (MOE_ERR_SHAPE). */
 int moe_clip_grad_norm(const moe_grad_tensor* list, int64_t count, float max_norm, float* norm, void* workspace,
                        size_t workspace_bytes, hipStream_t stream);
 

@@ -167,6 +167,22 @@ int check_grad_outputs(const char* fn, const moe::GradTensor* t, int64_t count) 
   return MOE_OK;
 }
 
+// Whether `bytes` from p on lie over a gradient (`reads`) or an output of the call.
+bool over_tensor(const moe::GradTensor* t, int64_t count, bool reads, const void* p, int64_t bytes) {
+  return std::any_of(t, t + count, [&](const moe::GradTensor& g) {
+    const int64_t size = g.n * (g.f32 ? 4 : 2);
+    return size > 0 && ((reads && overlap(g.g, size, p, bytes)) || overlap(g.out, size, p, bytes));
+  });
+}
+
+// The norm, which every workgroup of the second pass reads while others write the outputs;
+// `written`: by that pass, while others read the gradients.
+int check_grad_norm(const char* fn, const moe::GradTensor* t, int64_t count, const float* norm, bool written) {
+  if (reinterpret_cast<uintptr_t>(norm) % 4) return fail_status(MOE_ERR_SHAPE, "%s: norm is not aligned to its element", fn);
+  if (over_tensor(t, count, written, norm, 4)) return fail_status(MOE_ERR_SHAPE, "%s: norm overlaps a tensor of the call", fn);
+  return MOE_OK;
+}
+
 bool all_in_place(const moe::GradTensor* t, int64_t count) {
   return std::all_of(t, t + count, [](const moe::GradTensor& g) { return g.n == 0 || g.g == g.out; });
 }
@@ -176,11 +192,15 @@ int check_max_norm(const char* fn, float max_norm) {
   return MOE_OK;
 }
 
-int check_grad_workspace(const char* fn, int64_t count, const void* workspace, size_t bytes) {
+// The workspace, which is written while the gradients are read, and read beside the outputs.
+int check_grad_workspace(const char* fn, const moe::GradTensor* t, int64_t count, const float* norm, const void* workspace,
+                         size_t bytes) {
   const size_t need = moe::grad_norm_workspace(count);
   if (workspace == nullptr) return null_arg(fn, "workspace");
   if (bytes < need) return fail_status(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes, needs %zu", fn, bytes, need);
   if (reinterpret_cast<uintptr_t>(workspace) % 8) return fail_status(MOE_ERR_SHAPE, "%s: workspace is not 8-byte aligned", fn);
+  if (overlap(norm, 4, workspace, need) || over_tensor(t, count, true, workspace, need))
+    return fail_status(MOE_ERR_SHAPE, "%s: workspace overlaps the norm or a tensor of the call", fn);
   return MOE_OK;
 }
 
@@ -625,7 +645,8 @@ int moe_grad_norm(const moe_grad_tensor* list, int64_t count, float* norm, void*
   GradList t;
   if (int rc = take_grads(fn, list, count, false, t)) return rc;
   if (norm == nullptr) return null_arg(fn, "norm");
-  if (int rc = check_grad_workspace(fn, count, workspace, workspace_bytes)) return rc;
+  if (int rc = check_grad_workspace(fn, t.get(), count, norm, workspace, workspace_bytes)) return rc;
+  if (int rc = check_grad_norm(fn, nullptr, 0, norm, true)) return rc;  // written once the gradients are read
   double* part = static_cast<double*>(workspace);
   int parts = 0;
   hipError_t e = moe::launch_grad_squares(t.get(), count, part, &parts, stream);
@@ -640,6 +661,7 @@ int moe_grad_clip(const moe_grad_tensor* list, int64_t count, const float* norm,
   if (int rc = check_max_norm(fn, max_norm)) return rc;
   if (norm == nullptr) return null_arg(fn, "norm");
   if (int rc = check_grad_outputs(fn, t.get(), count)) return rc;
+  if (int rc = check_grad_norm(fn, t.get(), count, norm, false)) return rc;
   return hip_status(fn, moe::launch_grad_clip(t.get(), count, nullptr, 0, const_cast<float*>(norm), max_norm,
                                               all_in_place(t.get(), count), stream));
 }
@@ -652,7 +674,8 @@ int moe_clip_grad_norm(const moe_grad_tensor* list, int64_t count, float max_nor
   if (int rc = check_max_norm(fn, max_norm)) return rc;
   if (norm == nullptr) return null_arg(fn, "norm");
   if (int rc = check_grad_outputs(fn, t.get(), count)) return rc;
-  if (int rc = check_grad_workspace(fn, count, workspace, workspace_bytes)) return rc;
+  if (int rc = check_grad_workspace(fn, t.get(), count, norm, workspace, workspace_bytes)) return rc;
+  if (int rc = check_grad_norm(fn, t.get(), count, norm, true)) return rc;
   double* part = static_cast<double*>(workspace);
   int parts = 0;
   hipError_t e = moe::launch_grad_squares(t.get(), count, part, &parts, stream);
