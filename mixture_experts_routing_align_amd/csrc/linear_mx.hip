@@ -35,6 +35,7 @@
 #include "moe_internal.h"
 #include "moe_mi355x_ops.h"
 #include "mx_common.h"
+#include "mx_forms.h"
 #include "row_common.h"
 
 namespace moe {
@@ -42,6 +43,7 @@ namespace {
 
 using namespace tile;
 using namespace epilogue;
+using mx::Form;
 
 extern __shared__ __attribute__((aligned(1024))) char smem[];
 
@@ -1083,77 +1085,36 @@ hipError_t run_tiles(const MxLinearArgs& a, int cols, hipStream_t s) {
   return launch(kern, SERIES ? std::min(items, kCUs * (160 * 1024 / lds)) : items, C::kThreads, lds, a, s, allowed);
 }
 
-// Rows per expert on average, of the matrix's height, in which the alignment's padding
-// counts: the runs themselves are known on the device only.
-int64_t mean_rows(const MxLinearArgs& a) { return ceil_div(a.rows, a.E); }
-
-// Square tiles of `edge` that the rows and `cols` columns make.
-int64_t tiles(const MxLinearArgs& a, int64_t cols, int64_t edge) {
-  return (a.rows + edge - 1) / edge * ((cols + edge - 1) / edge);
+mx::Sizes sizes_of(const MxLinearArgs& a) {
+  return mx::Sizes{a.rows, a.E, a.offsets == nullptr, a.N, a.K, a.parts, a.ysb != nullptr};
 }
 
-// The depth-split form: few tiles in all (of 16 rows and 32 columns), which the staged forms
-// walk one memory trip after another.  Dense rows of bf16 by 2048 x 2048: 16 rows 8.6 us,
-// 12.9 in 32 x 64 tiles; 64 rows 9.1 and 13.0; 256 rows 24.5 and 13.8; 16 rows by 8192 x
-// 7168 25 and 36 (MXFP4 rows: 15 and 15).  Over many experts it is the slower one, 64 rows on
-// 51 of 128, SwiGLU of 2 x 768 x 2048: 33 us, 30 in 32 x 128 tiles (MXFP4 rows: 28 and 19).
-bool few_tiles(const MxLinearArgs& a) {
-  const int64_t mean = mean_rows(a);
-  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, 16) * ((a.N + 31) / 32);
-  return items <= (mean <= 32 ? 1024 : mean <= 64 ? 256 : 0);
-}
-
-// 8 waves along the depth while its tiles are fewer than 512, of half the columns where the
-// result allows it (8 dense rows, 2048 x 7168: 10 us, 16 on 32 columns); else 2 (16384
-// columns: 30 us, 31 with 8).
-template <bool ROWS4, bool GATED>
-hipError_t run_few_tiles(const MxLinearArgs& a, hipStream_t s) {
-  const int64_t items = row_tiles_bound(a.rows, a.E, a.offsets == nullptr, 16) * ((a.N + 31) / 32);
-  if (items >= 512) return run_few<ROWS4, GATED, 2, 2>(a, s);
-  return a.ysb != nullptr ? run_few<ROWS4, GATED, 2, 8>(a, s) : run_few<ROWS4, GATED, 1, 8>(a, s);
-}
-
-// 256-wide tiles read each operand byte half as often as 128-wide ones and are four times the
-// work: taken where they fill the GPU and the runs fill most of them.  SwiGLU of 2 x 768 x
-// 2048 over 128 experts, rows an expert on average, 256- and 128-wide tiles, us:
-//                        96          128          256       16384 rows, 16 experts, 2 x 2048 x 7168
-//   MXFP4 rows        77   73      84   84     115   121       305   362
-//   bf16 rows        139  135     160  166     239   262       800   951
-//   their gradient   164  162     175  186     268   306       872  1160
-constexpr int kWideRuns = 120;
-bool wide_tiles(const MxLinearArgs& a, int64_t cols) { return tiles(a, cols, 256) >= 256 && mean_rows(a) >= kWideRuns; }
-
-// Rows per expert on average up to which tiles have 32 rows: SwiGLU of 2 x 768 x 2048 over
-// 128 experts, MXFP4 rows, in 32 x 128 and 128 x 128 tiles: 8 rows an expert 42 and 50 us,
-// 24 52 and 56, 48 64 and 62 (bf16 rows: 61 and 82, 83 and 91, 111 and 110).
-constexpr int64_t kShortRuns = 40;
-
+// The forms, as the rules of mx_forms.h choose them.
 template <bool GATED, bool ALIGNED>
-hipError_t rows4_by_shape(const MxLinearArgs& a, hipStream_t s) {
-  if (few_tiles(a)) return run_few_tiles<true, GATED>(a, s);
-  const int64_t cols = a.parts * (int64_t)a.N;
-  if (wide_tiles(a, cols)) return run_tiles<R4<GATED, ALIGNED, 256, 256, 2, 4, 2, 2>, false>(a, a.N, s);
-  if (mean_rows(a) <= kShortRuns) return run_tiles<R4<GATED, ALIGNED, 32, 128, 2, 2, 2, 2>, true>(a, a.N, s);
-  // few 128-wide tiles: smaller ones (1024 dense rows by 4096 x 2048: 13.1 us, 14.8; 2048 x
-  // 2048: 12.8 and 14.7; in 64 x 64 16.7)
-  if (tiles(a, cols, 128) < 256) return run_tiles<R4<GATED, ALIGNED, 64, 128, 2, 2, 2, 2>, false>(a, a.N, s);
-  return run_tiles<R4<GATED, ALIGNED, 128, 128, 2, 2, 2, 2>, true>(a, a.N, s);
-}
-
-template <bool GATED, bool ALIGNED>
-hipError_t rows16_by_shape(const MxLinearArgs& a, hipStream_t s) {
-  if (few_tiles(a)) return run_few_tiles<false, GATED>(a, s);
-  const int64_t cols = a.parts * (int64_t)a.N;
-  if (wide_tiles(a, cols)) return run_tiles<R16<GATED, ALIGNED, 256, 256, 2, 4>, false>(a, a.N, s);
-  if (mean_rows(a) <= kShortRuns) return run_tiles<R16<GATED, ALIGNED, 32, 128, 2, 2>, true>(a, a.N, s);
-  // few tiles: smaller ones, of which more than one shares a compute unit (dense rows by 2048 x
-  // 2048, in 32 x 64, 64 x 64 and 128 x 128: 256 rows 13.8, 16.5 and 28.5 us; 512 15.2, 16.8 and
-  // 26; 2048 35, 26 and 28)
-  if (tiles(a, cols, 128) < 256) {
-    if (tiles(a, cols, 64) <= 256) return run_tiles<R16<GATED, ALIGNED, 32, 64, 2, GATED ? 1 : 2>, false>(a, a.N, s);
-    return run_tiles<R16<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2>, false>(a, a.N, s);
+hipError_t rows4_by_form(const MxLinearArgs& a, hipStream_t s) {
+  switch (mx::rows4_form(sizes_of(a))) {
+    case Form::kSplit16: return run_few<true, GATED, 1, 8>(a, s);
+    case Form::kSplit32: return run_few<true, GATED, 2, 8>(a, s);
+    case Form::kSplit32By2: return run_few<true, GATED, 2, 2>(a, s);
+    case Form::k32x128: return run_tiles<R4<GATED, ALIGNED, 32, 128, 2, 2, 2, 2>, true>(a, a.N, s);
+    case Form::k64x128: return run_tiles<R4<GATED, ALIGNED, 64, 128, 2, 2, 2, 2>, false>(a, a.N, s);
+    case Form::k256x256: return run_tiles<R4<GATED, ALIGNED, 256, 256, 2, 4, 2, 2>, false>(a, a.N, s);
+    default: return run_tiles<R4<GATED, ALIGNED, 128, 128, 2, 2, 2, 2>, true>(a, a.N, s);
   }
-  return run_tiles<R16<GATED, ALIGNED, 128, 128, 2, 2>, true>(a, a.N, s);
+}
+
+template <bool GATED, bool ALIGNED>
+hipError_t rows16_by_form(const MxLinearArgs& a, hipStream_t s) {
+  switch (mx::rows16_form(sizes_of(a))) {
+    case Form::kSplit16: return run_few<false, GATED, 1, 8>(a, s);
+    case Form::kSplit32: return run_few<false, GATED, 2, 8>(a, s);
+    case Form::kSplit32By2: return run_few<false, GATED, 2, 2>(a, s);
+    case Form::k32x64: return run_tiles<R16<GATED, ALIGNED, 32, 64, 2, GATED ? 1 : 2>, false>(a, a.N, s);
+    case Form::k32x128: return run_tiles<R16<GATED, ALIGNED, 32, 128, 2, 2>, true>(a, a.N, s);
+    case Form::k64x64: return run_tiles<R16<GATED, ALIGNED, 64, 64, GATED ? 4 : 2, GATED ? 1 : 2>, false>(a, a.N, s);
+    case Form::k256x256: return run_tiles<R16<GATED, ALIGNED, 256, 256, 2, 4>, false>(a, a.N, s);
+    default: return run_tiles<R16<GATED, ALIGNED, 128, 128, 2, 2>, true>(a, a.N, s);
+  }
 }
 
 }  // namespace
@@ -1162,20 +1123,20 @@ hipError_t launch_linear_mx(const MxLinearArgs& a, hipStream_t s) {
   const uintptr_t lead = reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.wsb[0]) | reinterpret_cast<uintptr_t>(a.wsb[1]);
   const bool aligned = a.K % 128 == 0 && lead % 4 == 0, gated = a.parts == 2;
   if (a.xs != nullptr) {
-    if (aligned) return gated ? rows4_by_shape<true, true>(a, s) : rows4_by_shape<false, true>(a, s);
-    return gated ? rows4_by_shape<true, false>(a, s) : rows4_by_shape<false, false>(a, s);
+    if (aligned) return gated ? rows4_by_form<true, true>(a, s) : rows4_by_form<false, true>(a, s);
+    return gated ? rows4_by_form<true, false>(a, s) : rows4_by_form<false, false>(a, s);
   }
-  if (aligned) return gated ? rows16_by_shape<true, true>(a, s) : rows16_by_shape<false, true>(a, s);
-  return gated ? rows16_by_shape<true, false>(a, s) : rows16_by_shape<false, false>(a, s);
+  if (aligned) return gated ? rows16_by_form<true, true>(a, s) : rows16_by_form<false, true>(a, s);
+  return gated ? rows16_by_form<true, false>(a, s) : rows16_by_form<false, false>(a, s);
 }
 
 hipError_t launch_linear_mx_backward_x(const MxLinearArgs& a, hipStream_t s) {
-  if (wide_tiles(a, a.K)) return run_tiles<B16<256, 256, 2, 4>, false>(a, a.K, s);
-  // 2 x 768 x 2048, 16 rows an expert: 85 us, 109 in 128 x 128 tiles; 48 rows 130 and 128
-  if (mean_rows(a) <= kShortRuns) return run_tiles<B16<32, 128, 2, 2>, true>(a, a.K, s);
-  // few tiles: 64 rows on each of 8 experts 20 us, 25; 1024 dense rows by 2 x 2048 x 2048 43, 54
-  if (tiles(a, a.K, 128) < 256) return run_tiles<B16<64, 128, 2, 2>, true>(a, a.K, s);
-  return run_tiles<B16<128, 128, 2, 2>, true>(a, a.K, s);
+  switch (mx::back_form(sizes_of(a))) {
+    case Form::k32x128: return run_tiles<B16<32, 128, 2, 2>, true>(a, a.K, s);
+    case Form::k64x128: return run_tiles<B16<64, 128, 2, 2>, true>(a, a.K, s);
+    case Form::k256x256: return run_tiles<B16<256, 256, 2, 4>, false>(a, a.K, s);
+    default: return run_tiles<B16<128, 128, 2, 2>, true>(a, a.K, s);
+  }
 }
 
 }  // namespace moe

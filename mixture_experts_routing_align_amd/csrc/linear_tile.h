@@ -147,11 +147,6 @@ __device__ __forceinline__ Item find_item(const LinearArgs& a, int b, int bq, in
   return runs.item(a, i);
 }
 
-// Row tiles all runs can need: one partly filled tile per expert on top of the full ones.
-inline int64_t row_tiles_bound(int64_t rows, int E, bool dense, int bq) {
-  return dense ? (rows + bq - 1) / bq : rows / bq + (E < rows ? E : rows);
-}
-
 // ---------------------------------------------------------- staging, "R" --
 
 // Bytes of depth a stage holds of each operand row: 64 bf16 or 128 8-bit elements (one

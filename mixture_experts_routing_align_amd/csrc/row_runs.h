@@ -16,6 +16,11 @@ constexpr int run_length(int off, int cnt, int rows) {
   return cnt < rows - off ? cnt : rows - off;
 }
 
+// Row tiles all runs can need: one partly filled tile per expert on top of the full ones.
+constexpr int64_t row_tiles_bound(int64_t rows, int E, bool dense, int bq) {
+  return dense ? (rows + bq - 1) / bq : rows / bq + (E < rows ? E : rows);
+}
+
 // Part `split` of `splits` of a run of `count` rows: equal parts, in whole stages of
 // `depth` rows; the last ones may be shorter or empty.
 struct RowRange {
