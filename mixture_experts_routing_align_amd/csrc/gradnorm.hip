@@ -14,8 +14,8 @@
 // still holds (648 us from the first on, 627 so), and its results go past the caches where
 // they do not fit there (659 us into them).
 //
-// 604 million bf16 gradients in three tensors: the norm 202 us (6.0 TB/s of 1.2 GB), norm
-// and clipped copy 623 us (5.8 TB/s of 3.6 GB), nothing to clip in place 203.
+// 604 million bf16 gradients in three tensors: the norm 200 us (6.0 TB/s of 1.2 GB), norm
+// and clipped copy 625 us (5.8 TB/s of 3.6 GB), in place 613, nothing to clip in place 200.
 #include <hip/hip_runtime.h>
 
 #include <float.h>

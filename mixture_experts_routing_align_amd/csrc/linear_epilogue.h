@@ -39,8 +39,8 @@ __device__ __forceinline__ void unpack4(uint2 v, float (&f)[4]) {
 __device__ __forceinline__ uint2 pack4(const float (&f)[4]) { return make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])); }
 
 // 1 / (1 + exp(-x)) without the remainder of x log2(e), whose rounding costs |x| 2^-24 of the
-// result where the exponential dominates: for epilogues that round to 8 bits or fewer and are
-// bound by their arithmetic.  The infinities need no care: the exponential is 0 or an
+// result where the exponential dominates (|x| is at most 89 there: 2^-17): for epilogues that
+// round to 8 significant bits (bf16) or fewer and are bound by their arithmetic.  The infinities need no care: the exponential is 0 or an
 // infinity there, as it is past 89.
 __device__ __forceinline__ float sigmoid_short(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));

@@ -12,17 +12,23 @@
 // direct loads: Rows4, Rows16 and Back16.  A few rows take linear_mx_few_kernel.  32768 rows
 // over 128 experts, 2 x 768 x 2048, SwiGLU, runs of uneven length, against the bytes at a
 // large copy's 4.9 TB/s or the operations at a large bf16 product's 1.43 PFLOP/s:
-//   bf16 rows, pre-activations kept     239 us, floor 144 (operations); matrix cores busy 44%
-//   MXFP4 rows                          115 us, floor  61 (bytes); 23%
-//   the gradient of the bf16 rows       268 us, floor 144 (operations); 36%
-// Equal runs with one expert's weights take 183, 73 and 194 us: the rest is partly filled
-// tiles and weights that come from HBM.  MXFP4 rows, dense, 8192 x 2048 x 7168: 80 us, 3.0
-// PFLOP/s; in copies without the loads of its loop 64, without its products 60, without the
-// loads and most LDS reads 57, so neither hides the other whole: a tile has its compute unit
-// alone, and its two stages leave one step's time for the next one's loads.  Three stages
-// need smaller tiles, which load more (256 x 128 and 128 x 256: 88 us), and lines touched
-// ahead of their loads cost what they hide (82 us).  8 tokens top-8 in 16-row runs, 51 of 128 experts: 30 us,
-// floor 17 (bytes), MXFP4 rows 19.
+//   bf16 rows, pre-activations kept     230 us, floor 144 (operations); matrix cores busy 44%
+//   MXFP4 rows                          110 us, floor  61 (bytes); 23%
+//   the gradient of the bf16 rows       264 us, floor 144 (operations); 36%
+// Equal runs with one expert's weights take 181, 71 and 189 us: the rest is partly filled
+// tiles and weights that come from HBM.  MXFP4 rows, dense, 8192 x 2048 x 7168, bias and
+// residual: 76 us, 3.2 PFLOP/s; 62 without the residual, whose rows are read one subtile
+// ahead after the last product while the compute unit has nothing else to do (7 us of bytes
+// for 15).  Ablations in copies (80 us then): without the loads of its loop 64, without its
+// products 60, also without the reads of scales and weights from LDS 57, the reads of rows
+// still in.  So the loads are hidden but for a fifth, and more than half of the rest is reads
+// of rows, the products' issue, and a tile's start and end.  A tile has its compute unit
+// alone, and its two stages leave one step's time for the next one's loads; three stages need
+// smaller tiles, which load more (256 x 128 and 128 x 256: 88 us), and lines touched ahead of
+// their loads cost what they hide (82 us).  8 tokens top-8 in 16-row runs, 54 of 128 experts:
+// 29 us, floor 19 (bytes), MXFP4 rows 19: what the bf16 rows lack is not the weights' rate but
+// longer steps, 32 meetings of 64 deep for 8 of 256, and weights that have to land a step
+// after they are asked for.
 
 #include <math.h>
 #include <stdint.h>

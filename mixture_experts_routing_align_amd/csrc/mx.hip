@@ -9,9 +9,9 @@
 // lanes, whose maximum meets on the DPP crossbar; a row is shared by as many threads as it
 // has pieces, up to a workgroup, and a thread's pieces are loaded ahead of their rounding.
 //
-// Measured (kernels alone): 4096 bf16 rows of 2048 to 32768 sorted rows 14.2 us, 6.2 TB/s;
-// 98304 float32 rows of 2048 200 us, 4.6 TB/s (201 million weights), back to bf16 77 us, 6.6
-// TB/s; 8 rows to 64 4.1 us, the launch and one trip to memory.
+// Measured (kernels alone): 4096 bf16 rows of 2048 to 32768 sorted rows 14.0 us, 3.7 TB/s;
+// 98304 float32 rows of 2048 191 us, 4.8 TB/s (201 million weights), back to bf16 75 us, 6.8
+// TB/s; 8 rows to 64 4.0 us, the launch and one trip to memory.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>

@@ -24,7 +24,10 @@ struct Sizes {
 };
 
 // Rows per expert on average, of the matrix's height, in which the alignment's padding
-// counts.
+// counts: runs far below the block size can get tiles that are too large.  SwiGLU of 2 x 768 x
+// 2048 over 128 experts, 16 and 32 tokens top-8 aligned to 16 rows and to 64 (128-row tiles):
+// bf16 rows 49 and 61 us, 59 and 80; MXFP4 rows 31 and 35, 39 and 47; the gradient 51 and 75,
+// 70 and 100.
 constexpr int64_t mean_rows(const Sizes& a) { return (a.rows + a.E - 1) / a.E; }
 
 // Square tiles of `edge` that the rows and `cols` columns make.
@@ -55,15 +58,17 @@ constexpr Form split_form(const Sizes& a) {
 // work: taken where they fill the GPU and the runs fill most of them.  SwiGLU of 2 x 768 x
 // 2048 over 128 experts, rows an expert on average, 256- and 128-wide tiles, us:
 //                        96          128          256       16384 rows, 16 experts, 2 x 2048 x 7168
-//   MXFP4 rows        77   73      84   84     115   121       305   362
-//   bf16 rows        139  135     160  166     239   262       800   951
-//   their gradient   164  162     175  186     268   306       872  1160
+//   MXFP4 rows        77   73      83   83     113   123       303   354
+//   bf16 rows        138  135     152  158     222   242       766   913
+//   their gradient   163  163     176  187     267   301       837  1121
 constexpr int kWideRuns = 120;
 constexpr bool wide_tiles(const Sizes& a, int64_t cols) { return tiles(a, cols, 256) >= 256 && mean_rows(a) >= kWideRuns; }
 
 // Rows per expert on average up to which tiles have 32 rows: SwiGLU of 2 x 768 x 2048 over
 // 128 experts, MXFP4 rows, in 32 x 128 and 128 x 128 tiles: 8 rows an expert 42 and 50 us,
-// 24 52 and 56, 48 64 and 62 (bf16 rows: 61 and 82, 83 and 91, 111 and 110).
+// 24 52 and 56, 48 64 and 62 (bf16 rows: 61 and 82, 83 and 91, 111 and 110).  Over few experts
+// it is not as good a rule: 40 and 41 dense rows by 4096 x 4096 take 32 and 23 us with bf16
+// rows, 10 and 13 with MXFP4 ones.
 constexpr int64_t kShortRuns = 40;
 
 constexpr Form rows4_form(const Sizes& a) {
